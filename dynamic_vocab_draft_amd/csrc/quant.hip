@@ -1,0 +1,362 @@
+// 8-bit rows: quantisation, the integer product, and the restricted LM head
+// over 8-bit rows.
+//
+// A row x of d elements becomes d 8-bit integers and one float32 scale,
+//     a = max |x_i|,  s = a / 127,  q_i = round(127 x_i / a)  (halves to even),
+// and the product of a token row and a channel row is
+//     out[m, n] = (sum_i xq[m, i] wq[n, i]) * (xs[m] * ws[n]).
+// The integer sum is exact: |q| <= 128 and d <= 16384 keep it within 2^28,
+// inside the int32 accumulators of v_mfma_i32_16x16x64_i8.  It is rounded
+// once to float32, multiplied by the float32 product of the two scales, and
+// rounded once to the output type, so results do not depend on how the sum
+// was split, and two runs agree bit for bit.
+#include "common.hpp"
+#include "select.hpp"
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPitch = 128;            // 8-bit rows start every multiple of 128 bytes
+__host__ __device__ constexpr int pitch_of(int d) { return (d + kPitch - 1) / kPitch * kPitch; }
+
+// ---------------------------------------------------------------------------
+// Row quantisation
+// ---------------------------------------------------------------------------
+template <int ET>
+__device__ __forceinline__ float load_elem(const void* x, size_t i) {
+  if (ET == NS_FP32) return ((const float*)x)[i];
+  const uint32_t w = ((const uint16_t*)x)[i];
+  return ET == NS_BF16 ? ns::bf16_lo(w) : ns::fp16_lo(w);
+}
+
+// round(127 |x| / a), halves to even, exactly.  t = |x| * (127 / a) carries
+// at most two roundings, 127 * 2^-23 in all; only where that could reach a
+// half is the side decided, by comparing 254 |x| with (2 f + 1) a, both exact
+// in float64 (24 + 8 bits).
+__device__ __forceinline__ float quant_abs(float x, float inv, float a) {
+  const float t = x * inv;
+  const float f = floorf(t), r = t - f;
+  float q = r > 0.5f ? f + 1.f : f;
+  if (fabsf(r - 0.5f) < 4e-5f) {
+    const double l = 254.0 * (double)x, h = (2.0 * (double)f + 1.0) * (double)a;
+    q = l > h ? f + 1.f : (l < h ? f : f + (float)((int)f & 1));
+  }
+  return q;
+}
+
+__device__ __forceinline__ int quant_one(float x, float inv, float a) {
+  const int q = (int)quant_abs(fabsf(x), inv, a);
+  return x < 0.f ? -q : q;
+}
+
+template <int ET>
+__global__ __launch_bounds__(256) void k_quant_rows(const void* __restrict__ x, int64_t ld, int d,
+                                                    int8_t* __restrict__ q, float* __restrict__ scale) {
+  __shared__ float sh[4];
+  const size_t r = blockIdx.x;
+  const int tid = threadIdx.x, pitch = pitch_of(d);
+  const size_t base = r * (size_t)ld;
+  // The bit patterns of |x| order like the values, NaN above infinity.
+  uint32_t top = 0;
+  for (int i = tid; i < d; i += 256) {
+    const uint32_t u = __float_as_uint(load_elem<ET>(x, base + i)) & 0x7FFFFFFFu;
+    top = u > top ? u : top;
+  }
+  for (int m = 32; m >= 1; m >>= 1) {
+    const uint32_t o = __shfl_xor(top, m, NS_WAVE);
+    top = o > top ? o : top;
+  }
+  if ((tid & 63) == 0) sh[tid / 64] = __uint_as_float(top);
+  __syncthreads();
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t o = __float_as_uint(sh[i]);
+    top = o > top ? o : top;
+  }
+  const bool bad = top >= 0x7F800000u, none = top == 0;
+  const float a = __uint_as_float(top);
+  // A maximum below 2^-100 is raised by 2^64 (exactly) so that 127 / a stays finite.
+  const float up = a < 0x1p-100f ? 0x1p64f : 1.f;
+  const float inv = 127.f / (a * up);
+  int8_t* row = q + r * (size_t)pitch;
+  for (int i = tid; i < pitch; i += 256) {
+    int v = 0;
+    if (i < d && !bad && !none) v = quant_one(load_elem<ET>(x, base + i) * up, inv, a * up);
+    row[i] = (int8_t)v;
+  }
+  if (tid == 0) scale[r] = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
+}
+
+int quant_rows(const void* x, int64_t ld, int R, int d, int dtype, int8_t* q, float* scale, hipStream_t stream) {
+  const dim3 grid((unsigned)R), block(256);
+  if (dtype == NS_BF16) hipLaunchKernelGGL(k_quant_rows<NS_BF16>, grid, block, 0, stream, x, ld, d, q, scale);
+  else if (dtype == NS_FP16) hipLaunchKernelGGL(k_quant_rows<NS_FP16>, grid, block, 0, stream, x, ld, d, q, scale);
+  else hipLaunchKernelGGL(k_quant_rows<NS_FP32>, grid, block, 0, stream, x, ld, d, q, scale);
+  return ns_launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Integer product
+// ---------------------------------------------------------------------------
+// Scaled value of an exact integer sum.
+__device__ __forceinline__ float scaled(int acc, float s) { return (float)acc * s; }
+
+// A float32 value as it is: without this the compiler forms mixed-precision
+// multiplies that round a product to fp16 at once.
+__device__ __forceinline__ float as_float32(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+template <int OT>
+__device__ __forceinline__ void store_out(void* out, size_t i, float v) {
+  if (OT == NS_FP32) ((float*)out)[i] = v;
+  else if (OT == NS_BF16) ((__bf16*)out)[i] = (__bf16)v;
+  else ((_Float16*)out)[i] = (_Float16)as_float32(v);
+}
+
+struct Product {
+  const int8_t* x;          // [B][M][pitch]
+  const float* xs;          // [B][M]
+  const int8_t* w;          // [rows][pitch]
+  const float* ws;          // [rows]
+  const int32_t* ids;       // [B][N] row of column j, or NULL: j
+  const int32_t* n_dev;     // [B] live columns, or NULL: N
+  int M, N, V, pitch;
+  void* out;                // [B][M] rows, ld_out elements apart
+  int64_t ld_out;
+};
+
+// A wave owns 16 channel rows (the A operand: lane (i, g) holds bytes
+// 16 g .. 16 g + 15 of row i) and 64 token rows (four B operands); lane
+// (i, g) of a result holds channels 4 g .. 4 g + 3 of token i.
+template <int OT>
+__global__ __launch_bounds__(256) void k_product(Product p) {
+  const int b = blockIdx.z, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  int n = p.n_dev ? p.n_dev[b] : p.N;
+  n = n < 0 ? 0 : (n > p.N ? p.N : n);
+  const int j0 = (int)blockIdx.x * 64 + (int)(threadIdx.x >> 6) * 16;
+  if (j0 >= n) return;
+  const int32_t* ids = p.ids ? p.ids + (size_t)b * p.N : nullptr;
+  const int j = j0 + i < n ? j0 + i : j0;
+  int gid = ids ? ids[j] : j;
+  gid = gid < 0 || gid >= p.V ? 0 : gid;
+  const int8_t* wr = p.w + (size_t)gid * p.pitch + g * 16;
+  const int m0 = (int)blockIdx.y * 64;
+  const int8_t* xr[4];
+  for (int t = 0; t < 4; ++t) {
+    int m = m0 + t * 16 + i;
+    m = m < p.M ? m : p.M - 1;
+    xr[t] = p.x + ((size_t)b * p.M + m) * p.pitch + g * 16;
+  }
+  i32x4 acc[4] = {};
+  for (int k = 0; k < p.pitch; k += 64) {
+    const i32x4 a = *(const i32x4*)(wr + k);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, *(const i32x4*)(xr[t] + k), acc[t], 0, 0, 0);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int m = m0 + t * 16 + i;
+    if (m >= p.M) continue;
+    const float xs = p.xs[(size_t)b * p.M + m];
+    for (int c = 0; c < 4; ++c) {
+      const int jj = j0 + g * 4 + c;
+      if (jj >= n) continue;
+      const int id = ids ? ids[jj] : jj;
+      if (id < 0 || id >= p.V) continue;
+      store_out<OT>(p.out, ((size_t)b * p.M + m) * (size_t)p.ld_out + jj, scaled(acc[t][c], xs * p.ws[id]));
+    }
+  }
+}
+
+template <int OT>
+void launch_product(const Product& p, int B, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 63) / 64), (unsigned)B);
+  hipLaunchKernelGGL(k_product<OT>, grid, dim3(256), 0, stream, p);
+}
+
+// ---------------------------------------------------------------------------
+// Top-k over the scaled logits of each hidden row
+// ---------------------------------------------------------------------------
+constexpr int kTopCols = 4;
+constexpr int kTopChunk = kSelectThreads * kTopCols;
+
+struct Top {
+  const float* z;           // [B][M] rows, ld floats apart
+  int64_t ld;
+  const int32_t* ids;
+  const int32_t* n_dev;
+  int n_max, V, M, k;
+  float* logits;            // [B][M][n_max] or NULL
+  int32_t* out_ids;
+  float* out_vals;
+  uint64_t* cand;           // [B][M][chunks][k]
+};
+
+__device__ __forceinline__ void put_top(const Top& t, size_t row, int r, uint64_t key) {
+  t.out_ids[row * t.k + r] = key ? ns::key_id(key) : -1;
+  t.out_vals[row * t.k + r] = key ? ns::key_val(key) : -INFINITY;
+}
+
+// Block (m, c, b): the k best of chunk c of hidden row m of sequence b.
+__global__ __launch_bounds__(kSelectThreads) void k_top_chunk(Top t) {
+  __shared__ SelectSmem sm;
+  const int m = blockIdx.x, c = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  int n = t.n_dev ? t.n_dev[b] : t.n_max;
+  n = n < 0 ? 0 : (n > t.n_max ? t.n_max : n);
+  const bool final_here = n <= kTopChunk;
+  if (final_here && c > 0) return;
+  const size_t row = (size_t)b * t.M + m;
+  const int j0 = c * kTopChunk;
+  float val[kTopCols];
+  int id[kTopCols];
+#pragma unroll
+  for (int u = 0; u < kTopCols; ++u) {
+    const int j = j0 + tid + u * kSelectThreads;
+    val[u] = 0.f;
+    id[u] = -1;
+    if (j < n) {
+      const int g = t.ids ? t.ids[(size_t)b * t.n_max + j] : j;
+      if (g >= 0 && g < t.V) {
+        const float v = t.z[row * (size_t)t.ld + j];
+        if (t.logits) t.logits[row * (size_t)t.n_max + j] = v;
+        if (v == v) {
+          val[u] = v;
+          id[u] = g;
+        }
+      }
+    }
+  }
+  const int nlive = n > j0 ? (n - j0 < kTopChunk ? n - j0 : kTopChunk) : 0;
+  if (final_here)
+    block_select_topk<kTopCols>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { put_top(t, row, r, x); });
+  else {
+    uint64_t* dst = t.cand + (row * gridDim.y + c) * (size_t)t.k;
+    block_select_topk<kTopCols>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { dst[r] = x; });
+  }
+}
+
+// Block (m, b): the k best of the nk = chunks * k keys of its chunks.
+template <int U>
+__global__ __launch_bounds__(kSelectThreads) void k_top_keys(Top t, int nk) {
+  __shared__ SelectSmem sm;
+  const int m = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  int n = t.n_dev ? t.n_dev[b] : t.n_max;
+  if (n > t.n_max) n = t.n_max;
+  if (n <= kTopChunk) return;
+  const size_t row = (size_t)b * t.M + m;
+  float val[U];
+  int id[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int q = tid + u * kSelectThreads;
+    const uint64_t key = q < nk ? t.cand[row * nk + q] : 0;
+    val[u] = key ? ns::key_val(key) : 0.f;
+    id[u] = key ? ns::key_id(key) : -1;
+  }
+  block_select_topk<U>(val, id, t.k, nk, sm, [&](int r, uint64_t x) { put_top(t, row, r, x); });
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Workspace of the restricted head: the quantised hidden rows and their
+// scales, the logits, and the chunks' keys.
+struct HeadWs {
+  size_t q, scale, z, cand, bytes;
+  int64_t ld;
+  int chunks;
+};
+
+HeadWs head_ws(int B, int n_max, int M, int k, int d) {
+  HeadWs w;
+  w.ld = ((int64_t)n_max + 3) / 4 * 4;
+  w.chunks = (n_max + kTopChunk - 1) / kTopChunk;
+  const size_t rows = (size_t)B * M;
+  w.q = 0;
+  w.scale = w.q + align256(rows * pitch_of(d));
+  w.z = w.scale + align256(rows * 4);
+  w.cand = w.z + align256(rows * (size_t)w.ld * 4);
+  w.bytes = w.cand + (w.chunks > 1 ? align256(rows * w.chunks * (size_t)k * 8) : 0);
+  return w;
+}
+
+bool known_dtype(int t) { return t == NS_BF16 || t == NS_FP32 || t == NS_FP16; }
+bool aligned16(const void* p) { return (((uintptr_t)p) & 15u) == 0; }
+
+bool head_dims_ok(int B, int n_max, int M, int k, int d) {
+  return B >= 1 && B <= NS_MAX_BATCH && n_max >= 1 && n_max <= NS_MAX_V && M >= 1 && M <= NS_MAX_M && k >= 1 &&
+         k <= NS_MAX_K && d >= 1 && d <= NS_MAX_D;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t nanospec_quant_pitch(int32_t d) { return d < 1 || d > NS_MAX_D ? 0 : pitch_of(d); }
+
+int nanospec_quant_rows(const void* x, int64_t ld, int32_t R, int32_t d, int32_t dtype, int8_t* q, float* scale,
+                        hipStream_t stream) {
+  if (!known_dtype(dtype)) return NS_EDTYPE;
+  if (R < 0 || R > NS_MAX_ROWS || d < 1 || d > NS_MAX_D || ld < d) return NS_EINVAL;
+  if (R == 0) return NS_OK;
+  if (!x || !q || !scale || !aligned16(q)) return NS_EINVAL;
+  if (((uintptr_t)x) % (dtype == NS_FP32 ? 4 : 2)) return NS_EINVAL;
+  (void)hipGetLastError();
+  return quant_rows(x, ld, R, d, dtype, q, scale, stream);
+}
+
+int nanospec_quant_matmul(const int8_t* xq, const float* xs, int32_t M, const int8_t* wq, const float* ws, int32_t N,
+                          int32_t d, void* out, int64_t ld_out, int32_t out_dtype, hipStream_t stream) {
+  if (!known_dtype(out_dtype)) return NS_EDTYPE;
+  if (M < 0 || M > NS_MAX_ROWS || N < 1 || N > NS_MAX_V || d < 1 || d > NS_MAX_D || ld_out < N) return NS_EINVAL;
+  if (M == 0) return NS_OK;
+  if (!xq || !xs || !wq || !ws || !out || !aligned16(xq) || !aligned16(wq)) return NS_EINVAL;
+  if (((uintptr_t)out) % (out_dtype == NS_FP32 ? 4 : 2)) return NS_EINVAL;
+  (void)hipGetLastError();
+  const Product p{xq, xs, wq, ws, nullptr, nullptr, M, N, N, pitch_of(d), out, ld_out};
+  if (out_dtype == NS_FP32) launch_product<NS_FP32>(p, 1, stream);
+  else if (out_dtype == NS_BF16) launch_product<NS_BF16>(p, 1, stream);
+  else launch_product<NS_FP16>(p, 1, stream);
+  return ns_launch_status();
+}
+
+size_t nanospec_quant_logits_workspace_bytes(int32_t B, int32_t n_max, int32_t M, int32_t k, int32_t d) {
+  return head_dims_ok(B, n_max, M, k, d) ? head_ws(B, n_max, M, k, d).bytes : 0;
+}
+
+int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int32_t* row_ids, const int32_t* n_dev,
+                               int32_t n_max, int32_t B, int32_t V, int32_t d, const void* h, int32_t dtype, int32_t M,
+                               int32_t k, float* logits, int32_t* topk_ids, float* topk_vals, void* ws,
+                               size_t ws_bytes, hipStream_t stream) {
+  if (!known_dtype(dtype)) return NS_EDTYPE;
+  if (!head_dims_ok(B, n_max, M, k, d) || V < 1 || V > NS_MAX_V || (!row_ids && n_max > V)) return NS_EINVAL;
+  if (!wq || !wscale || !h || !topk_ids || !topk_vals || !ws) return NS_EINVAL;
+  if (!aligned16(wq) || (((uintptr_t)ws) & 255u) || ((uintptr_t)h) % (dtype == NS_FP32 ? 4 : 2)) return NS_EINVAL;
+  const HeadWs l = head_ws(B, n_max, M, k, d);
+  if (ws_bytes < l.bytes) return NS_ECAPACITY;
+  (void)hipGetLastError();
+  char* base = (char*)ws;
+  int8_t* hq = (int8_t*)(base + l.q);
+  float* hs = (float*)(base + l.scale);
+  float* z = (float*)(base + l.z);
+  int rc = quant_rows(h, d, B * M, d, dtype, hq, hs, stream);
+  if (rc != NS_OK) return rc;
+  launch_product<NS_FP32>(Product{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld}, B, stream);
+  rc = ns_launch_status();
+  if (rc != NS_OK) return rc;
+  const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};
+  hipLaunchKernelGGL(k_top_chunk, dim3((unsigned)M, (unsigned)l.chunks, (unsigned)B), dim3(kSelectThreads), 0, stream,
+                     t);
+  rc = ns_launch_status();
+  if (rc != NS_OK || l.chunks == 1) return rc;
+  const int nk = l.chunks * k;
+  const dim3 grid((unsigned)M, (unsigned)B), block(kSelectThreads);
+  if (nk <= kSelectThreads) hipLaunchKernelGGL(k_top_keys<1>, grid, block, 0, stream, t, nk);
+  else if (nk <= 4 * kSelectThreads) hipLaunchKernelGGL(k_top_keys<4>, grid, block, 0, stream, t, nk);
+  else hipLaunchKernelGGL(k_top_keys<16>, grid, block, 0, stream, t, nk);
+  return ns_launch_status();
+}
+
+}  // extern "C"

@@ -33,6 +33,8 @@ NS_MAX_D = 16384
 NS_MAX_BATCH = 4096
 NS_MAX_SLOTS = 16384
 NS_MAX_TREE_CAND = 4096
+NS_MAX_ROWS = 1 << 20
+NS_MIN_INV_TEMP, NS_MAX_INV_TEMP = 2.0 ** -20, 2.0 ** 20
 
 
 class NanoSpecError(RuntimeError):
@@ -64,6 +66,7 @@ def _check_single_runtime() -> None:
 
 _lib = _load()
 
+c_int64, c_float = ctypes.c_int64, ctypes.c_float
 c_int32, c_size, c_vp, c_u32p = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)
 
 _SIGS = {
@@ -124,6 +127,18 @@ _SIGS = {
     "nanospec_batch_decode_step": (ctypes.c_int, [c_vp, c_vp, c_int32, c_vp, c_int32, c_vp, c_int32, c_vp, c_int32,
                                                   c_vp, c_vp, c_vp, c_int32, c_int32, c_int32, c_vp, c_int32, c_int32,
                                                   c_vp, c_vp, c_vp, c_size, c_vp]),
+    "nanospec_quant_pitch": (c_int32, [c_int32]),
+    "nanospec_quant_rows": (ctypes.c_int, [c_vp, c_int64, c_int32, c_int32, c_int32, c_vp, c_vp, c_vp]),
+    "nanospec_quant_matmul": (ctypes.c_int, [c_vp, c_vp, c_int32, c_vp, c_vp, c_int32, c_int32, c_vp, c_int64, c_int32,
+                                             c_vp]),
+    "nanospec_quant_logits_workspace_bytes": (c_size, [c_int32] * 5),
+    "nanospec_quant_logits_topk": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_int32, c_int32, c_int32, c_int32, c_vp,
+                                                  c_int32, c_int32, c_int32, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "nanospec_token_logprobs_workspace_bytes": (c_size, [c_int32] * 3),
+    "nanospec_token_logprobs": (ctypes.c_int, [c_vp, c_int64, c_int32, c_int32, c_int32, c_float, c_vp, c_int32,
+                                               c_int32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "nanospec_token_logprobs_grad": (ctypes.c_int, [c_vp, c_int64, c_int32, c_int32, c_int32, c_float, c_vp, c_int32,
+                                                    c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int64, c_vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -544,3 +559,201 @@ def alloc_workspace(n_max: int, M: int, k: int, d: int, device="cuda") -> torch.
     mem = torch.zeros(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-mem.data_ptr()) % 256
     return mem[off:off + nbytes]
+
+
+# ---------------------------------------------------------------------------
+# 8-bit rows and token log-probabilities.  Sizes come from the tensors, so the
+# tensors are checked here: device, type, shape and strides.
+# ---------------------------------------------------------------------------
+
+
+def _want(ok: bool, where: str, what: str, code: int = NS_EINVAL) -> None:
+    if not ok:
+        raise NanoSpecError(code, f"{where}: {what}")
+
+
+def _tensor(t, where: str, name: str, dtypes, shape, device=None) -> torch.Tensor:
+    """Checks a contiguous device tensor of one of `dtypes` and of `shape`."""
+    _want(isinstance(t, torch.Tensor) and t.device.type == "cuda", where, f"{name} is no device tensor")
+    _want(device is None or t.device == device, where, f"{name} is on {t.device}, not {device}")
+    _want(t.dtype in dtypes, where, f"{name} has dtype {t.dtype}", NS_EDTYPE)
+    _want(tuple(t.shape) == tuple(shape), where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    _want(t.is_contiguous(), where, f"{name} is not contiguous")
+    return t
+
+
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _matrix(t, where: str, name: str, dtypes=_FLOATS, device=None):
+    """Checks a device matrix whose rows are contiguous; returns its row stride in elements."""
+    _want(isinstance(t, torch.Tensor) and t.device.type == "cuda", where, f"{name} is no device tensor")
+    _want(device is None or t.device == device, where, f"{name} is on {t.device}, not {device}")
+    _want(t.dtype in dtypes, where, f"{name} has dtype {t.dtype}", NS_EDTYPE)
+    _want(t.dim() == 2 and t.shape[1] >= 1, where, f"{name} has shape {tuple(t.shape)}")
+    _want(t.shape[1] == 1 or t.stride(1) == 1, where, f"the rows of {name} are not contiguous")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    _want(ld >= t.shape[1], where, f"the rows of {name} overlap")
+    return ld
+
+
+def _on(device, stream, where: str):
+    """The launch stream, on the tensors' own device."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    _want(s.device == device, where, f"the stream is on {s.device}, not {device}")
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def nanospec_quant_pitch(d: int) -> int:
+    return _lib.nanospec_quant_pitch(d)
+
+
+def nanospec_quant_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
+    """x [R, d] (rows contiguous, any row stride) -> q [R, pitch] int8, scale [R] float32."""
+    where = "nanospec_quant_rows"
+    ld = _matrix(x, where, "x")
+    R, d = x.shape
+    _tensor(q, where, "q", (torch.int8,), (R, nanospec_quant_pitch(d)), x.device)
+    _tensor(scale, where, "scale", (torch.float32,), (R,), x.device)
+    with torch.cuda.device(x.device):
+        _check(_lib.nanospec_quant_rows(_ptr(x), ld, R, d, dtype_code(x), _ptr(q), _ptr(scale),
+                                        _on(x.device, stream, where)), where)
+
+
+def nanospec_quant_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, d: int,
+                          out: torch.Tensor, stream=None) -> None:
+    """xq [M, pitch], wq [N, pitch] int8 with scales xs [M], ws [N] -> out [M, N] (rows contiguous, any row stride)."""
+    where = "nanospec_quant_matmul"
+    ld = _matrix(out, where, "out")
+    M, N = out.shape
+    pitch = nanospec_quant_pitch(d)
+    _tensor(xq, where, "xq", (torch.int8,), (M, pitch), out.device)
+    _tensor(wq, where, "wq", (torch.int8,), (N, pitch), out.device)
+    _tensor(xs, where, "xs", (torch.float32,), (M,), out.device)
+    _tensor(ws, where, "ws", (torch.float32,), (N,), out.device)
+    with torch.cuda.device(out.device):
+        _check(_lib.nanospec_quant_matmul(_ptr(xq), _ptr(xs), M, _ptr(wq), _ptr(ws), N, d, _ptr(out), ld,
+                                          dtype_code(out), _on(out.device, stream, where)), where)
+
+
+def nanospec_quant_logits_workspace_bytes(B: int, n_max: int, M: int, k: int, d: int) -> int:
+    return _lib.nanospec_quant_logits_workspace_bytes(B, n_max, M, k, d)
+
+
+def nanospec_quant_logits_topk(wq: torch.Tensor, wscale: torch.Tensor, row_ids: Optional[torch.Tensor],
+                               n_dev: Optional[torch.Tensor], h: torch.Tensor, k: int, logits: Optional[torch.Tensor],
+                               topk_ids: torch.Tensor, topk_vals: torch.Tensor, work: torch.Tensor,
+                               stream=None) -> None:
+    """The head over 8-bit rows: wq [V, pitch], h [B, M, d], row_ids [B, n_max] (None: all V rows), n_dev [B] or None."""
+    where = "nanospec_quant_logits_topk"
+    _want(isinstance(h, torch.Tensor) and h.dim() == 3, where, "h is no [B, M, d] tensor")
+    B, M, d = h.shape
+    _tensor(h, where, "h", _FLOATS, (B, M, d), None)
+    dev = h.device
+    _want(isinstance(wq, torch.Tensor) and wq.dim() == 2, where, "wq is no [V, pitch] tensor")
+    V = wq.shape[0]
+    _tensor(wq, where, "wq", (torch.int8,), (V, nanospec_quant_pitch(d)), dev)
+    _tensor(wscale, where, "wscale", (torch.float32,), (V,), dev)
+    n_max = V
+    if row_ids is not None:
+        _want(row_ids.dim() == 2, where, "row_ids is no [B, n_max] tensor")
+        n_max = row_ids.shape[1]
+        _tensor(row_ids, where, "row_ids", (torch.int32,), (B, n_max), dev)
+    if n_dev is not None:
+        _tensor(n_dev, where, "n_dev", (torch.int32,), (B,), dev)
+    if logits is not None:
+        _tensor(logits, where, "logits", (torch.float32,), (B, M, n_max), dev)
+    _tensor(topk_ids, where, "topk_ids", (torch.int32,), (B, M, k), dev)
+    _tensor(topk_vals, where, "topk_vals", (torch.float32,), (B, M, k), dev)
+    _tensor(work, where, "work", (torch.uint8,), (work.numel(),), dev)
+    with torch.cuda.device(dev):
+        _check(_lib.nanospec_quant_logits_topk(_ptr(wq), _ptr(wscale), _ptr(row_ids), _ptr(n_dev), n_max, B, V, d,
+                                               _ptr(h), dtype_code(h), M, k, _ptr(logits), _ptr(topk_ids),
+                                               _ptr(topk_vals), _ptr(work), work.numel(), _on(dev, stream, where)),
+               where)
+
+
+def nanospec_token_logprobs_workspace_bytes(L: int, V: int, k: int) -> int:
+    return _lib.nanospec_token_logprobs_workspace_bytes(L, V, k)
+
+
+def nanospec_token_logprobs(logits: torch.Tensor, inv_temp: float, tokens: Optional[torch.Tensor],
+                            logprob: Optional[torch.Tensor], lse: torch.Tensor, entropy: Optional[torch.Tensor],
+                            top_ids: Optional[torch.Tensor], top_logprobs: Optional[torch.Tensor], work: torch.Tensor,
+                            stream=None) -> None:
+    """logits [L, V] (rows contiguous, any row stride), tokens and logprob [L, T] or None, lse [L], entropy [L] or None,
+    top_ids and top_logprobs [L, k] or None."""
+    where = "nanospec_token_logprobs"
+    ld = _matrix(logits, where, "logits")
+    L, V = logits.shape
+    dev = logits.device
+    T, k = 0, 0
+    _want((tokens is None) == (logprob is None), where, "tokens and logprob go together")
+    _want((top_ids is None) == (top_logprobs is None), where, "top_ids and top_logprobs go together")
+    if tokens is not None:
+        _want(tokens.dim() == 2, where, "tokens is no [L, T] tensor")
+        T = tokens.shape[1]
+        _tensor(tokens, where, "tokens", (torch.int32,), (L, T), dev)
+        _tensor(logprob, where, "logprob", (torch.float32,), (L, T), dev)
+    if top_ids is not None:
+        _want(top_ids.dim() == 2, where, "top_ids is no [L, k] tensor")
+        k = top_ids.shape[1]
+        _tensor(top_ids, where, "top_ids", (torch.int32,), (L, k), dev)
+        _tensor(top_logprobs, where, "top_logprobs", (torch.float32,), (L, k), dev)
+    _tensor(lse, where, "lse", (torch.float32,), (L,), dev)
+    if entropy is not None:
+        _tensor(entropy, where, "entropy", (torch.float32,), (L,), dev)
+    _tensor(work, where, "work", (torch.uint8,), (work.numel(),), dev)
+    with torch.cuda.device(dev):
+        _check(_lib.nanospec_token_logprobs(_ptr(logits), ld, L, V, dtype_code(logits), inv_temp, _ptr(tokens), T, k,
+                                            _ptr(logprob), _ptr(lse), _ptr(entropy), _ptr(top_ids),
+                                            _ptr(top_logprobs), _ptr(work), work.numel(), _on(dev, stream, where)),
+               where)
+
+
+def nanospec_token_logprobs_grad(logits: torch.Tensor, inv_temp: float, tokens: Optional[torch.Tensor],
+                                 lse: torch.Tensor, entropy: Optional[torch.Tensor],
+                                 g_logprob: Optional[torch.Tensor], g_entropy: Optional[torch.Tensor],
+                                 g_lse: Optional[torch.Tensor], dlogits: torch.Tensor, stream=None) -> None:
+    """dlogits [L, V] of the logits' dtype from the gradients of nanospec_token_logprobs's outputs (None: zeros); dlogits
+    may be logits."""
+    where = "nanospec_token_logprobs_grad"
+    ld = _matrix(logits, where, "logits")
+    L, V = logits.shape
+    dev = logits.device
+    ld_d = _matrix(dlogits, where, "dlogits", (logits.dtype,), dev)
+    _want(tuple(dlogits.shape) == (L, V), where, f"dlogits has shape {tuple(dlogits.shape)}, not {(L, V)}")
+    T = 0
+    _want((tokens is None) == (g_logprob is None), where, "tokens and g_logprob go together")
+    if tokens is not None:
+        _want(tokens.dim() == 2, where, "tokens is no [L, T] tensor")
+        T = tokens.shape[1]
+        _tensor(tokens, where, "tokens", (torch.int32,), (L, T), dev)
+        _tensor(g_logprob, where, "g_logprob", (torch.float32,), (L, T), dev)
+    _tensor(lse, where, "lse", (torch.float32,), (L,), dev)
+    for t, name in ((entropy, "entropy"), (g_entropy, "g_entropy"), (g_lse, "g_lse")):
+        if t is not None:
+            _tensor(t, where, name, (torch.float32,), (L,), dev)
+    with torch.cuda.device(dev):
+        _check(_lib.nanospec_token_logprobs_grad(_ptr(logits), ld, L, V, dtype_code(logits), inv_temp, _ptr(tokens), T,
+                                                 _ptr(lse), _ptr(entropy), _ptr(g_logprob), _ptr(g_entropy),
+                                                 _ptr(g_lse), _ptr(dlogits), ld_d, _on(dev, stream, where)), where)
+
+
+def _alloc(nbytes: int, where: str, device) -> torch.Tensor:
+    if nbytes == 0:
+        raise NanoSpecError(NS_EINVAL, where)
+    mem = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-mem.data_ptr()) % 256
+    return mem[off:off + nbytes]
+
+
+def alloc_quant_logits_workspace(B: int, n_max: int, M: int, k: int, d: int, device="cuda") -> torch.Tensor:
+    """A 256-byte-aligned uint8 workspace of nanospec_quant_logits_workspace_bytes."""
+    return _alloc(nanospec_quant_logits_workspace_bytes(B, n_max, M, k, d), "nanospec_quant_logits_workspace_bytes",
+                  device)
+
+
+def alloc_token_logprobs_workspace(L: int, V: int, k: int, device="cuda") -> torch.Tensor:
+    """A 256-byte-aligned uint8 workspace of nanospec_token_logprobs_workspace_bytes."""
+    return _alloc(nanospec_token_logprobs_workspace_bytes(L, V, k), "nanospec_token_logprobs_workspace_bytes", device)

@@ -82,6 +82,9 @@ extern "C" {
 #define NS_MAX_BATCH  4096      /* sequences in one batch */
 #define NS_MAX_SLOTS  16384     /* slots of a slot-stable packed buffer */
 #define NS_MAX_TREE_CAND 4096   /* candidates of one nanospec_tree_select */
+#define NS_MAX_ROWS   1048576   /* rows of one quant_rows, quant_matmul or token_logprobs call */
+#define NS_MIN_INV_TEMP 9.5367431640625e-07f  /* inverse temperatures: 2^-20 .. */
+#define NS_MAX_INV_TEMP 1048576.0f            /* .. 2^20 */
 
 typedef struct nanospec_state nanospec_state;   /* opaque host handle */
 typedef struct nanospec_batch nanospec_batch;   /* opaque host handle of B states */
@@ -539,6 +542,127 @@ int nanospec_tree_select(const float* vals, const int32_t* ids, int32_t C, int32
 int nanospec_prefill_topk(const void* logits, int32_t L, int32_t V, int32_t dtype,
                           int32_t k, int32_t* out_ids, float* out_vals,
                           hipStream_t stream);
+
+/* ======================================================================
+ * 8-bit rows.  The LM head is bound by the bytes of W_head; rows of 8-bit
+ * integers with one float32 scale a row halve those of bf16.
+ * A row x of d elements becomes
+ *     a = max |x_i|,  scale = a / 127,  q_i = round(127 x_i / a)
+ * (halves to even, decided exactly; scale rounded to float32).  A row of
+ * zeros has scale 0 and zeros; a row holding a NaN or an infinity has scale
+ * NaN and zeros, so that it cannot pass unseen.
+ * Row r starts at q + r * nanospec_quant_pitch(d): d rounded up to 128.  The
+ * bytes behind the d-th are zero, which the products below rely on (callers
+ * who lay out rows of their own clear them).
+ *   nanospec_quant_pitch : bytes of one row; 0 if d is outside [1, NS_MAX_D].
+ *   nanospec_quant_rows  : quantises R rows.
+ *     x     : rows of d elements of `dtype`, ld >= d elements apart, at any
+ *             address their element type may have.
+ *     q     : [R x pitch] int8, 16-byte aligned.   scale : [R] float32.
+ *   W_head is quantised once, hidden rows before each product.
+ * R = 0 enqueues nothing.  R <= NS_MAX_ROWS.
+ * Errors: NS_EINVAL (nulls, limits, misalignment), NS_EDTYPE, NS_EHIP. */
+int32_t nanospec_quant_pitch(int32_t d);
+int nanospec_quant_rows(const void* x, int64_t ld, int32_t R, int32_t d, int32_t dtype, int8_t* q,
+                        float* scale, hipStream_t stream);
+
+/* The product of M 8-bit token rows and N 8-bit channel rows:
+ *     out[m, n] = (sum_i xq[m, i] wq[n, i]) * (xs[m] * ws[n])
+ * for one token up to whole prompts (with wq = W_head the full-vocabulary
+ * logits that nanospec_prefill_topk and nanospec_token_logprobs read).  The
+ * sum is exact (int32), rounded once to float32, times the float32 product
+ * of the scales, rounded once to out_dtype; results do not depend on how the
+ * work was split.
+ *   xq, wq : rows as above (16-byte aligned); values -128 .. 127.
+ *   xs, ws : [M], [N] float32.
+ *   out    : [M] rows of N elements of out_dtype, ld_out >= N elements apart;
+ *            what lies between rows is untouched.
+ * M in [0, NS_MAX_ROWS] (0 enqueues nothing), N in [1, NS_MAX_V].
+ * Errors: NS_EINVAL (nulls, limits, misalignment), NS_EDTYPE, NS_EHIP. */
+int nanospec_quant_matmul(const int8_t* xq, const float* xs, int32_t M, const int8_t* wq,
+                          const float* ws, int32_t N, int32_t d, void* out, int64_t ld_out,
+                          int32_t out_dtype, hipStream_t stream);
+
+/* nanospec_draft_logits_topk and its batched form over 8-bit rows of W_head
+ * (NS_INDEXED): for each of B sequences the M hidden rows are quantised as by
+ * nanospec_quant_rows, multiplied as by nanospec_quant_matmul with the rows
+ * row_ids names, and the k largest logits of each are written with their ids.
+ *   wq, wscale : W_head's 8-bit rows [V x pitch] and scales [V].
+ *   row_ids    : [B x n_max] row ids; entries outside [0, V) are holes.  NULL:
+ *                row j has id j (the full-vocabulary head; n_max <= V).
+ *   n_dev      : [B] live counts on the device, each clamped to [0, n_max];
+ *                NULL: n_max.
+ *   h          : [B x M x d] hidden rows of `dtype`.
+ *   logits     : [B x M x n_max] float32 or NULL; columns at or past the live
+ *                count and holes are left untouched.
+ *   topk_ids, topk_vals : [B x M x k], ordered by (value desc, id asc), padded
+ *                with (-1, -INFINITY).  NaN logits are never selected.
+ *   ws         : >= nanospec_quant_logits_workspace_bytes(...) bytes, 256-byte
+ *                aligned, no initialisation needed.  Calls sharing a workspace
+ *                must be ordered (two captured graphs among them).
+ * row_ids must be distinct within a sequence apart from holes.
+ * B in [1, NS_MAX_BATCH], M in [1, 64], k in [1, 64], n_max in [1, NS_MAX_V],
+ * d in [1, NS_MAX_D].  The workspace query returns 0 outside them.
+ * Errors: NS_EINVAL, NS_EDTYPE, NS_ECAPACITY (ws too small), NS_EHIP. */
+size_t nanospec_quant_logits_workspace_bytes(int32_t B, int32_t n_max, int32_t M, int32_t k,
+                                             int32_t d);
+int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int32_t* row_ids,
+                               const int32_t* n_dev, int32_t n_max, int32_t B, int32_t V, int32_t d,
+                               const void* h, int32_t dtype, int32_t M, int32_t k, float* logits,
+                               int32_t* topk_ids, float* topk_vals, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
+/* ======================================================================
+ * Log-probabilities of given tokens under full-vocabulary logits, with
+ * entropy and top alternatives: the target's side of verification (the
+ * children of each tree node), prompt log-probabilities, and, with the
+ * gradient below, training.  For row i with z' = inv_temp * z:
+ *     lse = log sum_j exp(z'_j),  logp_j = z'_j - lse,
+ *     logprob[i, t] = logp of tokens[i, t],  entropy = -sum_j p_j logp_j.
+ *   logits  : L rows of V elements of `dtype`, ld >= V elements apart, at any
+ *             address their element type may have.
+ *   tokens  : [L x T] ids; one outside [0, V) (padding) has log-probability 0.
+ *             T in [0, 64]; tokens and logprob may be NULL when T = 0.
+ *   logprob : [L x T], lse : [L], entropy : [L] or NULL; float32.
+ *   top_ids, top_logprobs : [L x k], the k largest logits by (value desc, id
+ *             asc) with their log-probabilities; k in [0, min(64, V)]; NULL
+ *             allowed when k = 0.
+ *   ws      : >= nanospec_token_logprobs_workspace_bytes(L, V, k) bytes,
+ *             256-byte aligned, no initialisation needed.  Calls sharing a
+ *             workspace must be ordered (two captured graphs among them).
+ * A logit of -INFINITY (masked) has probability 0 and log-probability
+ * -INFINITY.  A row with nothing else has lse -INFINITY, entropy 0 and every
+ * log-probability -INFINITY.  A row with a NaN or +INFINITY has no
+ * distribution: lse, entropy and log-probabilities NaN (0 for padding
+ * tokens), top ids -1.  L = 0 enqueues nothing; L <= NS_MAX_ROWS.
+ * inv_temp in [NS_MIN_INV_TEMP, NS_MAX_INV_TEMP].  Statistics are float32;
+ * no atomics, so results repeat bit for bit.
+ * Errors: NS_EINVAL, NS_EDTYPE, NS_ECAPACITY (ws too small), NS_EHIP. */
+size_t nanospec_token_logprobs_workspace_bytes(int32_t L, int32_t V, int32_t k);
+int nanospec_token_logprobs(const void* logits, int64_t ld, int32_t L, int32_t V, int32_t dtype,
+                            float inv_temp, const int32_t* tokens, int32_t T, int32_t k,
+                            float* logprob, float* lse, float* entropy, int32_t* top_ids,
+                            float* top_logprobs, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of nanospec_token_logprobs with respect to the logits:
+ *     dlogits[i, j] = inv_temp * (p_j (g_lse - sum_t g_logprob[t]
+ *                     - g_entropy (logp_j + entropy))
+ *                     + sum_t g_logprob[t] [tokens[i, t] = j]),
+ * t over the tokens inside [0, V); a token named twice counts twice.  The top
+ * alternatives are not differentiated.
+ *   lse, entropy : what the forward call wrote (entropy may be NULL without
+ *                  g_entropy).
+ *   g_logprob    : [L x T];  g_entropy, g_lse : [L] or NULL (zeros).
+ *   dlogits      : L rows of `dtype`, ld_d >= V elements apart; either the
+ *                  logits themselves (ld_d = ld), which it then replaces, or
+ *                  memory apart from them.  What lies between rows is untouched.
+ * A row whose lse is -INFINITY, or so large (over 2^24) that float32 no longer
+ * resolves probabilities from it, has gradient 0; one whose lse is NaN, NaN.
+ * Errors: NS_EINVAL, NS_EDTYPE, NS_EHIP. */
+int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int32_t V, int32_t dtype,
+                                 float inv_temp, const int32_t* tokens, int32_t T, const float* lse,
+                                 const float* entropy, const float* g_logprob, const float* g_entropy,
+                                 const float* g_lse, void* dlogits, int64_t ld_d, hipStream_t stream);
 
 #ifdef __cplusplus
 }

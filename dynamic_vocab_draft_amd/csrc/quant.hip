@@ -171,8 +171,234 @@ __global__ __launch_bounds__(256) void k_product(Product p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The product for more than 64 token rows: compute-bound, tiles in LDS.
+//
+// A block of eight waves owns 256 channel rows and TB * 64 token rows; a wave
+// owns 128 channel rows (eight 16-row operands) and TB * 16 token rows (TB
+// operands), TB * 8 accumulator tiles in registers.  The sum runs in stages
+// of 64 bytes a row.  Four stages of both tiles lie in LDS (32 KB each with
+// TB = 4), filled by direct global-to-LDS loads, so a stage is asked for three
+// stages (about 3000 cycles) before it is read; a wave reads stage s + 1 into
+// registers between the matrix instructions of stage s.  One block barrier a
+// stage: it says that stage s + 1 has landed and that stage s has been read
+// by all, so its place takes stage s + 4.
+//
+// LDS rows are 64 bytes in four 16-byte places; place c of row r holds chunk
+// c ^ (r / 2 % 4), so that eight consecutive lanes of an operand read, one
+// row each, meet no bank twice.  Each load instruction fills 16 rows.
+//
+// Blocks take tiles so that the 32 CUs of an XCD work at one time on about
+// eight token tiles by four channel tiles, which share their rows in that
+// XCD's L2.
+// ---------------------------------------------------------------------------
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+constexpr int kTileN = 256;                        // channel rows of a block
+constexpr int kTileThreads = 512;
+constexpr int kStages = 4;
+constexpr int kStageK = 64;                        // bytes of a row in a stage
+
+// 16 bytes a lane from a buffer straight into LDS at byte `lds` (the same
+// for the wave) + 16 * lane.  The compiler does not count these loads: the
+// waits below do.  m0 holds the LDS address; nothing else in these kernels
+// uses it.
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
+               : "memory");
+}
+
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00027000u};
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+template <int OT>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  if (OT == NS_BF16) {
+    const __bf16 x = (__bf16)a, y = (__bf16)b;
+    return (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
+  }
+  const _Float16 x = (_Float16)as_float32(a), y = (_Float16)as_float32(b);
+  return (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
+}
+
+// Eight consecutive outputs, n of them inside the row.
+template <int OT>
+__device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v)[8], int n) {
+  if (n >= 8) {
+    if (OT == NS_FP32) {
+      u32x4_any* d = (u32x4_any*)((float*)out + i);
+      d[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      d[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else {
+      *(u32x4_any*)((uint16_t*)out + i) = u32x4{narrow2<OT>(v[0], v[1]), narrow2<OT>(v[2], v[3]),
+                                                narrow2<OT>(v[4], v[5]), narrow2<OT>(v[6], v[7])};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) store_out<OT>(out, i + e, v[e]);
+  }
+}
+
+template <int OT, int TB>
+__global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, int tiles_m, int tiles_n) {
+  constexpr int TM = TB * 64;                      // token rows of a block
+  constexpr int ROWS = kTileN + TM, STAGE = ROWS * kStageK;
+  constexpr int LA = kTileN / 16 / 8, LB = TM / 16 / 8, LW = LA + LB;   // loads of a wave and stage
+  __shared__ __attribute__((aligned(16))) char lds[kStages * STAGE];
+  // tile of this block: a contiguous run of the tile order for each XCD
+  const int total = tiles_m * tiles_n;
+  const int per = (total + 7) / 8;
+  const int t_id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || t_id >= total) return;
+  const int group = t_id / (tiles_m * 4), rest = t_id % (tiles_m * 4);
+  const int wide = tiles_n - group * 4 < 4 ? tiles_n - group * 4 : 4;   // channel tiles of this group
+  const int n0 = (group * 4 + rest % wide) * kTileN, m0 = rest / wide * TM;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int r16 = lane >> 2, chunk = ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
+  uint32_t ao[LA], bo[LB];                         // rows past the end read the last one and are not stored
+#pragma unroll
+  for (int u = 0; u < LA; ++u) {
+    const int r = (u * 8 + w) * 16 + r16;
+    ao[u] = (uint32_t)((n0 + r < p.N ? r : p.N - 1 - n0) * p.pitch + chunk);
+  }
+#pragma unroll
+  for (int u = 0; u < LB; ++u) {
+    const int r = (u * 8 + w) * 16 + r16;
+    bo[u] = (uint32_t)((m0 + r < p.M ? r : p.M - 1 - m0) * p.pitch + chunk);
+  }
+  const u32x4 ra = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(kTileN * p.pitch));
+  const u32x4 rb = buffer_of(p.x + (size_t)m0 * p.pitch, (uint32_t)(TM * p.pitch));
+  const uint32_t base = lds_offset(lds);
+  const auto issue = [&](int buf, int k) {
+#pragma unroll
+    for (int u = 0; u < LA; ++u) load_to_lds(ra, ao[u], k, base + buf * STAGE + (u * 8 + w) * 1024);
+#pragma unroll
+    for (int u = 0; u < LB; ++u) load_to_lds(rb, bo[u], k, base + buf * STAGE + kTileN * kStageK + (u * 8 + w) * 1024);
+  };
+  const int wr = w >> 2, wc = w & 3;
+  i32x4 acc[8][TB] = {};
+  i32x4 fa[2][8], fb[2][TB];
+  const int place = i * kStageK + (g ^ ((i >> 1) & 3)) * 16;
+  const char* la = lds + wr * 128 * kStageK + place;
+  const char* lb = lds + (kTileN + wc * TB * 16) * kStageK + place;
+  const int S = p.pitch / kStageK;                 // even
+  issue(0, 0);
+  issue(1, kStageK);
+  if (S > 2) {
+    issue(2, 2 * kStageK);
+    issue(3, 3 * kStageK);
+    wait_loads<3 * LW>();
+  } else {
+    wait_loads<LW>();
+  }
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < TB; ++u) fb[0][u] = *(const i32x4*)(lb + u * 1024);
+#pragma unroll
+  for (int t = 0; t < 8; ++t) fa[0][t] = *(const i32x4*)(la + t * 1024);
+  // Stage s is in registers f and in buffer buf; s + 1 goes from buffer next to registers 1 - f.
+  const auto step = [&](int f, int buf, int next, bool more, int k) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): this wave has read stage s
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) issue(buf, k);
+#pragma unroll
+    for (int u = 0; u < TB; ++u) fb[1 - f][u] = *(const i32x4*)(lb + next * STAGE + u * 1024);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      fa[1 - f][t] = *(const i32x4*)(la + next * STAGE + t * 1024);
+#pragma unroll
+      for (int u = 0; u < TB; ++u) acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[f][t], fb[f][u], acc[t][u], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int s = 0;
+  for (; s + 4 < S; s += 2) {
+    const int b = s & 3;
+    wait_loads<2 * LW>();
+    step(0, b, (b + 1) & 3, true, (s + 4) * kStageK);
+    wait_loads<2 * LW>();
+    step(1, b + 1, (b + 2) & 3, true, (s + 5) * kStageK);
+  }
+  for (; s < S; s += 2) {                          // nothing left to ask for; the last step reads a stage it does not use
+    const int b = s & 3;
+    wait_loads<0>();
+    step(0, b, (b + 1) & 3, false, 0);
+    step(1, b + 1, (b + 2) & 3, false, 0);
+  }
+  // Outputs go through LDS, 16 token rows of a wave at a time, so that a store covers whole lines of a row.
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  constexpr int OP = 132;                          // floats between two token rows there
+  float* lo = (float*)(lds + w * (16 * OP * 4));
+  static_assert(8 * 16 * OP * 4 <= kStages * STAGE, "the waves' output rows fit");
+  const int nw = n0 + wr * 128;
+  float ws[8][4];
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int n = nw + t * 16 + g * 4 + c;
+      ws[t][c] = p.ws[n < p.N ? n : p.N - 1];
+    }
+#pragma unroll
+  for (int u = 0; u < TB; ++u) {
+    const int mt = m0 + (wc * TB + u) * 16;
+    const float xs = p.xs[mt + i < p.M ? mt + i : p.M - 1];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      typedef float f32x4 __attribute__((ext_vector_type(4)));
+      f32x4 v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = scaled(acc[t][u][c], xs * ws[t][c]);
+      *(f32x4*)(lo + i * OP + t * 16 + g * 4) = v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = q * 4 + g, m = mt + r, n = nw + i * 8;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = lo[r * OP + i * 8 + e];
+      if (m < p.M && n < p.N) store_eight<OT>(p.out, (size_t)m * (size_t)p.ld_out + n, v, p.N - n);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int OT, int TB>
+void launch_tiled(const Product& p, hipStream_t stream) {
+  const int tm = (p.M + TB * 64 - 1) / (TB * 64), tn = (p.N + kTileN - 1) / kTileN;
+  const unsigned per = ((unsigned)tm * (unsigned)tn + 7) / 8;
+  hipLaunchKernelGGL((k_product_tiled<OT, TB>), dim3(per * 8), dim3(kTileThreads), 0, stream, p, tm, tn);
+}
+
 template <int OT>
 void launch_product(const Product& p, int B, hipStream_t stream) {
+  if (p.M > 64) {
+    if (p.M > 128) launch_tiled<OT, 4>(p, stream);
+    else launch_tiled<OT, 2>(p, stream);
+    return;
+  }
   const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 63) / 64), (unsigned)B);
   hipLaunchKernelGGL(k_product<OT>, grid, dim3(256), 0, stream, p);
 }

@@ -563,8 +563,14 @@ def alloc_workspace(n_max: int, M: int, k: int, d: int, device="cuda") -> torch.
 
 # ---------------------------------------------------------------------------
 # 8-bit rows and token log-probabilities.  Sizes come from the tensors, so the
-# tensors are checked here: device, type, shape and strides.
+# tensors are checked here: device, type, shape and strides.  A small call
+# takes a few microseconds on the GPU, so each check is one expression and the
+# reason is looked for only where it fails.
 # ---------------------------------------------------------------------------
+
+_FLOATS = {torch.bfloat16: NS_BF16, torch.float16: NS_FP16, torch.float32: NS_FP32}
+_INT8, _INT32, _UINT8, _F32 = torch.int8, torch.int32, torch.uint8, torch.float32
+_current_device = torch._C._cuda_getDevice
 
 
 def _want(ok: bool, where: str, what: str, code: int = NS_EINVAL) -> None:
@@ -572,36 +578,50 @@ def _want(ok: bool, where: str, what: str, code: int = NS_EINVAL) -> None:
         raise NanoSpecError(code, f"{where}: {what}")
 
 
-def _tensor(t, where: str, name: str, dtypes, shape, device=None) -> torch.Tensor:
-    """Checks a contiguous device tensor of one of `dtypes` and of `shape`."""
-    _want(isinstance(t, torch.Tensor) and t.device.type == "cuda", where, f"{name} is no device tensor")
-    _want(device is None or t.device == device, where, f"{name} is on {t.device}, not {device}")
+def _misfit(t, where: str, name: str, dtypes, shape, dev: int) -> None:
+    """Raises what is wrong with a tensor that failed a check."""
+    _want(isinstance(t, torch.Tensor), where, f"{name} is no tensor")
+    _want(t.get_device() >= 0, where, f"{name} is on the host")
+    _want(t.get_device() == dev, where, f"{name} is on {t.device}, not device {dev}")
     _want(t.dtype in dtypes, where, f"{name} has dtype {t.dtype}", NS_EDTYPE)
-    _want(tuple(t.shape) == tuple(shape), where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    _want(t.is_contiguous(), where, f"{name} is not contiguous")
-    return t
+    _want(shape is None or t.shape == shape, where, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    _want(False, where, f"{name} is not contiguous" if shape is not None else f"{name} is no matrix of contiguous rows")
 
 
-_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+def _tensor(t, where: str, name: str, dtype, shape, dev: int):
+    """The address of a contiguous device tensor of `dtype` and `shape`."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _misfit(t, where, name, (dtype,), shape, dev)
+    return t.data_ptr()
 
 
-def _matrix(t, where: str, name: str, dtypes=_FLOATS, device=None):
-    """Checks a device matrix whose rows are contiguous; returns its row stride in elements."""
-    _want(isinstance(t, torch.Tensor) and t.device.type == "cuda", where, f"{name} is no device tensor")
-    _want(device is None or t.device == device, where, f"{name} is on {t.device}, not {device}")
-    _want(t.dtype in dtypes, where, f"{name} has dtype {t.dtype}", NS_EDTYPE)
-    _want(t.dim() == 2 and t.shape[1] >= 1, where, f"{name} has shape {tuple(t.shape)}")
-    _want(t.shape[1] == 1 or t.stride(1) == 1, where, f"the rows of {name} are not contiguous")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    _want(ld >= t.shape[1], where, f"the rows of {name} overlap")
-    return ld
+def _matrix(t, where: str, name: str):
+    """(rows, columns, row stride in elements, dtype code, device) of a device matrix whose rows are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() >= 0 and t.dtype in _FLOATS and t.dim() == 2):
+        _misfit(t, where, name, _FLOATS, None, t.get_device() if isinstance(t, torch.Tensor) else -1)
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    _want(cols >= 1 and (step == 1 or cols == 1), where, f"{name} is no matrix of contiguous rows")
+    if rows <= 1:
+        ld = cols
+    _want(ld >= cols, where, f"the rows of {name} overlap")
+    return rows, cols, ld, _FLOATS[t.dtype], t.get_device()
 
 
-def _on(device, stream, where: str):
-    """The launch stream, on the tensors' own device."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    _want(s.device == device, where, f"the stream is on {s.device}, not {device}")
-    return ctypes.c_void_p(s.cuda_stream)
+def _launch(where: str, fn, dev: int, stream, *args) -> None:
+    """Calls an entry point on the tensors' device, on `stream` or that device's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        _want(stream.device_index == dev, where, f"the stream is on {stream.device}, not device {dev}")
+        raw = stream.cuda_stream
+    if _current_device() == dev:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc != NS_OK:
+        raise NanoSpecError(rc, where)
 
 
 def nanospec_quant_pitch(d: int) -> int:
@@ -611,29 +631,21 @@ def nanospec_quant_pitch(d: int) -> int:
 def nanospec_quant_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
     """x [R, d] (rows contiguous, any row stride) -> q [R, pitch] int8, scale [R] float32."""
     where = "nanospec_quant_rows"
-    ld = _matrix(x, where, "x")
-    R, d = x.shape
-    _tensor(q, where, "q", (torch.int8,), (R, nanospec_quant_pitch(d)), x.device)
-    _tensor(scale, where, "scale", (torch.float32,), (R,), x.device)
-    with torch.cuda.device(x.device):
-        _check(_lib.nanospec_quant_rows(_ptr(x), ld, R, d, dtype_code(x), _ptr(q), _ptr(scale),
-                                        _on(x.device, stream, where)), where)
+    R, d, ld, code, dev = _matrix(x, where, "x")
+    _launch(where, _lib.nanospec_quant_rows, dev, stream, x.data_ptr(), ld, R, d, code,
+            _tensor(q, where, "q", _INT8, (R, _lib.nanospec_quant_pitch(d)), dev),
+            _tensor(scale, where, "scale", _F32, (R,), dev))
 
 
 def nanospec_quant_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, d: int,
                           out: torch.Tensor, stream=None) -> None:
     """xq [M, pitch], wq [N, pitch] int8 with scales xs [M], ws [N] -> out [M, N] (rows contiguous, any row stride)."""
     where = "nanospec_quant_matmul"
-    ld = _matrix(out, where, "out")
-    M, N = out.shape
-    pitch = nanospec_quant_pitch(d)
-    _tensor(xq, where, "xq", (torch.int8,), (M, pitch), out.device)
-    _tensor(wq, where, "wq", (torch.int8,), (N, pitch), out.device)
-    _tensor(xs, where, "xs", (torch.float32,), (M,), out.device)
-    _tensor(ws, where, "ws", (torch.float32,), (N,), out.device)
-    with torch.cuda.device(out.device):
-        _check(_lib.nanospec_quant_matmul(_ptr(xq), _ptr(xs), M, _ptr(wq), _ptr(ws), N, d, _ptr(out), ld,
-                                          dtype_code(out), _on(out.device, stream, where)), where)
+    M, N, ld, code, dev = _matrix(out, where, "out")
+    pitch = _lib.nanospec_quant_pitch(d)
+    _launch(where, _lib.nanospec_quant_matmul, dev, stream, _tensor(xq, where, "xq", _INT8, (M, pitch), dev),
+            _tensor(xs, where, "xs", _F32, (M,), dev), M, _tensor(wq, where, "wq", _INT8, (N, pitch), dev),
+            _tensor(ws, where, "ws", _F32, (N,), dev), N, d, out.data_ptr(), ld, code)
 
 
 def nanospec_quant_logits_workspace_bytes(B: int, n_max: int, M: int, k: int, d: int) -> int:
@@ -646,35 +658,39 @@ def nanospec_quant_logits_topk(wq: torch.Tensor, wscale: torch.Tensor, row_ids: 
                                stream=None) -> None:
     """The head over 8-bit rows: wq [V, pitch], h [B, M, d], row_ids [B, n_max] (None: all V rows), n_dev [B] or None."""
     where = "nanospec_quant_logits_topk"
-    _want(isinstance(h, torch.Tensor) and h.dim() == 3, where, "h is no [B, M, d] tensor")
+    if not (isinstance(h, torch.Tensor) and h.get_device() >= 0 and h.dtype in _FLOATS and h.dim() == 3
+            and h.is_contiguous()):
+        _misfit(h, where, "h", _FLOATS, None, h.get_device() if isinstance(h, torch.Tensor) else -1)
+    dev = h.get_device()
     B, M, d = h.shape
-    _tensor(h, where, "h", _FLOATS, (B, M, d), None)
-    dev = h.device
-    _want(isinstance(wq, torch.Tensor) and wq.dim() == 2, where, "wq is no [V, pitch] tensor")
-    V = wq.shape[0]
-    _tensor(wq, where, "wq", (torch.int8,), (V, nanospec_quant_pitch(d)), dev)
-    _tensor(wscale, where, "wscale", (torch.float32,), (V,), dev)
-    n_max = V
+    _want(isinstance(wscale, torch.Tensor) and wscale.dim() == 1, where, "wscale is no [V] tensor")
+    V = n_max = wscale.shape[0]
     if row_ids is not None:
-        _want(row_ids.dim() == 2, where, "row_ids is no [B, n_max] tensor")
+        _want(isinstance(row_ids, torch.Tensor) and row_ids.dim() == 2, where, "row_ids is no [B, n_max] tensor")
         n_max = row_ids.shape[1]
-        _tensor(row_ids, where, "row_ids", (torch.int32,), (B, n_max), dev)
-    if n_dev is not None:
-        _tensor(n_dev, where, "n_dev", (torch.int32,), (B,), dev)
-    if logits is not None:
-        _tensor(logits, where, "logits", (torch.float32,), (B, M, n_max), dev)
-    _tensor(topk_ids, where, "topk_ids", (torch.int32,), (B, M, k), dev)
-    _tensor(topk_vals, where, "topk_vals", (torch.float32,), (B, M, k), dev)
-    _tensor(work, where, "work", (torch.uint8,), (work.numel(),), dev)
-    with torch.cuda.device(dev):
-        _check(_lib.nanospec_quant_logits_topk(_ptr(wq), _ptr(wscale), _ptr(row_ids), _ptr(n_dev), n_max, B, V, d,
-                                               _ptr(h), dtype_code(h), M, k, _ptr(logits), _ptr(topk_ids),
-                                               _ptr(topk_vals), _ptr(work), work.numel(), _on(dev, stream, where)),
-               where)
+    _launch(where, _lib.nanospec_quant_logits_topk, dev, stream,
+            _tensor(wq, where, "wq", _INT8, (V, _lib.nanospec_quant_pitch(d)), dev),
+            _tensor(wscale, where, "wscale", _F32, (V,), dev),
+            None if row_ids is None else _tensor(row_ids, where, "row_ids", _INT32, (B, n_max), dev),
+            None if n_dev is None else _tensor(n_dev, where, "n_dev", _INT32, (B,), dev), n_max, B, V, d,
+            h.data_ptr(), _FLOATS[h.dtype], M, k,
+            None if logits is None else _tensor(logits, where, "logits", _F32, (B, M, n_max), dev),
+            _tensor(topk_ids, where, "topk_ids", _INT32, (B, M, k), dev),
+            _tensor(topk_vals, where, "topk_vals", _F32, (B, M, k), dev),
+            _tensor(work, where, "work", _UINT8, (work.numel(),), dev), work.numel())
 
 
 def nanospec_token_logprobs_workspace_bytes(L: int, V: int, k: int) -> int:
     return _lib.nanospec_token_logprobs_workspace_bytes(L, V, k)
+
+
+def _pair(a, b, where: str, names: str) -> int:
+    """Columns of a matrix that is given with another of its shape, or not at all (0)."""
+    _want((a is None) == (b is None), where, f"{names} go together")
+    if a is None:
+        return 0
+    _want(isinstance(a, torch.Tensor) and a.dim() == 2, where, f"{names}: no matrix")
+    return a.shape[1]
 
 
 def nanospec_token_logprobs(logits: torch.Tensor, inv_temp: float, tokens: Optional[torch.Tensor],
@@ -684,31 +700,17 @@ def nanospec_token_logprobs(logits: torch.Tensor, inv_temp: float, tokens: Optio
     """logits [L, V] (rows contiguous, any row stride), tokens and logprob [L, T] or None, lse [L], entropy [L] or None,
     top_ids and top_logprobs [L, k] or None."""
     where = "nanospec_token_logprobs"
-    ld = _matrix(logits, where, "logits")
-    L, V = logits.shape
-    dev = logits.device
-    T, k = 0, 0
-    _want((tokens is None) == (logprob is None), where, "tokens and logprob go together")
-    _want((top_ids is None) == (top_logprobs is None), where, "top_ids and top_logprobs go together")
-    if tokens is not None:
-        _want(tokens.dim() == 2, where, "tokens is no [L, T] tensor")
-        T = tokens.shape[1]
-        _tensor(tokens, where, "tokens", (torch.int32,), (L, T), dev)
-        _tensor(logprob, where, "logprob", (torch.float32,), (L, T), dev)
-    if top_ids is not None:
-        _want(top_ids.dim() == 2, where, "top_ids is no [L, k] tensor")
-        k = top_ids.shape[1]
-        _tensor(top_ids, where, "top_ids", (torch.int32,), (L, k), dev)
-        _tensor(top_logprobs, where, "top_logprobs", (torch.float32,), (L, k), dev)
-    _tensor(lse, where, "lse", (torch.float32,), (L,), dev)
-    if entropy is not None:
-        _tensor(entropy, where, "entropy", (torch.float32,), (L,), dev)
-    _tensor(work, where, "work", (torch.uint8,), (work.numel(),), dev)
-    with torch.cuda.device(dev):
-        _check(_lib.nanospec_token_logprobs(_ptr(logits), ld, L, V, dtype_code(logits), inv_temp, _ptr(tokens), T, k,
-                                            _ptr(logprob), _ptr(lse), _ptr(entropy), _ptr(top_ids),
-                                            _ptr(top_logprobs), _ptr(work), work.numel(), _on(dev, stream, where)),
-               where)
+    L, V, ld, code, dev = _matrix(logits, where, "logits")
+    T = _pair(tokens, logprob, where, "tokens and logprob")
+    k = _pair(top_ids, top_logprobs, where, "top_ids and top_logprobs")
+    _launch(where, _lib.nanospec_token_logprobs, dev, stream, logits.data_ptr(), ld, L, V, code, inv_temp,
+            None if tokens is None else _tensor(tokens, where, "tokens", _INT32, (L, T), dev), T, k,
+            None if tokens is None else _tensor(logprob, where, "logprob", _F32, (L, T), dev),
+            _tensor(lse, where, "lse", _F32, (L,), dev),
+            None if entropy is None else _tensor(entropy, where, "entropy", _F32, (L,), dev),
+            None if top_ids is None else _tensor(top_ids, where, "top_ids", _INT32, (L, k), dev),
+            None if top_ids is None else _tensor(top_logprobs, where, "top_logprobs", _F32, (L, k), dev),
+            _tensor(work, where, "work", _UINT8, (work.numel(),), dev), work.numel())
 
 
 def nanospec_token_logprobs_grad(logits: torch.Tensor, inv_temp: float, tokens: Optional[torch.Tensor],
@@ -718,26 +720,18 @@ def nanospec_token_logprobs_grad(logits: torch.Tensor, inv_temp: float, tokens: 
     """dlogits [L, V] of the logits' dtype from the gradients of nanospec_token_logprobs's outputs (None: zeros); dlogits
     may be logits."""
     where = "nanospec_token_logprobs_grad"
-    ld = _matrix(logits, where, "logits")
-    L, V = logits.shape
-    dev = logits.device
-    ld_d = _matrix(dlogits, where, "dlogits", (logits.dtype,), dev)
-    _want(tuple(dlogits.shape) == (L, V), where, f"dlogits has shape {tuple(dlogits.shape)}, not {(L, V)}")
-    T = 0
-    _want((tokens is None) == (g_logprob is None), where, "tokens and g_logprob go together")
-    if tokens is not None:
-        _want(tokens.dim() == 2, where, "tokens is no [L, T] tensor")
-        T = tokens.shape[1]
-        _tensor(tokens, where, "tokens", (torch.int32,), (L, T), dev)
-        _tensor(g_logprob, where, "g_logprob", (torch.float32,), (L, T), dev)
-    _tensor(lse, where, "lse", (torch.float32,), (L,), dev)
-    for t, name in ((entropy, "entropy"), (g_entropy, "g_entropy"), (g_lse, "g_lse")):
-        if t is not None:
-            _tensor(t, where, name, (torch.float32,), (L,), dev)
-    with torch.cuda.device(dev):
-        _check(_lib.nanospec_token_logprobs_grad(_ptr(logits), ld, L, V, dtype_code(logits), inv_temp, _ptr(tokens), T,
-                                                 _ptr(lse), _ptr(entropy), _ptr(g_logprob), _ptr(g_entropy),
-                                                 _ptr(g_lse), _ptr(dlogits), ld_d, _on(dev, stream, where)), where)
+    L, V, ld, code, dev = _matrix(logits, where, "logits")
+    L_d, V_d, ld_d, code_d, dev_d = _matrix(dlogits, where, "dlogits")
+    _want((L_d, V_d, dev_d) == (L, V, dev), where, f"dlogits is {(L_d, V_d)} on device {dev_d}, not {(L, V)} on {dev}")
+    _want(code_d == code, where, f"dlogits has dtype {dlogits.dtype}, not {logits.dtype}", NS_EDTYPE)
+    T = _pair(tokens, g_logprob, where, "tokens and g_logprob")
+    _launch(where, _lib.nanospec_token_logprobs_grad, dev, stream, logits.data_ptr(), ld, L, V, code, inv_temp,
+            None if tokens is None else _tensor(tokens, where, "tokens", _INT32, (L, T), dev), T,
+            _tensor(lse, where, "lse", _F32, (L,), dev),
+            None if entropy is None else _tensor(entropy, where, "entropy", _F32, (L,), dev),
+            None if tokens is None else _tensor(g_logprob, where, "g_logprob", _F32, (L, T), dev),
+            None if g_entropy is None else _tensor(g_entropy, where, "g_entropy", _F32, (L,), dev),
+            None if g_lse is None else _tensor(g_lse, where, "g_lse", _F32, (L,), dev), dlogits.data_ptr(), ld_d)
 
 
 def _alloc(nbytes: int, where: str, device) -> torch.Tensor:

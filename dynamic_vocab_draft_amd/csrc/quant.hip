@@ -174,31 +174,34 @@ __global__ __launch_bounds__(256) void k_product(Product p) {
 // ---------------------------------------------------------------------------
 // The product for more than 64 token rows: compute-bound, tiles in LDS.
 //
-// A block of eight waves owns 256 channel rows and TB * 64 token rows; a wave
-// owns 128 channel rows (eight 16-row operands) and TB * 16 token rows (TB
-// operands), TB * 8 accumulator tiles in registers.  The sum runs in stages
-// of 64 bytes a row.  Four stages of both tiles lie in LDS (32 KB each with
-// TB = 4), filled by direct global-to-LDS loads, so a stage is asked for three
-// stages (about 3000 cycles) before it is read; a wave reads stage s + 1 into
-// registers between the matrix instructions of stage s.  One block barrier a
-// stage: it says that stage s + 1 has landed and that stage s has been read
-// by all, so its place takes stage s + 4.
+// A block of eight waves owns 256 channel rows and TB * 64 token rows of the
+// output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
+// token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
+// in stages of 128 bytes a row, two in LDS (64 KB each with TB = 4), filled by
+// direct global-to-LDS loads.  While one half of a stage (64 bytes a row) is
+// multiplied, the next half is read into a second set of registers; once a
+// wave holds a stage's second half and the next stage has landed, one block
+// barrier frees the stage's place for the stage after next.
 //
-// LDS rows are 64 bytes in four 16-byte places; place c of row r holds chunk
-// c ^ (r / 2 % 4), so that eight consecutive lanes of an operand read, one
-// row each, meet no bank twice.  Each load instruction fills 16 rows.
+// Blocks stay: each takes one tile after the other, and the stages of all its
+// tiles (with the tiles' scales) are one stream of loads, so the next tile's
+// first stages arrive while the last ones of this tile are multiplied and its
+// outputs are stored.  Tiles go to the blocks of one XCD from one contiguous
+// run, in groups of four channel tiles by all token tiles, so that its 32 CUs
+// share rows in its L2.
 //
-// Blocks take tiles so that the 32 CUs of an XCD work at one time on about
-// eight token tiles by four channel tiles, which share their rows in that
-// XCD's L2.
+// Lane i of channel operand t is channel row 8 i + t, so the eight
+// accumulators of a lane are eight consecutive outputs and a store of 16
+// lanes covers 128 of them, without a detour through LDS.  Place c of row r
+// in LDS holds 16-byte chunk c ^ (r / 8 % 8) of channel rows and c ^ (r % 8)
+// of token rows: eight lanes of an operand read meet no bank twice.
 // ---------------------------------------------------------------------------
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 constexpr int kTileN = 256;                        // channel rows of a block
 constexpr int kTileThreads = 512;
-constexpr int kStages = 4;
-constexpr int kStageK = 64;                        // bytes of a row in a stage
+constexpr int kStageK = 128;                       // bytes of a row in a stage
 
 // 16 bytes a lane from a buffer straight into LDS at byte `lds` (the same
 // for the wave) + 16 * lane.  The compiler does not count these loads: the
@@ -206,6 +209,14 @@ constexpr int kStageK = 64;                        // bytes of a row in a stage
 // uses it.
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
+               : "memory");
+}
+
+// The same for four bytes a lane.
+__device__ __forceinline__ void load_word_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :
                : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
                : "memory");
@@ -257,139 +268,164 @@ __device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v
 template <int OT, int TB>
 __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, int tiles_m, int tiles_n) {
   constexpr int TM = TB * 64;                      // token rows of a block
-  constexpr int ROWS = kTileN + TM, STAGE = ROWS * kStageK;
-  constexpr int LA = kTileN / 16 / 8, LB = TM / 16 / 8, LW = LA + LB;   // loads of a wave and stage
-  __shared__ __attribute__((aligned(16))) char lds[kStages * STAGE];
-  // tile of this block: a contiguous run of the tile order for each XCD
-  const int total = tiles_m * tiles_n;
-  const int per = (total + 7) / 8;
-  const int t_id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || t_id >= total) return;
-  const int group = t_id / (tiles_m * 4), rest = t_id % (tiles_m * 4);
-  const int wide = tiles_n - group * 4 < 4 ? tiles_n - group * 4 : 4;   // channel tiles of this group
-  const int n0 = (group * 4 + rest % wide) * kTileN, m0 = rest / wide * TM;
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
-  const int r16 = lane >> 2, chunk = ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
-  uint32_t ao[LA], bo[LB];                         // rows past the end read the last one and are not stored
-#pragma unroll
-  for (int u = 0; u < LA; ++u) {
-    const int r = (u * 8 + w) * 16 + r16;
-    ao[u] = (uint32_t)((n0 + r < p.N ? r : p.N - 1 - n0) * p.pitch + chunk);
-  }
-#pragma unroll
-  for (int u = 0; u < LB; ++u) {
-    const int r = (u * 8 + w) * 16 + r16;
-    bo[u] = (uint32_t)((m0 + r < p.M ? r : p.M - 1 - m0) * p.pitch + chunk);
-  }
-  const u32x4 ra = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(kTileN * p.pitch));
-  const u32x4 rb = buffer_of(p.x + (size_t)m0 * p.pitch, (uint32_t)(TM * p.pitch));
-  const uint32_t base = lds_offset(lds);
-  const auto issue = [&](int buf, int k) {
-#pragma unroll
-    for (int u = 0; u < LA; ++u) load_to_lds(ra, ao[u], k, base + buf * STAGE + (u * 8 + w) * 1024);
-#pragma unroll
-    for (int u = 0; u < LB; ++u) load_to_lds(rb, bo[u], k, base + buf * STAGE + kTileN * kStageK + (u * 8 + w) * 1024);
+  constexpr int STAGE = (kTileN + TM) * kStageK;
+  constexpr int LA = kTileN / 64, LB = TM / 64;    // loads of a wave and stage: 8 rows each
+  constexpr int STORES = TB * 4 * (OT == NS_FP32 ? 2 : 1);   // of a wave and whole tile
+  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE + 2 * 2048];
+  const int total = tiles_m * tiles_n, per = (total + 7) / 8, slots = (int)(gridDim.x >> 3);
+  const int first = (int)(blockIdx.x & 7) * per, end = first + per < total ? first + per : total;
+  int tile = first + (int)(blockIdx.x >> 3);
+  if (tile >= end) return;
+  const auto origin = [&](int t, int& m0, int& n0) {
+    const int group = t / (tiles_m * 4), rest = t % (tiles_m * 4);
+    const int wide = tiles_n - group * 4 < 4 ? tiles_n - group * 4 : 4;   // channel tiles of this group
+    n0 = (group * 4 + rest % wide) * kTileN;
+    m0 = rest / wide * TM;
   };
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int S = p.pitch / kStageK;
+  const uint32_t base = lds_offset(lds);
+
+  // The stream of loads: stage `lk` of tile `lt` comes next.
+  int lt = tile, lk = 0, parity = 0;
+  u32x4 ra, rb, rs;
+  int last_a, last_b, last_s;                      // rows past the end read the last one and are not stored
+  const auto aim = [&]() {
+    int m0, n0;
+    origin(lt, m0, n0);
+    last_a = p.N - 1 - n0;
+    last_b = p.M - 1 - m0;
+    last_s = w < 4 ? last_a : last_b;
+    ra = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(kTileN * p.pitch));
+    rb = buffer_of(p.x + (size_t)m0 * p.pitch, (uint32_t)(TM * p.pitch));
+    // scales: waves 0 to 3 the channels', waves 4 to 7 the tokens', 64 each
+    rs = buffer_of(w < 4 ? p.ws + n0 : p.xs + m0, 1024);
+  };
+  // Load u of the next stage's LA + LB, into buffer buf.
+  const auto load = [&](int u, int buf) {
+    int l = lane;                                  // opaque: the few values below are computed anew each
+    asm volatile("" : "+v"(l));                    // time instead of being held in registers all along
+    const int v = u < LA ? u : u - LA, r = (v * 8 + w) * 8 + (l >> 3), last = u < LA ? last_a : last_b;
+    const int chunk = (l & 7) ^ (u < LA ? w : l >> 3);
+    load_to_lds(u < LA ? ra : rb, __umul24(r < last ? r : last, p.pitch) + chunk * 16, lk * kStageK,
+                base + buf * STAGE + (u < LA ? 0 : kTileN * kStageK) + (v * 8 + w) * 1024);
+  };
+  // Behind a stage's loads: the tile's scales with its first stage, then on to the next stage.
+  const auto advance = [&]() {
+    if (lk == 0) {
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      const int q = (w & 3) * 64 + l;
+      load_word_to_lds(rs, (uint32_t)(q < last_s ? q : last_s) * 4, 0, base + 2 * STAGE + parity * 2048 + w * 256);
+      parity ^= 1;
+    }
+    if (++lk == S) {                               // behind the last tile the stream reads that tile again,
+      lk = 0;                                      // which spares every load a question
+      if (lt + slots < end) {
+        lt += slots;
+        aim();
+      }
+    }
+  };
+
   const int wr = w >> 2, wc = w & 3;
   i32x4 acc[8][TB] = {};
-  i32x4 fa[2][8], fb[2][TB];
-  const int place = i * kStageK + (g ^ ((i >> 1) & 3)) * 16;
-  const char* la = lds + wr * 128 * kStageK + place;
-  const char* lb = lds + (kTileN + wc * TB * 16) * kStageK + place;
-  const int S = p.pitch / kStageK;                 // even
-  issue(0, 0);
-  issue(1, kStageK);
-  if (S > 2) {
-    issue(2, 2 * kStageK);
-    issue(3, 3 * kStageK);
-    wait_loads<3 * LW>();
-  } else {
-    wait_loads<LW>();
+  // The channel operands of the half that is multiplied, 6 and 7 apart: the
+  // next half's replace 0 to 5 as they fall free, and 6 and 7 alternate, so
+  // that no read is still to come behind the half's last products.
+  i32x4 fa[6], fe[2][2], fb[2][TB];
+  // operand t: channel rows wr * 128 + 8 i + t; operand u: token rows (wc * TB + u) * 16 + i
+  const char* la = lds + (wr * 128 + i * 8) * kStageK;
+  const char* lb = lds + (kTileN + wc * TB * 16 + i) * kStageK;
+  const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
+  aim();
+#pragma unroll
+  for (int buf = 0; buf < 2; ++buf) {
+#pragma unroll
+    for (int u = 0; u < LA + LB; ++u) load(u, buf);
+    advance();
   }
+  wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int u = 0; u < TB; ++u) fb[0][u] = *(const i32x4*)(lb + u * 1024);
+  for (int u = 0; u < TB; ++u) fb[0][u] = *(const i32x4*)(lb + place0 + u * 16 * kStageK);
 #pragma unroll
-  for (int t = 0; t < 8; ++t) fa[0][t] = *(const i32x4*)(la + t * 1024);
-  // Stage s is in registers f and in buffer buf; s + 1 goes from buffer next to registers 1 - f.
-  const auto step = [&](int f, int buf, int next, bool more, int k) {
-    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): this wave has read stage s
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    if (more) issue(buf, k);
+  for (int t = 0; t < 6; ++t) fa[t] = *(const i32x4*)(la + place0 + t * kStageK);
+  fe[0][0] = *(const i32x4*)(la + place0 + 6 * kStageK);
+  fe[0][1] = *(const i32x4*)(la + place0 + 7 * kStageK);
+  // Multiplies the half in registers (fe, fb of f) and reads the next from
+  // `at`.  With `more`, the next stage's loads go out between the products,
+  // one for each operand: eight waves that issue theirs all at once wait for
+  // the load unit (64 KB at 64 bytes a cycle) with their products behind them.
+  const auto step = [&](int f, int at, bool more, int buf) {
 #pragma unroll
-    for (int u = 0; u < TB; ++u) fb[1 - f][u] = *(const i32x4*)(lb + next * STAGE + u * 1024);
+    for (int u = 0; u < TB; ++u) fb[1 - f][u] = *(const i32x4*)(lb + at + u * 16 * kStageK);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      fa[1 - f][t] = *(const i32x4*)(la + next * STAGE + t * 1024);
+      if (more && t < LA + LB) load(t, buf);
+      const i32x4 a = t < 6 ? fa[t % 6] : fe[f][t & 1];
 #pragma unroll
-      for (int u = 0; u < TB; ++u) acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[f][t], fb[f][u], acc[t][u], 0, 0, 0);
+      for (int u = 0; u < TB; ++u) acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[f][u], a, acc[t][u], 0, 0, 0);
+      if (t < 6) fa[t % 6] = *(const i32x4*)(la + at + t * kStageK);
+      if (t == 3 || t == 4) fe[1 - f][t - 3] = *(const i32x4*)(la + at + (t + 3) * kStageK);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int s = 0;
-  for (; s + 4 < S; s += 2) {
-    const int b = s & 3;
-    wait_loads<2 * LW>();
-    step(0, b, (b + 1) & 3, true, (s + 4) * kStageK);
-    wait_loads<2 * LW>();
-    step(1, b + 1, (b + 2) & 3, true, (s + 5) * kStageK);
-  }
-  for (; s < S; s += 2) {                          // nothing left to ask for; the last step reads a stage it does not use
-    const int b = s & 3;
-    wait_loads<0>();
-    step(0, b, (b + 1) & 3, false, 0);
-    step(1, b + 1, (b + 2) & 3, false, 0);
-  }
-  // Outputs go through LDS, 16 token rows of a wave at a time, so that a store covers whole lines of a row.
-  __builtin_amdgcn_s_waitcnt(0xC07F);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  constexpr int OP = 132;                          // floats between two token rows there
-  float* lo = (float*)(lds + w * (16 * OP * 4));
-  static_assert(8 * 16 * OP * 4 <= kStages * STAGE, "the waves' output rows fit");
-  const int nw = n0 + wr * 128;
-  float ws[8][4];
-#pragma unroll
-  for (int t = 0; t < 8; ++t)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int n = nw + t * 16 + g * 4 + c;
-      ws[t][c] = p.ws[n < p.N ? n : p.N - 1];
+  int b = 0, scales = 0;
+  bool stored = false;                             // the tile before was whole: STORES stores are behind the loads
+  for (; tile < end; tile += slots) {
+    for (int s = 0; s < S; ++s) {
+      step(0, b * STAGE + place1, false, 0);
+      __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0): this wave has read the stage
+      if (s == 0 && stored) wait_loads<STORES>();
+      else wait_loads<0>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      step(1, (1 - b) * STAGE + place0, true, b);
+      advance();
+      b ^= 1;
     }
+    int m0, n0, l = lane;
+    asm volatile("" : "+v"(l));                    // as in issue
+    const int ni = (l & 15) * 8, mg = (l >> 4) * 4;
+    origin(tile, m0, n0);
+    const float* sw = (const float*)(lds + 2 * STAGE + scales * 2048) + wr * 128 + ni;
+    const float* sx = (const float*)(lds + 2 * STAGE + scales * 2048) + 256 + wc * TB * 16 + mg;
+    scales ^= 1;
+    float ws[8];
 #pragma unroll
-  for (int u = 0; u < TB; ++u) {
-    const int mt = m0 + (wc * TB + u) * 16;
-    const float xs = p.xs[mt + i < p.M ? mt + i : p.M - 1];
+    for (int e = 0; e < 8; ++e) ws[e] = sw[e];
+    const int n = n0 + wr * 128 + ni;
+    stored = m0 + TM <= p.M && n0 + kTileN <= p.N;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      typedef float f32x4 __attribute__((ext_vector_type(4)));
-      f32x4 v;
+    for (int u = 0; u < TB; ++u)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = scaled(acc[t][u][c], xs * ws[t][c]);
-      *(f32x4*)(lo + i * OP + t * 16 + g * 4) = v;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+      for (int r = 0; r < 4; ++r) {
+        const int m = m0 + (wc * TB + u) * 16 + mg + r;
+        const float xs = sx[u * 16 + r];
+        float v[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = q * 4 + g, m = mt + r, n = nw + i * 8;
-      float v[8];
+        for (int e = 0; e < 8; ++e) v[e] = scaled(acc[e][u][r], xs * ws[e]);
+        const size_t at = (size_t)m * (size_t)p.ld_out + n;
+        if (stored) store_eight<OT>(p.out, at, v, 8);
+        else if (m < p.M && n < p.N) store_eight<OT>(p.out, at, v, p.N - n);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = lo[r * OP + i * 8 + e];
-      if (m < p.M && n < p.N) store_eight<OT>(p.out, (size_t)m * (size_t)p.ld_out + n, v, p.N - n);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int u = 0; u < TB; ++u) acc[t][u] = i32x4{0, 0, 0, 0};
   }
+  wait_loads<0>();                                 // the stream's last loads end before their LDS is given back
 }
 
 template <int OT, int TB>
 void launch_tiled(const Product& p, hipStream_t stream) {
   const int tm = (p.M + TB * 64 - 1) / (TB * 64), tn = (p.N + kTileN - 1) / kTileN;
+  // one block a CU, eight XCDs of 32 CUs
   const unsigned per = ((unsigned)tm * (unsigned)tn + 7) / 8;
-  hipLaunchKernelGGL((k_product_tiled<OT, TB>), dim3(per * 8), dim3(kTileThreads), 0, stream, p, tm, tn);
+  hipLaunchKernelGGL((k_product_tiled<OT, TB>), dim3((per < 32 ? per : 32) * 8), dim3(kTileThreads), 0, stream, p, tm,
+                     tn);
 }
 
 template <int OT>

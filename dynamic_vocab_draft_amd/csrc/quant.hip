@@ -171,36 +171,9 @@ __global__ __launch_bounds__(256) void k_product(Product p) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// The product for more than 64 token rows: compute-bound, tiles in LDS.
-//
-// A block of eight waves owns 256 channel rows and TB * 64 token rows of the
-// output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
-// token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
-// in stages of 128 bytes a row, two in LDS (64 KB each with TB = 4), filled by
-// direct global-to-LDS loads.  While one half of a stage (64 bytes a row) is
-// multiplied, the next half is read into a second set of registers; once a
-// wave holds a stage's second half and the next stage has landed, one block
-// barrier frees the stage's place for the stage after next.
-//
-// Blocks stay: each takes one tile after the other, and the stages of all its
-// tiles (with the tiles' scales) are one stream of loads, so the next tile's
-// first stages arrive while the last ones of this tile are multiplied and its
-// outputs are stored.  Tiles go to the blocks of one XCD from one contiguous
-// run, in groups of four channel tiles by all token tiles, so that its 32 CUs
-// share rows in its L2.
-//
-// Lane i of channel operand t is channel row 8 i + t, so the eight
-// accumulators of a lane are eight consecutive outputs and a store of 16
-// lanes covers 128 of them, without a detour through LDS.  Place c of row r
-// in LDS holds 16-byte chunk c ^ (r / 8 % 8) of channel rows and c ^ (r % 8)
-// of token rows: eight lanes of an operand read meet no bank twice.
-// ---------------------------------------------------------------------------
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
-constexpr int kTileN = 256;                        // channel rows of a block
-constexpr int kTileThreads = 512;
 constexpr int kStageK = 128;                       // bytes of a row in a stage
 
 // 16 bytes a lane from a buffer straight into LDS at byte `lds` (the same
@@ -209,6 +182,14 @@ constexpr int kStageK = 128;                       // bytes of a row in a stage
 // uses it.
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
+               : "memory");
+}
+
+// The same for bytes that are read once: the caches need not keep them.
+__device__ __forceinline__ void load_to_lds_once(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
                :
                : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
                : "memory");
@@ -264,6 +245,175 @@ __device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v
       if (e < n) store_out<OT>(out, i + e, v[e]);
   }
 }
+
+// ---------------------------------------------------------------------------
+// The product for up to 64 token rows: bound by the bytes of the channel rows,
+// each read once.
+//
+// One block of eight waves a CU takes an even share of the 16-row channel
+// units and runs through it eight units at a time, one a wave, in stages of
+// 128 bytes a row.  A ring of stages in LDS is filled by direct
+// global-to-LDS loads, R - 1 stages (80 to 100 KB a CU) ahead, across the
+// ends of units; channel rows are private to their wave, token rows shared by
+// the block, so one barrier a stage orders the ring.  Waits count the loads
+// that may still be out; outputs leave by buffer stores, which out-of-range
+// lanes take part in without effect, so the stores behind a unit's last
+// stage are as many for every unit and the waits can allow for them.
+//
+// The token rows are operand A and the channel rows operand B, so 16 lanes
+// hold 16 consecutive outputs of a token.  Place c of row r in LDS holds
+// 16-byte chunk c ^ (r % 8).
+// ---------------------------------------------------------------------------
+constexpr int kStreamWaves = 8;
+
+constexpr int stream_ring(int NMT) { return NMT <= 2 ? 7 : 6; }
+
+template <int OT, int NMT>
+__global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Product p, int units, int per_block) {
+  constexpr int R = stream_ring(NMT);
+  constexpr int XOFF = kStreamWaves * 16 * kStageK, SOFF = XOFF + NMT * 16 * kStageK;
+  constexpr int STAGE = SOFF + kStreamWaves * 256;   // channel rows, token rows, channel scales
+  constexpr int LW = 2 + (NMT == 4 ? 1 : NMT);       // loads of a wave and stage
+  constexpr int STORES = NMT * 4;
+  __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
+  const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
+  const int passes = (u1 - u0 + kStreamWaves - 1) / kStreamWaves;
+  if (passes <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int S = p.pitch / kStageK;
+  const uint32_t base = lds_offset(lds);
+  const int n0 = u0 * 16;                            // the block's first channel row
+  const int last = (u1 * 16 < p.N ? u1 * 16 : p.N) - 1 - n0;
+  const u32x4 rw = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(last + 1) * p.pitch);
+  const u32x4 rx = buffer_of(p.x, (uint32_t)(p.M * p.pitch));
+  const u32x4 rs = buffer_of(p.ws + n0, (uint32_t)(last + 1) * 4);
+  // token rows past the end read the last one and are not stored
+  uint32_t xo[NMT == 4 ? 1 : NMT];
+  if (NMT == 4) {
+    const int r = w * 8 + (lane >> 3);
+    xo[0] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + ((lane & 7) ^ (lane >> 3)) * 16);
+  } else {
+#pragma unroll
+    for (int v = 0; v < NMT; ++v) {                  // two rows a load, a word a lane
+      const int r = v * 16 + w * 2 + (lane >> 5), q = lane & 31;
+      xo[v] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + (((q >> 2) ^ (r & 7)) * 4 + (q & 3)) * 4);
+    }
+  }
+  // The stream of loads: stage `lk` of pass `lp` comes next, into place `lb`.
+  int lp = 0, lk = 0, lb = 0;
+  const auto issue = [&]() {
+    const uint32_t to = base + lb * STAGE;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int r = (lp * kStreamWaves + w) * 16 + v * 8 + (lane >> 3);
+      load_to_lds_once(rw, __umul24(r < last ? r : last, p.pitch) + ((lane & 7) ^ (lane >> 3)) * 16, lk * kStageK,
+                       to + (w * 2 + v) * 1024);
+    }
+    if (NMT == 4) {
+      load_to_lds(rx, xo[0], lk * kStageK, to + XOFF + w * 1024);
+    } else {
+#pragma unroll
+      for (int v = 0; v < NMT; ++v) load_word_to_lds(rx, xo[v], lk * kStageK, to + XOFF + (v * 8 + w) * 256);
+    }
+    if (lk == 0) {
+      const int r = (lp * kStreamWaves + w) * 16 + i;
+      load_word_to_lds(rs, (uint32_t)(r < last ? r : last) * 4, 0, to + SOFF + w * 256);
+    }
+    lb = lb + 1 == R ? 0 : lb + 1;
+    if (++lk == S) {                                 // behind the last pass the stream reads that pass again,
+      lk = 0;                                        // which spares every load a question
+      if (lp + 1 < passes) ++lp;
+    }
+  };
+  float xs[NMT][4];
+#pragma unroll
+  for (int u = 0; u < NMT; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = u * 16 + g * 4 + r;
+      xs[u][r] = p.xs[m < p.M ? m : p.M - 1];
+    }
+  const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(p.out, 0, 0x7FFFFFFF, 0x00027000);
+  constexpr int ESZ = OT == NS_FP32 ? 4 : 2;
+  i32x4 acc[NMT] = {};
+  // the scales are here before the loads are counted
+#pragma unroll
+  for (int u = 0; u < NMT; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(xs[u][r]));
+#pragma unroll
+  for (int v = 0; v < R - 1; ++v) issue();
+  const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
+  const char* lw = lds + (w * 16 + i) * kStageK;
+  const char* lx = lds + XOFF + i * kStageK;
+  int b = 0, since = R;                              // stages since the last stores
+  float ws = 0.f;
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int s = 0; s < S; ++s) {
+      // this stage's loads are done when at most those of the R - 2 stages
+      // behind it, and the stores between them, are out
+      if (since < R - 2) wait_loads<(R - 2) * LW + STORES>();
+      else wait_loads<(R - 2) * LW>();
+      ++since;
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      issue();                                       // into the place of the stage before, which all have read
+      const char* at = lw + b * STAGE;
+      const char* xt = lx + b * STAGE;
+      if (s == 0) ws = *(const float*)(lds + b * STAGE + SOFF + w * 256 + i * 4);
+      const i32x4 f0 = *(const i32x4*)(at + place0), f1 = *(const i32x4*)(at + place1);
+#pragma unroll
+      for (int u = 0; u < NMT; ++u) {
+        acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4*)(xt + u * 16 * kStageK + place0), f0, acc[u], 0, 0, 0);
+        acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4*)(xt + u * 16 * kStageK + place1), f1, acc[u], 0, 0, 0);
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): this wave has read the stage
+      b = b + 1 == R ? 0 : b + 1;
+    }
+    const int j = (pass * kStreamWaves + w) * 16 + i;
+#pragma unroll
+    for (int u = 0; u < NMT; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int m = u * 16 + g * 4 + r;
+        const float v = scaled(acc[u][r], xs[u][r] * ws);
+        const uint32_t at = m < p.M && j <= last ? (uint32_t)(((size_t)m * (size_t)p.ld_out + n0 + j) * ESZ) : 0x80000000u;
+        if (OT == NS_FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)narrow2<OT>(v, 0.f), ro, at, 0, 0);
+        acc[u][r] = 0;
+      }
+    since = 0;
+  }
+  wait_loads<0>();                                   // the stream's last loads end before their LDS is given back
+}
+
+// ---------------------------------------------------------------------------
+// The product for more than 64 token rows: compute-bound, tiles in LDS.
+//
+// A block of eight waves owns 256 channel rows and TB * 64 token rows of the
+// output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
+// token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
+// in stages of 128 bytes a row, two in LDS (64 KB each with TB = 4), filled by
+// direct global-to-LDS loads.  While one half of a stage (64 bytes a row) is
+// multiplied, the next half is read into a second set of registers; once a
+// wave holds a stage's second half and the next stage has landed, one block
+// barrier frees the stage's place for the stage after next.
+//
+// Blocks stay: each takes one tile after the other, and the stages of all its
+// tiles (with the tiles' scales) are one stream of loads, so the next tile's
+// first stages arrive while the last ones of this tile are multiplied and its
+// outputs are stored.  Tiles go to the blocks of one XCD from one contiguous
+// run, in groups of four channel tiles by all token tiles, so that its 32 CUs
+// share rows in its L2.
+//
+// Lane i of channel operand t is channel row 8 i + t, so the eight
+// accumulators of a lane are eight consecutive outputs and a store of 16
+// lanes covers 128 of them, without a detour through LDS.  Place c of row r
+// in LDS holds 16-byte chunk c ^ (r / 8 % 8) of channel rows and c ^ (r % 8)
+// of token rows: eight lanes of an operand read meet no bank twice.
+// ---------------------------------------------------------------------------
+constexpr int kTileN = 256;                        // channel rows of a block
+constexpr int kTileThreads = 512;
 
 template <int OT, int TB>
 __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, int tiles_m, int tiles_n) {
@@ -428,8 +578,22 @@ void launch_tiled(const Product& p, hipStream_t stream) {
                      tn);
 }
 
+template <int OT, int NMT>
+void launch_stream(const Product& p, hipStream_t stream) {
+  const int units = (p.N + 15) / 16, per = (units + 255) / 256;
+  hipLaunchKernelGGL((k_product_stream<OT, NMT>), dim3((unsigned)((units + per - 1) / per)),
+                     dim3(kStreamWaves * NS_WAVE), 0, stream, p, units, per);
+}
+
 template <int OT>
 void launch_product(const Product& p, int B, hipStream_t stream) {
+  if (p.M <= 64 && !p.ids && (uint64_t)p.M * (uint64_t)p.ld_out * (OT == NS_FP32 ? 4 : 2) < 0x7FFFFFFFull) {
+    if (p.M <= 16) launch_stream<OT, 1>(p, stream);
+    else if (p.M <= 32) launch_stream<OT, 2>(p, stream);
+    else if (p.M <= 48) launch_stream<OT, 3>(p, stream);
+    else launch_stream<OT, 4>(p, stream);
+    return;
+  }
   if (p.M > 64) {
     if (p.M > 128) launch_tiled<OT, 4>(p, stream);
     else launch_tiled<OT, 2>(p, stream);

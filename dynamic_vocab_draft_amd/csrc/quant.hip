@@ -251,33 +251,42 @@ __device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v
 // each read once.
 //
 // One block of eight waves a CU takes an even share of the 16-row channel
-// units and runs through it eight units at a time, one a wave, in stages of
+// units and runs through it in passes of 8 RT units, RT a wave, in stages of
 // 128 bytes a row.  A ring of stages in LDS is filled by direct
-// global-to-LDS loads, R - 1 stages (80 to 100 KB a CU) ahead, across the
-// ends of units; channel rows are private to their wave, token rows shared by
+// global-to-LDS loads, R - 1 stages (64 to 96 KB a CU) ahead, across the
+// ends of passes; channel rows are private to their wave, token rows shared by
 // the block, so one barrier a stage orders the ring.  Waits count the loads
 // that may still be out; outputs leave by buffer stores, which out-of-range
-// lanes take part in without effect, so the stores behind a unit's last
-// stage are as many for every unit and the waits can allow for them.
+// lanes take part in without effect, so the stores behind a pass are as many
+// for every pass and the waits can allow for them.
+//
+// Block b begins every row at stage 5 b mod S and goes round (the sum is
+// exact in any order): blocks that walked along their rows in step would read
+// addresses alike in their low bits, a few memory channels' worth.  8 x 128256
+// x 4096: 98.9 -> 79.0 us (6.6 TB/s).
 //
 // The token rows are operand A and the channel rows operand B, so 16 lanes
 // hold 16 consecutive outputs of a token.  Place c of row r in LDS holds
-// 16-byte chunk c ^ (r % 8).
+// 16-byte chunk c ^ (r % 8): no bank is met twice.
+// More than 32 tokens take RT = 2: a stage's token rows, which all eight waves
+// read from LDS, then serve twice the channel rows (60 x 151936 x 3584: 110
+// -> 103 us, 5.5 TB/s with the outputs; 8 x 128256 x 4096 79 -> 81 us).
+// Without the output stores it takes 89 us; stores of two outputs a lane took
+// as long as these.
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8;
 
-constexpr int stream_ring(int NMT) { return NMT <= 2 ? 7 : 6; }
-
-template <int OT, int NMT>
+template <int OT, int NMT, int RT, int R>
 __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Product p, int units, int per_block) {
-  constexpr int R = stream_ring(NMT);
-  constexpr int XOFF = kStreamWaves * 16 * kStageK, SOFF = XOFF + NMT * 16 * kStageK;
+  constexpr int WROWS = RT * 16, PROWS = kStreamWaves * WROWS;
+  constexpr int XOFF = PROWS * kStageK, SOFF = XOFF + NMT * 16 * kStageK;
   constexpr int STAGE = SOFF + kStreamWaves * 256;   // channel rows, token rows, channel scales
-  constexpr int LW = 2 + (NMT == 4 ? 1 : NMT);       // loads of a wave and stage
-  constexpr int STORES = NMT * 4;
+  constexpr int LW = 2 * RT + (NMT == 4 ? 1 : NMT);  // loads of a wave and stage
+  constexpr int STORES = RT * NMT * 4;
+  static_assert((R - 2) * LW + STORES < 64, "vmcnt range");
   __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
   const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
-  const int passes = (u1 - u0 + kStreamWaves - 1) / kStreamWaves;
+  const int passes = (u1 - u0 + kStreamWaves * RT - 1) / (kStreamWaves * RT);
   if (passes <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
   const int S = p.pitch / kStageK;
@@ -299,27 +308,28 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
       xo[v] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + (((q >> 2) ^ (r & 7)) * 4 + (q & 3)) * 4);
     }
   }
-  // The stream of loads: stage `lk` of pass `lp` comes next, into place `lb`.
-  int lp = 0, lk = 0, lb = 0;
+  // The stream of loads: the lk-th stage of pass lp comes next, bytes ks of the rows, into place lb.
+  int lp = 0, lk = 0, lb = 0, ks = (int)(blockIdx.x * 5u) % S * kStageK;
   const auto issue = [&]() {
     const uint32_t to = base + lb * STAGE;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int r = (lp * kStreamWaves + w) * 16 + v * 8 + (lane >> 3);
-      load_to_lds_once(rw, __umul24(r < last ? r : last, p.pitch) + ((lane & 7) ^ (lane >> 3)) * 16, lk * kStageK,
-                       to + (w * 2 + v) * 1024);
+    for (int v = 0; v < 2 * RT; ++v) {
+      const int r = (lp * kStreamWaves + w) * WROWS + v * 8 + (lane >> 3);
+      load_to_lds_once(rw, __umul24(r < last ? r : last, p.pitch) + ((lane & 7) ^ (lane >> 3)) * 16, ks,
+                       to + (w * 2 * RT + v) * 1024);
     }
     if (NMT == 4) {
-      load_to_lds(rx, xo[0], lk * kStageK, to + XOFF + w * 1024);
+      load_to_lds(rx, xo[0], ks, to + XOFF + w * 1024);
     } else {
 #pragma unroll
-      for (int v = 0; v < NMT; ++v) load_word_to_lds(rx, xo[v], lk * kStageK, to + XOFF + (v * 8 + w) * 256);
+      for (int v = 0; v < NMT; ++v) load_word_to_lds(rx, xo[v], ks, to + XOFF + (v * 8 + w) * 256);
     }
     if (lk == 0) {
-      const int r = (lp * kStreamWaves + w) * 16 + i;
+      const int r = (lp * kStreamWaves + w) * WROWS + (lane & (WROWS - 1));
       load_word_to_lds(rs, (uint32_t)(r < last ? r : last) * 4, 0, to + SOFF + w * 256);
     }
     lb = lb + 1 == R ? 0 : lb + 1;
+    ks = ks + kStageK == p.pitch ? 0 : ks + kStageK;
     if (++lk == S) {                                 // behind the last pass the stream reads that pass again,
       lk = 0;                                        // which spares every load a question
       if (lp + 1 < passes) ++lp;
@@ -335,7 +345,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     }
   const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(p.out, 0, 0x7FFFFFFF, 0x00027000);
   constexpr int ESZ = OT == NS_FP32 ? 4 : 2;
-  i32x4 acc[NMT] = {};
+  i32x4 acc[RT][NMT] = {};
   // the scales are here before the loads are counted
 #pragma unroll
   for (int u = 0; u < NMT; ++u)
@@ -344,15 +354,15 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
 #pragma unroll
   for (int v = 0; v < R - 1; ++v) issue();
   const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
-  const char* lw = lds + (w * 16 + i) * kStageK;
+  const char* lw = lds + (w * WROWS + i) * kStageK;
   const char* lx = lds + XOFF + i * kStageK;
   int b = 0, since = R;                              // stages since the last stores
-  float ws = 0.f;
+  float ws[RT] = {};
   for (int pass = 0; pass < passes; ++pass) {
     for (int s = 0; s < S; ++s) {
       // this stage's loads are done when at most those of the R - 2 stages
       // behind it, and the stores between them, are out
-      if (since < R - 2) wait_loads<(R - 2) * LW + STORES>();
+      if (since < R - 1) wait_loads<(R - 2) * LW + STORES>();
       else wait_loads<(R - 2) * LW>();
       ++since;
       __builtin_amdgcn_s_barrier();
@@ -360,28 +370,45 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
       issue();                                       // into the place of the stage before, which all have read
       const char* at = lw + b * STAGE;
       const char* xt = lx + b * STAGE;
-      if (s == 0) ws = *(const float*)(lds + b * STAGE + SOFF + w * 256 + i * 4);
-      const i32x4 f0 = *(const i32x4*)(at + place0), f1 = *(const i32x4*)(at + place1);
+      if (s == 0) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) ws[t] = *(const float*)(lds + b * STAGE + SOFF + w * 256 + (t * 16 + i) * 4);
+      }
+      i32x4 f[RT][2];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        f[t][0] = *(const i32x4*)(at + t * 16 * kStageK + place0);
+        f[t][1] = *(const i32x4*)(at + t * 16 * kStageK + place1);
+      }
 #pragma unroll
       for (int u = 0; u < NMT; ++u) {
-        acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4*)(xt + u * 16 * kStageK + place0), f0, acc[u], 0, 0, 0);
-        acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4*)(xt + u * 16 * kStageK + place1), f1, acc[u], 0, 0, 0);
+        const i32x4 x0 = *(const i32x4*)(xt + u * 16 * kStageK + place0);
+        const i32x4 x1 = *(const i32x4*)(xt + u * 16 * kStageK + place1);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x0, f[t][0], acc[t][u], 0, 0, 0);
+          acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x1, f[t][1], acc[t][u], 0, 0, 0);
+        }
       }
       __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): this wave has read the stage
       b = b + 1 == R ? 0 : b + 1;
     }
-    const int j = (pass * kStreamWaves + w) * 16 + i;
 #pragma unroll
-    for (int u = 0; u < NMT; ++u)
+    for (int t = 0; t < RT; ++t) {
+      const int j = (pass * kStreamWaves + w) * WROWS + t * 16 + i;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int m = u * 16 + g * 4 + r;
-        const float v = scaled(acc[u][r], xs[u][r] * ws);
-        const uint32_t at = m < p.M && j <= last ? (uint32_t)(((size_t)m * (size_t)p.ld_out + n0 + j) * ESZ) : 0x80000000u;
-        if (OT == NS_FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)narrow2<OT>(v, 0.f), ro, at, 0, 0);
-        acc[u][r] = 0;
-      }
+      for (int u = 0; u < NMT; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int m = u * 16 + g * 4 + r;
+          const float v = scaled(acc[t][u][r], xs[u][r] * ws[t]);
+          const uint32_t at =
+              m < p.M && j <= last ? (uint32_t)(((size_t)m * (size_t)p.ld_out + n0 + j) * ESZ) : 0x80000000u;
+          if (OT == NS_FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)narrow2<OT>(v, 0.f), ro, at, 0, 0);
+          acc[t][u][r] = 0;
+        }
+    }
     since = 0;
   }
   wait_loads<0>();                                   // the stream's last loads end before their LDS is given back
@@ -578,20 +605,20 @@ void launch_tiled(const Product& p, hipStream_t stream) {
                      tn);
 }
 
-template <int OT, int NMT>
+template <int OT, int NMT, int RT, int R>
 void launch_stream(const Product& p, hipStream_t stream) {
   const int units = (p.N + 15) / 16, per = (units + 255) / 256;
-  hipLaunchKernelGGL((k_product_stream<OT, NMT>), dim3((unsigned)((units + per - 1) / per)),
+  hipLaunchKernelGGL((k_product_stream<OT, NMT, RT, R>), dim3((unsigned)((units + per - 1) / per)),
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p, units, per);
 }
 
 template <int OT>
 void launch_product(const Product& p, int B, hipStream_t stream) {
   if (p.M <= 64 && !p.ids && (uint64_t)p.M * (uint64_t)p.ld_out * (OT == NS_FP32 ? 4 : 2) < 0x7FFFFFFFull) {
-    if (p.M <= 16) launch_stream<OT, 1>(p, stream);
-    else if (p.M <= 32) launch_stream<OT, 2>(p, stream);
-    else if (p.M <= 48) launch_stream<OT, 3>(p, stream);
-    else launch_stream<OT, 4>(p, stream);
+    if (p.M <= 16) launch_stream<OT, 1, 1, 7>(p, stream);
+    else if (p.M <= 32) launch_stream<OT, 2, 1, 7>(p, stream);
+    else if (p.M <= 48) launch_stream<OT, 3, 2, 3>(p, stream);
+    else launch_stream<OT, 4, 2, 3>(p, stream);
     return;
   }
   if (p.M > 64) {

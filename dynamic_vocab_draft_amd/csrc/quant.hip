@@ -21,78 +21,202 @@ constexpr int kPitch = 128;            // 8-bit rows start every multiple of 128
 __host__ __device__ constexpr int pitch_of(int d) { return (d + kPitch - 1) / kPitch * kPitch; }
 
 // ---------------------------------------------------------------------------
-// Row quantisation
+// Row quantisation: one pass.  The lanes of a row hold it in registers (up to
+// eight groups of eight elements each) between the maximum and the rounding.
 // ---------------------------------------------------------------------------
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));   // rows start at any element
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
 template <int ET>
-__device__ __forceinline__ float load_elem(const void* x, size_t i) {
-  if (ET == NS_FP32) return ((const float*)x)[i];
-  const uint32_t w = ((const uint16_t*)x)[i];
-  return ET == NS_BF16 ? ns::bf16_lo(w) : ns::fp16_lo(w);
+__device__ __forceinline__ uint32_t load_bits(const void* x, size_t i) {
+  return ET == NS_FP32 ? ((const uint32_t*)x)[i] : ((const uint16_t*)x)[i];
 }
 
-// round(127 |x| / a), halves to even, exactly.  t = |x| * (127 / a) carries
-// at most two roundings, 127 * 2^-23 in all; only where that could reach a
-// half is the side decided, by comparing 254 |x| with (2 f + 1) a, both exact
-// in float64 (24 + 8 bits).
-__device__ __forceinline__ float quant_abs(float x, float inv, float a) {
-  const float t = x * inv;
-  const float f = floorf(t), r = t - f;
-  float q = r > 0.5f ? f + 1.f : f;
-  if (fabsf(r - 0.5f) < 4e-5f) {
-    const double l = 254.0 * (double)x, h = (2.0 * (double)f + 1.0) * (double)a;
-    q = l > h ? f + 1.f : (l < h ? f : f + (float)((int)f & 1));
+// Eight elements as they are stored: 16-bit types in one vector, float32 in two.
+template <int ET>
+struct Eight {
+  u32x4 v[ET == NS_FP32 ? 2 : 1];
+
+  // elements i .. i + 7 of a row, zeros at or past d
+  __device__ __forceinline__ void load(const char* row, int i, int d) {
+    constexpr int N = ET == NS_FP32 ? 2 : 1;
+    if (i + 8 <= d) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] = *(const u32x4_any*)(row + (size_t)i * (2 * N) + n * 16);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w = 0;
+          if (ET == NS_FP32) {
+            if (i + n * 4 + c < d) w = load_bits<ET>(row, i + n * 4 + c);
+          } else {
+            if (i + c * 2 < d) w = load_bits<ET>(row, i + c * 2);
+            if (i + c * 2 + 1 < d) w |= load_bits<ET>(row, i + c * 2 + 1) << 16;
+          }
+          v[n][c] = w;
+        }
+    }
   }
-  return q;
-}
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (ET == NS_FP32) return __uint_as_float(v[e >> 2][e & 3]);
+    else if constexpr (ET == NS_BF16) return e & 1 ? ns::bf16_hi(v[0][e >> 1]) : ns::bf16_lo(v[0][e >> 1]);
+    else return e & 1 ? ns::fp16_hi(v[0][e >> 1]) : ns::fp16_lo(v[0][e >> 1]);
+  }
+  // The largest magnitude as the type's own bits, which order like the values
+  // with infinities and NaN on top; two at once for 16-bit types.
+  __device__ __forceinline__ uint32_t top(uint32_t so_far) const {
+    if constexpr (ET == NS_FP32) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t u = v[n][c] & 0x7FFFFFFFu;
+          so_far = u > so_far ? u : so_far;
+        }
+      return so_far;
+    } else {
+      u16x2 m = __builtin_bit_cast(u16x2, so_far);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[0][c] & 0x7FFF7FFFu));
+      return __builtin_bit_cast(uint32_t, m);
+    }
+  }
+};
 
-__device__ __forceinline__ int quant_one(float x, float inv, float a) {
-  const int q = (int)quant_abs(fabsf(x), inv, a);
+// round(127 |x| / a), halves to even, decided without a rounding: 254 |x| and
+// (2 f + 1) a are exact in float64 (24 + 8 bits).
+__device__ __forceinline__ int quant_exact(float x, float a) {
+  const float t = fabsf(x) * (127.f / a);
+  const float f = floorf(t), r = t - f;
+  int q = (int)f + (r > 0.5f);
+  if (fabsf(r - 0.5f) < 4e-5f) {
+    const double l = 254.0 * (double)fabsf(x), h = (2.0 * (double)f + 1.0) * (double)a;
+    q = l > h ? (int)f + 1 : (l < h ? (int)f : (int)f + ((int)f & 1));
+  }
   return x < 0.f ? -q : q;
 }
 
+// Eight elements to eight bytes.  x * inv + 1.5 * 2^23 has round(x * inv) in
+// its low byte.  inv = 127 / a is off by at most 2^-24 relatively, so 127
+// times that in the product: only where that could reach a half (within
+// 1.6e-5 of one) are the eight decided exactly.
 template <int ET>
-__global__ __launch_bounds__(256) void k_quant_rows(const void* __restrict__ x, int64_t ld, int d,
-                                                    int8_t* __restrict__ q, float* __restrict__ scale) {
-  __shared__ float sh[4];
-  const size_t r = blockIdx.x;
-  const int tid = threadIdx.x, pitch = pitch_of(d);
-  const size_t base = r * (size_t)ld;
-  // The bit patterns of |x| order like the values, NaN above infinity.
-  uint32_t top = 0;
-  for (int i = tid; i < d; i += 256) {
-    const uint32_t u = __float_as_uint(load_elem<ET>(x, base + i)) & 0x7FFFFFFFu;
-    top = u > top ? u : top;
+__device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, float inv, float a) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t b[8];
+  float off = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = x.get(e), f = fmaf(v, inv, kMagic);
+    off = fmaxf(off, fabsf(fmaf(v, inv, kMagic - f)));
+    b[e] = __float_as_uint(f);
   }
-  for (int m = 32; m >= 1; m >>= 1) {
-    const uint32_t o = __shfl_xor(top, m, NS_WAVE);
-    top = o > top ? o : top;
+  if (off > 0.5f - 1.6e-5f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = (uint32_t)quant_exact(x.get(e), a);
   }
-  if ((tid & 63) == 0) sh[tid / 64] = __uint_as_float(top);
-  __syncthreads();
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t o = __float_as_uint(sh[i]);
-    top = o > top ? o : top;
+  u32x2 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000C0Cu);
+    r[h] = lo | hi;
   }
-  const bool bad = top >= 0x7F800000u, none = top == 0;
-  const float a = __uint_as_float(top);
-  // A maximum below 2^-100 is raised by 2^64 (exactly) so that 127 / a stays finite.
-  const float up = a < 0x1p-100f ? 0x1p64f : 1.f;
-  const float inv = 127.f / (a * up);
-  int8_t* row = q + r * (size_t)pitch;
-  for (int i = tid; i < pitch; i += 256) {
-    int v = 0;
-    if (i < d && !bad && !none) v = quant_one(load_elem<ET>(x, base + i) * up, inv, a * up);
-    row[i] = (int8_t)v;
+  return r;
+}
+
+constexpr int kQuantThreads = 256;
+
+// T lanes (a wave or the block) take a row, G groups of eight elements each.
+template <int ET, int T, int G>
+__global__ __launch_bounds__(kQuantThreads) void k_quant_rows(const void* __restrict__ x, int64_t ld, int R, int d,
+                                                              int8_t* __restrict__ q, float* __restrict__ scale) {
+  __shared__ uint32_t sh[kQuantThreads / NS_WAVE];
+  const int tid = threadIdx.x, t = tid & (T - 1);
+  const int64_t r = (int64_t)blockIdx.x * (kQuantThreads / T) + tid / T;
+  if (r >= R) return;                              // whole waves, where a wave takes a row
+  const int pitch = pitch_of(d);
+  const char* row = (const char*)x + (size_t)r * (size_t)ld * (ET == NS_FP32 ? 4 : 2);
+  Eight<ET> v[G];
+  uint32_t m = 0;
+#pragma unroll
+  for (int g = 0; g < G; ++g) v[g].load(row, (t + g * T) * 8, d);
+  NS_ISSUE_FENCE();
+#pragma unroll
+  for (int g = 0; g < G; ++g) m = v[g].top(m);
+  float top;
+  if (ET == NS_FP32) top = __uint_as_float(m);
+  else {
+    const uint32_t lo = m & 0xFFFFu, hi = m >> 16, b = lo > hi ? lo : hi;
+    top = ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b);
   }
-  if (tid == 0) scale[r] = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
+  m = __float_as_uint(top);                        // float32 bits order the same way
+#pragma unroll
+  for (int s = 32; s >= 1; s >>= 1) {
+    const uint32_t o = __shfl_xor(m, s, NS_WAVE);
+    m = o > m ? o : m;
+  }
+  if (T > NS_WAVE) {
+    if ((tid & 63) == 0) sh[tid / NS_WAVE] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < T / NS_WAVE; ++w) m = sh[w] > m ? sh[w] : m;
+  }
+  const bool bad = m >= 0x7F800000u;
+  const float a = __uint_as_float(m);
+  int8_t* out = q + (size_t)r * (size_t)pitch;
+  if (bad || a < 0x1p-100f) {                      // uniform over the row; zeros and the smallest magnitudes here
+    // 127 / a would overflow: everything 2^64 times as large, which is exact
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = (t + g * T) * 8;
+      for (int e = 0; e < 8 && i < pitch; ++e)
+        out[i + e] = bad || m == 0 ? (int8_t)0 : (int8_t)quant_exact(v[g].get(e) * 0x1p64f, a * 0x1p64f);
+    }
+  } else {
+    const float inv = 127.f / a;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = (t + g * T) * 8;
+      if (i < pitch) *(u32x2*)(out + i) = quant_eight<ET>(v[g], inv, a);
+    }
+  }
+  if (t == 0) scale[r] = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
+}
+
+template <int ET>
+int quant_rows_of(const void* x, int64_t ld, int R, int d, int8_t* q, float* scale, hipStream_t stream) {
+  const int groups = pitch_of(d) / 8;
+  // A wave takes a row where it can hold it and the rows fill the chip
+  // without a block each.
+  const bool wave = groups <= 8 * NS_WAVE && (R >= 1024 || groups <= NS_WAVE);
+  const int T = wave ? NS_WAVE : kQuantThreads, g = (groups + T - 1) / T;
+  const dim3 grid((unsigned)((R + kQuantThreads / T - 1) / (kQuantThreads / T))), block(kQuantThreads);
+#define NS_LAUNCH_QUANT(TT, G) \
+  hipLaunchKernelGGL((k_quant_rows<ET, TT, G>), grid, block, 0, stream, x, ld, R, d, q, scale)
+  if (wave) {
+    if (g <= 1) NS_LAUNCH_QUANT(NS_WAVE, 1);
+    else if (g <= 2) NS_LAUNCH_QUANT(NS_WAVE, 2);
+    else if (g <= 4) NS_LAUNCH_QUANT(NS_WAVE, 4);
+    else NS_LAUNCH_QUANT(NS_WAVE, 8);
+  } else {
+    if (g <= 1) NS_LAUNCH_QUANT(kQuantThreads, 1);
+    else if (g <= 2) NS_LAUNCH_QUANT(kQuantThreads, 2);
+    else if (g <= 4) NS_LAUNCH_QUANT(kQuantThreads, 4);
+    else NS_LAUNCH_QUANT(kQuantThreads, 8);
+  }
+#undef NS_LAUNCH_QUANT
+  return ns_launch_status();
 }
 
 int quant_rows(const void* x, int64_t ld, int R, int d, int dtype, int8_t* q, float* scale, hipStream_t stream) {
-  const dim3 grid((unsigned)R), block(256);
-  if (dtype == NS_BF16) hipLaunchKernelGGL(k_quant_rows<NS_BF16>, grid, block, 0, stream, x, ld, d, q, scale);
-  else if (dtype == NS_FP16) hipLaunchKernelGGL(k_quant_rows<NS_FP16>, grid, block, 0, stream, x, ld, d, q, scale);
-  else hipLaunchKernelGGL(k_quant_rows<NS_FP32>, grid, block, 0, stream, x, ld, d, q, scale);
-  return ns_launch_status();
+  if (dtype == NS_BF16) return quant_rows_of<NS_BF16>(x, ld, R, d, q, scale, stream);
+  if (dtype == NS_FP16) return quant_rows_of<NS_FP16>(x, ld, R, d, q, scale, stream);
+  return quant_rows_of<NS_FP32>(x, ld, R, d, q, scale, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -170,9 +294,6 @@ __global__ __launch_bounds__(256) void k_product(Product p) {
     }
   }
 }
-
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 constexpr int kStageK = 128;                       // bytes of a row in a stage
 

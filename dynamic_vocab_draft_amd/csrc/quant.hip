@@ -44,7 +44,7 @@ struct Eight {
     constexpr int N = ET == NS_FP32 ? 2 : 1;
     if (i + 8 <= d) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) v[n] = *(const u32x4_any*)(row + (size_t)i * (2 * N) + n * 16);
+      for (int n = 0; n < N; ++n) v[n] = __builtin_nontemporal_load((const u32x4_any*)(row + (size_t)i * (2 * N) + n * 16));
     } else {
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -251,50 +251,6 @@ struct Product {
   int64_t ld_out;
 };
 
-// A wave owns 16 channel rows (the A operand: lane (i, g) holds bytes
-// 16 g .. 16 g + 15 of row i) and 64 token rows (four B operands); lane
-// (i, g) of a result holds channels 4 g .. 4 g + 3 of token i.
-template <int OT>
-__global__ __launch_bounds__(256) void k_product(Product p) {
-  const int b = blockIdx.z, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  int n = p.n_dev ? p.n_dev[b] : p.N;
-  n = n < 0 ? 0 : (n > p.N ? p.N : n);
-  const int j0 = (int)blockIdx.x * 64 + (int)(threadIdx.x >> 6) * 16;
-  if (j0 >= n) return;
-  const int32_t* ids = p.ids ? p.ids + (size_t)b * p.N : nullptr;
-  const int j = j0 + i < n ? j0 + i : j0;
-  int gid = ids ? ids[j] : j;
-  gid = gid < 0 || gid >= p.V ? 0 : gid;
-  const int8_t* wr = p.w + (size_t)gid * p.pitch + g * 16;
-  const int m0 = (int)blockIdx.y * 64;
-  const int8_t* xr[4];
-  for (int t = 0; t < 4; ++t) {
-    int m = m0 + t * 16 + i;
-    m = m < p.M ? m : p.M - 1;
-    xr[t] = p.x + ((size_t)b * p.M + m) * p.pitch + g * 16;
-  }
-  i32x4 acc[4] = {};
-  for (int k = 0; k < p.pitch; k += 64) {
-    const i32x4 a = *(const i32x4*)(wr + k);
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, *(const i32x4*)(xr[t] + k), acc[t], 0, 0, 0);
-  }
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int m = m0 + t * 16 + i;
-    if (m >= p.M) continue;
-    const float xs = p.xs[(size_t)b * p.M + m];
-    for (int c = 0; c < 4; ++c) {
-      const int jj = j0 + g * 4 + c;
-      if (jj >= n) continue;
-      const int id = ids ? ids[jj] : jj;
-      if (id < 0 || id >= p.V) continue;
-      store_out<OT>(p.out, ((size_t)b * p.M + m) * (size_t)p.ld_out + jj, scaled(acc[t][c], xs * p.ws[id]));
-    }
-  }
-}
-
 constexpr int kStageK = 128;                       // bytes of a row in a stage
 
 // 16 bytes a lane from a buffer straight into LDS at byte `lds` (the same
@@ -397,8 +353,12 @@ __device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8;
 
-template <int OT, int NMT, int RT, int R>
-__global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Product p, int units, int per_block) {
+// With IDS the channel rows are those that ids names (n_dev of them), the
+// block's share of ids waiting in LDS, and blockIdx.y is the sequence.
+constexpr int kStreamIds = 4096;                     // ids of a block, at most
+
+template <int OT, int NMT, int RT, int R, bool IDS>
+__global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Product p) {
   constexpr int WROWS = RT * 16, PROWS = kStreamWaves * WROWS;
   constexpr int XOFF = PROWS * kStageK, SOFF = XOFF + NMT * 16 * kStageK;
   constexpr int STAGE = SOFF + kStreamWaves * 256;   // channel rows, token rows, channel scales
@@ -406,6 +366,17 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
   constexpr int STORES = RT * NMT * 4;
   static_assert((R - 2) * LW + STORES < 64, "vmcnt range");
   __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
+  __shared__ int s_id[IDS ? kStreamIds : 1];
+  int live = p.N;
+  if (IDS) {
+    const size_t seq = blockIdx.y;
+    if (p.n_dev) live = p.n_dev[seq] < 0 ? 0 : (p.n_dev[seq] < p.N ? p.n_dev[seq] : p.N);
+    p.x += seq * p.M * p.pitch;
+    p.xs += seq * p.M;
+    if (p.ids) p.ids += seq * p.N;
+    p.out = (char*)p.out + seq * p.M * (size_t)p.ld_out * (OT == NS_FP32 ? 4 : 2);
+  }
+  const int units = (live + 15) / 16, per_block = (units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
   const int passes = (u1 - u0 + kStreamWaves * RT - 1) / (kStreamWaves * RT);
   if (passes <= 0) return;
@@ -413,10 +384,18 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
   const int S = p.pitch / kStageK;
   const uint32_t base = lds_offset(lds);
   const int n0 = u0 * 16;                            // the block's first channel row
-  const int last = (u1 * 16 < p.N ? u1 * 16 : p.N) - 1 - n0;
-  const u32x4 rw = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(last + 1) * p.pitch);
+  const int last = (u1 * 16 < live ? u1 * 16 : live) - 1 - n0;
+  const u32x4 rw = IDS ? buffer_of(p.w, (uint32_t)p.V * p.pitch)
+                       : buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(last + 1) * p.pitch);
   const u32x4 rx = buffer_of(p.x, (uint32_t)(p.M * p.pitch));
-  const u32x4 rs = buffer_of(p.ws + n0, (uint32_t)(last + 1) * 4);
+  const u32x4 rs = IDS ? buffer_of(p.ws, (uint32_t)p.V * 4) : buffer_of(p.ws + n0, (uint32_t)(last + 1) * 4);
+  if (IDS) {                                         // a hole reads row 0; nobody reads its output
+    for (int r = tid; r <= last; r += kStreamWaves * NS_WAVE) {
+      const int id = p.ids ? p.ids[n0 + r] : n0 + r;
+      s_id[r] = id < 0 || id >= p.V ? 0 : id;
+    }
+    __syncthreads();
+  }
   // token rows past the end read the last one and are not stored
   uint32_t xo[NMT == 4 ? 1 : NMT];
   if (NMT == 4) {
@@ -431,31 +410,40 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
   }
   // The stream of loads: the lk-th stage of pass lp comes next, bytes ks of the rows, into place lb.
   int lp = 0, lk = 0, lb = 0, ks = (int)(blockIdx.x * 5u) % S * kStageK;
+  uint32_t wo[2 * RT], so;                           // of the pass
+  const auto aim = [&]() {
+    const int r0 = (lp * kStreamWaves + w) * WROWS;
+    const auto row = [&](int r) {
+      r = r < last ? r : last;
+      return (uint32_t)(IDS ? s_id[r] : r);
+    };
+#pragma unroll
+    for (int v = 0; v < 2 * RT; ++v)
+      wo[v] = __umul24(row(r0 + v * 8 + (lane >> 3)), p.pitch) + ((lane & 7) ^ (lane >> 3)) * 16;
+    so = row(r0 + (lane & (WROWS - 1))) * 4;
+  };
   const auto issue = [&]() {
     const uint32_t to = base + lb * STAGE;
 #pragma unroll
-    for (int v = 0; v < 2 * RT; ++v) {
-      const int r = (lp * kStreamWaves + w) * WROWS + v * 8 + (lane >> 3);
-      load_to_lds_once(rw, __umul24(r < last ? r : last, p.pitch) + ((lane & 7) ^ (lane >> 3)) * 16, ks,
-                       to + (w * 2 * RT + v) * 1024);
-    }
+    for (int v = 0; v < 2 * RT; ++v) load_to_lds_once(rw, wo[v], ks, to + (w * 2 * RT + v) * 1024);
     if (NMT == 4) {
       load_to_lds(rx, xo[0], ks, to + XOFF + w * 1024);
     } else {
 #pragma unroll
       for (int v = 0; v < NMT; ++v) load_word_to_lds(rx, xo[v], ks, to + XOFF + (v * 8 + w) * 256);
     }
-    if (lk == 0) {
-      const int r = (lp * kStreamWaves + w) * WROWS + (lane & (WROWS - 1));
-      load_word_to_lds(rs, (uint32_t)(r < last ? r : last) * 4, 0, to + SOFF + w * 256);
-    }
+    if (lk == 0) load_word_to_lds(rs, so, 0, to + SOFF + w * 256);
     lb = lb + 1 == R ? 0 : lb + 1;
     ks = ks + kStageK == p.pitch ? 0 : ks + kStageK;
     if (++lk == S) {                                 // behind the last pass the stream reads that pass again,
       lk = 0;                                        // which spares every load a question
-      if (lp + 1 < passes) ++lp;
+      if (lp + 1 < passes) {
+        ++lp;
+        aim();
+      }
     }
   };
+  aim();
   float xs[NMT][4];
 #pragma unroll
   for (int u = 0; u < NMT; ++u)
@@ -717,6 +705,72 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
   wait_loads<0>();                                 // the stream's last loads end before their LDS is given back
 }
 
+// ---------------------------------------------------------------------------
+// The product for few channel rows and up to 64 token rows: bound by latency.
+// A block of eight waves owns 16 channel rows and all token rows; each wave
+// takes an eighth of the row's bytes, asks for all of its operands at once
+// and multiplies; the eight sums are joined in LDS.  One block pulls 64 KB of
+// a 4096-byte row set in about a microsecond, and 63 blocks of a thousand
+// rows end together.
+// ---------------------------------------------------------------------------
+template <int OT, int NMT>
+__global__ __launch_bounds__(512) void k_product_few(Product p) {
+  constexpr int BATCH = NMT == 1 ? 8 : 4;            // operands of a row in flight
+  __shared__ i32x4 sh[8][NMT][NS_WAVE];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const size_t seq = blockIdx.y;
+  int n = p.n_dev ? p.n_dev[seq] : p.N;
+  n = n < p.N ? n : p.N;
+  const int j0 = (int)blockIdx.x * 16;
+  if (j0 >= n) return;
+  const int j = j0 + i < n ? j0 + i : n - 1;
+  int id = p.ids ? p.ids[seq * p.N + j] : j;
+  id = id < 0 || id >= p.V ? 0 : id;                 // a hole reads row 0; nobody reads its output
+  const int steps = p.pitch / 64, per = (steps + 7) / 8;
+  const int k0 = w * per, k1 = k0 + per < steps ? k0 + per : steps;
+  const int8_t* wr = p.w + (size_t)id * p.pitch + g * 16;
+  const int8_t* xr[NMT];
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) {
+    const int m = u * 16 + i < p.M ? u * 16 + i : p.M - 1;
+    xr[u] = p.x + (seq * p.M + m) * p.pitch + g * 16;
+  }
+  i32x4 acc[NMT] = {};
+  for (int k = k0; k < k1; k += BATCH) {
+    i32x4 a[BATCH], b[BATCH][NMT];
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q) {
+      const int at = (k + q < k1 ? k + q : k0) * 64;
+      a[q] = *(const i32x4*)(wr + at);
+#pragma unroll
+      for (int u = 0; u < NMT; ++u) b[q][u] = *(const i32x4*)(xr[u] + at);
+    }
+    NS_ISSUE_FENCE();
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q)
+      if (k + q < k1) {                              // uniform over the wave
+#pragma unroll
+        for (int u = 0; u < NMT; ++u) acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[q][u], a[q], acc[u], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) sh[w][u][lane] = acc[u];
+  const float ws = p.ws[id];
+  __syncthreads();
+  // wave w joins token operands w, w + 8 ..; lane (i, g) holds tokens 4 g .. 4 g + 3 of channel i
+  for (int u = w; u < NMT; u += 8) {
+    i32x4 s = sh[0][u][lane];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += sh[q][u][lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = u * 16 + g * 4 + r;
+      if (m < p.M && j0 + i < n)
+        store_out<OT>(p.out, (seq * p.M + m) * (size_t)p.ld_out + j0 + i, scaled(s[r], p.xs[seq * p.M + m] * ws));
+    }
+  }
+}
+
 template <int OT, int TB>
 void launch_tiled(const Product& p, hipStream_t stream) {
   const int tm = (p.M + TB * 64 - 1) / (TB * 64), tn = (p.N + kTileN - 1) / kTileN;
@@ -729,26 +783,51 @@ void launch_tiled(const Product& p, hipStream_t stream) {
 template <int OT, int NMT, int RT, int R>
 void launch_stream(const Product& p, hipStream_t stream) {
   const int units = (p.N + 15) / 16, per = (units + 255) / 256;
-  hipLaunchKernelGGL((k_product_stream<OT, NMT, RT, R>), dim3((unsigned)((units + per - 1) / per)),
-                     dim3(kStreamWaves * NS_WAVE), 0, stream, p, units, per);
+  hipLaunchKernelGGL((k_product_stream<OT, NMT, RT, R, false>), dim3((unsigned)((units + per - 1) / per)),
+                     dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
 template <int OT>
-void launch_product(const Product& p, int B, hipStream_t stream) {
-  if (p.M <= 64 && !p.ids && (uint64_t)p.M * (uint64_t)p.ld_out * (OT == NS_FP32 ? 4 : 2) < 0x7FFFFFFFull) {
+void launch_product(const Product& p, hipStream_t stream) {
+  if (p.M <= 64 && (uint64_t)p.M * (uint64_t)p.ld_out * (OT == NS_FP32 ? 4 : 2) < 0x7FFFFFFFull) {
     if (p.M <= 16) launch_stream<OT, 1, 1, 7>(p, stream);
     else if (p.M <= 32) launch_stream<OT, 2, 1, 7>(p, stream);
     else if (p.M <= 48) launch_stream<OT, 3, 2, 3>(p, stream);
     else launch_stream<OT, 4, 2, 3>(p, stream);
+  } else if (p.M > 128) {
+    launch_tiled<OT, 4>(p, stream);
+  } else {
+    launch_tiled<OT, 2>(p, stream);
+  }
+}
+
+template <int NMT, int RT, int R>
+void launch_head_of(const Product& p, int B, bool few, hipStream_t stream) {
+  if (few) {
+    hipLaunchKernelGGL((k_product_few<NS_FP32, NMT>), dim3((unsigned)((p.N + 15) / 16), (unsigned)B), dim3(512), 0,
+                       stream, p);
     return;
   }
-  if (p.M > 64) {
-    if (p.M > 128) launch_tiled<OT, 4>(p, stream);
-    else launch_tiled<OT, 2>(p, stream);
-    return;
-  }
-  const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 63) / 64), (unsigned)B);
-  hipLaunchKernelGGL(k_product<OT>, grid, dim3(256), 0, stream, p);
+  // one block a CU over all sequences, none with more ids than it holds
+  const int units = (p.N + 15) / 16, least = (units * 16 + kStreamIds - 1) / kStreamIds;
+  int gx = B < 256 ? 256 / B : 1;
+  gx = gx > units ? units : (gx < least ? least : gx);
+  hipLaunchKernelGGL((k_product_stream<NS_FP32, NMT, RT, R, true>), dim3((unsigned)gx, (unsigned)B),
+                     dim3(kStreamWaves * NS_WAVE), 0, stream, p);
+}
+
+// The head's logits, B sequences.  Below 16384 rows the kernel for few rows is
+// the faster (whole calls: M = 32, 4000 rows 17.9 against 23.2 us; M = 64, 8000
+// rows 36.4 against 37.1; 8 sequences of 1000 of 2048 rows, M = 8, 18.0 against
+// 20.2), from there on the stream (M = 16, 15500 rows 27.3 against 32.7 us; M =
+// 64 39.6 against 55.3; 32 sequences of 1000 of 2048, M = 8, 30.7 against
+// 41.9).  The stream's 32-bit row addresses reach 4 GB.
+void launch_head(const Product& p, int B, hipStream_t stream) {
+  const bool few = (int64_t)B * p.N < 16384 || (uint64_t)p.V * (uint64_t)p.pitch > 0xFFFFFFFFull;
+  if (p.M <= 16) launch_head_of<1, 1, 6>(p, B, few, stream);
+  else if (p.M <= 32) launch_head_of<2, 1, 6>(p, B, few, stream);
+  else if (p.M <= 48) launch_head_of<3, 2, 3>(p, B, few, stream);
+  else launch_head_of<4, 2, 3>(p, B, few, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -890,9 +969,9 @@ int nanospec_quant_matmul(const int8_t* xq, const float* xs, int32_t M, const in
   if (((uintptr_t)out) % (out_dtype == NS_FP32 ? 4 : 2)) return NS_EINVAL;
   (void)hipGetLastError();
   const Product p{xq, xs, wq, ws, nullptr, nullptr, M, N, N, pitch_of(d), out, ld_out};
-  if (out_dtype == NS_FP32) launch_product<NS_FP32>(p, 1, stream);
-  else if (out_dtype == NS_BF16) launch_product<NS_BF16>(p, 1, stream);
-  else launch_product<NS_FP16>(p, 1, stream);
+  if (out_dtype == NS_FP32) launch_product<NS_FP32>(p, stream);
+  else if (out_dtype == NS_BF16) launch_product<NS_BF16>(p, stream);
+  else launch_product<NS_FP16>(p, stream);
   return ns_launch_status();
 }
 
@@ -917,7 +996,8 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   float* z = (float*)(base + l.z);
   int rc = quant_rows(h, d, B * M, d, dtype, hq, hs, stream);
   if (rc != NS_OK) return rc;
-  launch_product<NS_FP32>(Product{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld}, B, stream);
+  const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld};
+  launch_head(p, B, stream);
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;
   const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};

@@ -357,12 +357,12 @@ constexpr int kStreamWaves = 8;
 // block's share of ids waiting in LDS, and blockIdx.y is the sequence.
 constexpr int kStreamIds = 4096;                     // ids of a block, at most
 
-template <int OT, int NMT, int RT, int R, bool IDS>
+template <int OT, int NMT, int ROWS, int R, bool IDS>
 __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Product p) {
-  constexpr int WROWS = RT * 16, PROWS = kStreamWaves * WROWS;
+  constexpr int RT = ROWS > 16 ? ROWS / 16 : 1, PROWS = kStreamWaves * ROWS, LR = ROWS / 8;
   constexpr int XOFF = PROWS * kStageK, SOFF = XOFF + NMT * 16 * kStageK;
   constexpr int STAGE = SOFF + kStreamWaves * 256;   // channel rows, token rows, channel scales
-  constexpr int LW = 2 * RT + (NMT == 4 ? 1 : NMT);  // loads of a wave and stage
+  constexpr int LW = LR + (NMT == 4 ? 1 : NMT);  // loads of a wave and stage
   constexpr int STORES = RT * NMT * 4;
   static_assert((R - 2) * LW + STORES < 64, "vmcnt range");
   __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
@@ -376,19 +376,27 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     if (p.ids) p.ids += seq * p.N;
     p.out = (char*)p.out + seq * p.M * (size_t)p.ld_out * (OT == NS_FP32 ? 4 : 2);
   }
-  const int units = (live + 15) / 16, per_block = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int units = (live + ROWS - 1) / ROWS, per_block = (units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
-  const int passes = (u1 - u0 + kStreamWaves * RT - 1) / (kStreamWaves * RT);
+  const int passes = (u1 - u0 + kStreamWaves - 1) / kStreamWaves;
   if (passes <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
   const int S = p.pitch / kStageK;
   const uint32_t base = lds_offset(lds);
-  const int n0 = u0 * 16;                            // the block's first channel row
-  const int last = (u1 * 16 < live ? u1 * 16 : live) - 1 - n0;
+  const int n0 = u0 * ROWS;                            // the block's first channel row
+  const int last = (u1 * ROWS < live ? u1 * ROWS : live) - 1 - n0;
   const u32x4 rw = IDS ? buffer_of(p.w, (uint32_t)p.V * p.pitch)
                        : buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(last + 1) * p.pitch);
   const u32x4 rx = buffer_of(p.x, (uint32_t)(p.M * p.pitch));
   const u32x4 rs = IDS ? buffer_of(p.ws, (uint32_t)p.V * 4) : buffer_of(p.ws + n0, (uint32_t)(last + 1) * 4);
+  float xs[NMT][4];
+#pragma unroll
+  for (int u = 0; u < NMT; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = u * 16 + g * 4 + r;
+      xs[u][r] = p.xs[m < p.M ? m : p.M - 1];
+    }
   if (IDS) {                                         // a hole reads row 0; nobody reads its output
     for (int r = tid; r <= last; r += kStreamWaves * NS_WAVE) {
       const int id = p.ids ? p.ids[n0 + r] : n0 + r;
@@ -410,22 +418,22 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
   }
   // The stream of loads: the lk-th stage of pass lp comes next, bytes ks of the rows, into place lb.
   int lp = 0, lk = 0, lb = 0, ks = (int)(blockIdx.x * 5u) % S * kStageK;
-  uint32_t wo[2 * RT], so;                           // of the pass
+  uint32_t wo[LR], so;                           // of the pass
   const auto aim = [&]() {
-    const int r0 = (lp * kStreamWaves + w) * WROWS;
+    const int r0 = (lp * kStreamWaves + w) * ROWS;
     const auto row = [&](int r) {
       r = r < last ? r : last;
       return (uint32_t)(IDS ? s_id[r] : r);
     };
 #pragma unroll
-    for (int v = 0; v < 2 * RT; ++v)
+    for (int v = 0; v < LR; ++v)
       wo[v] = __umul24(row(r0 + v * 8 + (lane >> 3)), p.pitch) + ((lane & 7) ^ (lane >> 3)) * 16;
-    so = row(r0 + (lane & (WROWS - 1))) * 4;
+    so = row(r0 + (lane & (ROWS - 1))) * 4;
   };
   const auto issue = [&]() {
     const uint32_t to = base + lb * STAGE;
 #pragma unroll
-    for (int v = 0; v < 2 * RT; ++v) load_to_lds_once(rw, wo[v], ks, to + (w * 2 * RT + v) * 1024);
+    for (int v = 0; v < LR; ++v) load_to_lds_once(rw, wo[v], ks, to + (w * LR + v) * 1024);
     if (NMT == 4) {
       load_to_lds(rx, xo[0], ks, to + XOFF + w * 1024);
     } else {
@@ -444,14 +452,6 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     }
   };
   aim();
-  float xs[NMT][4];
-#pragma unroll
-  for (int u = 0; u < NMT; ++u)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int m = u * 16 + g * 4 + r;
-      xs[u][r] = p.xs[m < p.M ? m : p.M - 1];
-    }
   const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(p.out, 0, 0x7FFFFFFF, 0x00027000);
   constexpr int ESZ = OT == NS_FP32 ? 4 : 2;
   i32x4 acc[RT][NMT] = {};
@@ -463,7 +463,8 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
 #pragma unroll
   for (int v = 0; v < R - 1; ++v) issue();
   const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
-  const char* lw = lds + (w * WROWS + i) * kStageK;
+  const int ir = ROWS < 16 ? i & (ROWS - 1) : i;     // with 8 rows the operand's upper half repeats the lower
+  const char* lw = lds + (w * ROWS + ir) * kStageK;
   const char* lx = lds + XOFF + i * kStageK;
   int b = 0, since = R;                              // stages since the last stores
   float ws[RT] = {};
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
       const char* xt = lx + b * STAGE;
       if (s == 0) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) ws[t] = *(const float*)(lds + b * STAGE + SOFF + w * 256 + (t * 16 + i) * 4);
+        for (int t = 0; t < RT; ++t) ws[t] = *(const float*)(lds + b * STAGE + SOFF + w * 256 + (t * 16 + ir) * 4);
       }
       i32x4 f[RT][2];
 #pragma unroll
@@ -504,7 +505,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int j = (pass * kStreamWaves + w) * WROWS + t * 16 + i;
+      const int j = (pass * kStreamWaves + w) * ROWS + t * 16 + i;
 #pragma unroll
       for (int u = 0; u < NMT; ++u)
 #pragma unroll
@@ -512,7 +513,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
           const int m = u * 16 + g * 4 + r;
           const float v = scaled(acc[t][u][r], xs[u][r] * ws[t]);
           const uint32_t at =
-              m < p.M && j <= last ? (uint32_t)(((size_t)m * (size_t)p.ld_out + n0 + j) * ESZ) : 0x80000000u;
+              m < p.M && j <= last && (ROWS >= 16 || i < ROWS) ? (uint32_t)(((size_t)m * (size_t)p.ld_out + n0 + j) * ESZ) : 0x80000000u;
           if (OT == NS_FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
           else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)narrow2<OT>(v, 0.f), ro, at, 0, 0);
           acc[t][u][r] = 0;
@@ -719,13 +720,24 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
   __shared__ i32x4 sh[8][NMT][NS_WAVE];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
   const size_t seq = blockIdx.y;
+  const int j0 = (int)blockIdx.x * 16, j = j0 + i < p.N ? j0 + i : p.N - 1;
+  // the count, the ids and the scales are asked for together; an id behind
+  // the count or a hole reads some row, and nobody reads its output
   int n = p.n_dev ? p.n_dev[seq] : p.N;
-  n = n < p.N ? n : p.N;
-  const int j0 = (int)blockIdx.x * 16;
-  if (j0 >= n) return;
-  const int j = j0 + i < n ? j0 + i : n - 1;
   int id = p.ids ? p.ids[seq * p.N + j] : j;
-  id = id < 0 || id >= p.V ? 0 : id;                 // a hole reads row 0; nobody reads its output
+  float xs[NMT][4];
+#pragma unroll
+  for (int u = 0; u < NMT; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = u * 16 + g * 4 + r;
+      xs[u][r] = p.xs[seq * p.M + (m < p.M ? m : p.M - 1)];
+    }
+  NS_ISSUE_FENCE();
+  n = n < p.N ? n : p.N;
+  if (j0 >= n) return;
+  id = id < 0 || id >= p.V ? 0 : id;
+  const float ws = p.ws[id];
   const int steps = p.pitch / 64, per = (steps + 7) / 8;
   const int k0 = w * per, k1 = k0 + per < steps ? k0 + per : steps;
   const int8_t* wr = p.w + (size_t)id * p.pitch + g * 16;
@@ -755,10 +767,11 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
   }
 #pragma unroll
   for (int u = 0; u < NMT; ++u) sh[w][u][lane] = acc[u];
-  const float ws = p.ws[id];
   __syncthreads();
-  // wave w joins token operands w, w + 8 ..; lane (i, g) holds tokens 4 g .. 4 g + 3 of channel i
-  for (int u = w; u < NMT; u += 8) {
+  // wave u joins token operand u; lane (i, g) holds tokens 4 g .. 4 g + 3 of channel i
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) {
+    if (u != w) continue;
     i32x4 s = sh[0][u][lane];
 #pragma unroll
     for (int q = 1; q < 8; ++q) s += sh[q][u][lane];
@@ -766,7 +779,7 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
     for (int r = 0; r < 4; ++r) {
       const int m = u * 16 + g * 4 + r;
       if (m < p.M && j0 + i < n)
-        store_out<OT>(p.out, (seq * p.M + m) * (size_t)p.ld_out + j0 + i, scaled(s[r], p.xs[seq * p.M + m] * ws));
+        store_out<OT>(p.out, (seq * p.M + m) * (size_t)p.ld_out + j0 + i, scaled(s[r], xs[u][r] * ws));
     }
   }
 }
@@ -780,20 +793,20 @@ void launch_tiled(const Product& p, hipStream_t stream) {
                      tn);
 }
 
-template <int OT, int NMT, int RT, int R>
+template <int OT, int NMT, int ROWS, int R>
 void launch_stream(const Product& p, hipStream_t stream) {
-  const int units = (p.N + 15) / 16, per = (units + 255) / 256;
-  hipLaunchKernelGGL((k_product_stream<OT, NMT, RT, R, false>), dim3((unsigned)((units + per - 1) / per)),
+  const int units = (p.N + ROWS - 1) / ROWS, per = (units + 255) / 256;
+  hipLaunchKernelGGL((k_product_stream<OT, NMT, ROWS, R, false>), dim3((unsigned)((units + per - 1) / per)),
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
 template <int OT>
 void launch_product(const Product& p, hipStream_t stream) {
   if (p.M <= 64 && (uint64_t)p.M * (uint64_t)p.ld_out * (OT == NS_FP32 ? 4 : 2) < 0x7FFFFFFFull) {
-    if (p.M <= 16) launch_stream<OT, 1, 1, 7>(p, stream);
-    else if (p.M <= 32) launch_stream<OT, 2, 1, 7>(p, stream);
-    else if (p.M <= 48) launch_stream<OT, 3, 2, 3>(p, stream);
-    else launch_stream<OT, 4, 2, 3>(p, stream);
+    if (p.M <= 16) launch_stream<OT, 1, 16, 7>(p, stream);
+    else if (p.M <= 32) launch_stream<OT, 2, 16, 7>(p, stream);
+    else if (p.M <= 48) launch_stream<OT, 3, 32, 3>(p, stream);
+    else launch_stream<OT, 4, 32, 3>(p, stream);
   } else if (p.M > 128) {
     launch_tiled<OT, 4>(p, stream);
   } else {
@@ -801,40 +814,56 @@ void launch_product(const Product& p, hipStream_t stream) {
   }
 }
 
-template <int NMT, int RT, int R>
-void launch_head_of(const Product& p, int B, bool few, hipStream_t stream) {
-  if (few) {
-    hipLaunchKernelGGL((k_product_few<NS_FP32, NMT>), dim3((unsigned)((p.N + 15) / 16), (unsigned)B), dim3(512), 0,
-                       stream, p);
-    return;
-  }
+template <int NMT, int ROWS, int R>
+void launch_head_stream(const Product& p, int B, hipStream_t stream) {
   // one block a CU over all sequences, none with more ids than it holds
-  const int units = (p.N + 15) / 16, least = (units * 16 + kStreamIds - 1) / kStreamIds;
+  const int units = (p.N + ROWS - 1) / ROWS, least = (units * ROWS + kStreamIds - 1) / kStreamIds;
   int gx = B < 256 ? 256 / B : 1;
   gx = gx > units ? units : (gx < least ? least : gx);
-  hipLaunchKernelGGL((k_product_stream<NS_FP32, NMT, RT, R, true>), dim3((unsigned)gx, (unsigned)B),
+  hipLaunchKernelGGL((k_product_stream<NS_FP32, NMT, ROWS, R, true>), dim3((unsigned)gx, (unsigned)B),
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-// The head's logits, B sequences.  Below 16384 rows the kernel for few rows is
-// the faster (whole calls: M = 32, 4000 rows 17.9 against 23.2 us; M = 64, 8000
-// rows 36.4 against 37.1; 8 sequences of 1000 of 2048 rows, M = 8, 18.0 against
-// 20.2), from there on the stream (M = 16, 15500 rows 27.3 against 32.7 us; M =
-// 64 39.6 against 55.3; 32 sequences of 1000 of 2048, M = 8, 30.7 against
-// 41.9).  The stream's 32-bit row addresses reach 4 GB.
+template <int NMT>
+void launch_head_few(const Product& p, int B, hipStream_t stream) {
+  hipLaunchKernelGGL((k_product_few<NS_FP32, NMT>), dim3((unsigned)((p.N + 15) / 16), (unsigned)B), dim3(512), 0,
+                     stream, p);
+}
+
+// The head's logits, B sequences.  Whole calls, the kernel for few rows
+// against the stream of eight-row units: M = 8, 1000 rows 13.4 against 18.2 us;
+// M = 64, 4000 rows 23.0 against 26.4, 8000 rows 36.5 against 31.4, 15500 rows
+// 54.1 against 33.0; 32 sequences of 1000 of 2048 rows, M = 8, 42.2 against
+// 30.3.  Taller units, with fewer barriers, pay once a CU has several passes
+// of eight-row ones (M = 8, 100000 rows 81.4 against 83.7 us; 15500 rows, M =
+// 64, 39.3 against 33.0).  The stream's 32-bit row addresses reach 4 GB.
 void launch_head(const Product& p, int B, hipStream_t stream) {
-  const bool few = (int64_t)B * p.N < 16384 || (uint64_t)p.V * (uint64_t)p.pitch > 0xFFFFFFFFull;
-  if (p.M <= 16) launch_head_of<1, 1, 6>(p, B, few, stream);
-  else if (p.M <= 32) launch_head_of<2, 1, 6>(p, B, few, stream);
-  else if (p.M <= 48) launch_head_of<3, 2, 3>(p, B, few, stream);
-  else launch_head_of<4, 2, 3>(p, B, few, stream);
+  const int64_t rows = (int64_t)B * p.N;
+  if (rows < 8192 || (uint64_t)p.V * (uint64_t)p.pitch > 0xFFFFFFFFull) {
+    if (p.M <= 16) launch_head_few<1>(p, B, stream);
+    else if (p.M <= 32) launch_head_few<2>(p, B, stream);
+    else if (p.M <= 48) launch_head_few<3>(p, B, stream);
+    else launch_head_few<4>(p, B, stream);
+  } else if (rows <= 65536) {
+    if (p.M <= 16) launch_head_stream<1, 8, 7>(p, B, stream);
+    else if (p.M <= 32) launch_head_stream<2, 8, 7>(p, B, stream);
+    else if (p.M <= 48) launch_head_stream<3, 8, 7>(p, B, stream);
+    else launch_head_stream<4, 8, 7>(p, B, stream);
+  } else {
+    if (p.M <= 16) launch_head_stream<1, 16, 6>(p, B, stream);
+    else if (p.M <= 32) launch_head_stream<2, 16, 6>(p, B, stream);
+    else if (p.M <= 48) launch_head_stream<3, 32, 3>(p, B, stream);
+    else launch_head_stream<4, 32, 3>(p, B, stream);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Top-k over the scaled logits of each hidden row
 // ---------------------------------------------------------------------------
-constexpr int kTopCols = 4;
-constexpr int kTopChunk = kSelectThreads * kTopCols;
+// Columns of a thread: 4 cover 4096 columns in one block; 16, for more, cover
+// 16384 (64 x 15500: 11.5 us in chunks of 4096 with a join, TOP16 us in one).
+constexpr int top_cols(int n_max) { return n_max <= 4 * kSelectThreads ? 4 : 16; }
+constexpr int top_chunk(int n_max) { return kSelectThreads * top_cols(n_max); }
 
 struct Top {
   const float* z;           // [B][M] rows, ld floats apart
@@ -854,40 +883,52 @@ __device__ __forceinline__ void put_top(const Top& t, size_t row, int r, uint64_
 }
 
 // Block (m, c, b): the k best of chunk c of hidden row m of sequence b.
+template <int U>
 __global__ __launch_bounds__(kSelectThreads) void k_top_chunk(Top t) {
+  constexpr int CHUNK = U * kSelectThreads;
   __shared__ SelectSmem sm;
   const int m = blockIdx.x, c = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  int n = t.n_dev ? t.n_dev[b] : t.n_max;
-  n = n < 0 ? 0 : (n > t.n_max ? t.n_max : n);
-  const bool final_here = n <= kTopChunk;
-  if (final_here && c > 0) return;
   const size_t row = (size_t)b * t.M + m;
-  const int j0 = c * kTopChunk;
-  float val[kTopCols];
-  int id[kTopCols];
+  const int j0 = c * CHUNK;
+  int n = t.n_dev ? t.n_dev[b] : t.n_max;
+  // Every column is asked for before the first is looked at; the first four of
+  // a thread together with the count, live or not.
+  float val[U];
+  int id[U];
+  const auto ask = [&](int u, int end) {
+    const int q = j0 + tid + u * kSelectThreads, j = q < end ? q : end - 1;
+    val[u] = t.z[row * (size_t)t.ld + j];
+    id[u] = t.ids ? t.ids[(size_t)b * t.n_max + j] : j;
+  };
 #pragma unroll
-  for (int u = 0; u < kTopCols; ++u) {
-    const int j = j0 + tid + u * kSelectThreads;
-    val[u] = 0.f;
-    id[u] = -1;
-    if (j < n) {
-      const int g = t.ids ? t.ids[(size_t)b * t.n_max + j] : j;
-      if (g >= 0 && g < t.V) {
-        const float v = t.z[row * (size_t)t.ld + j];
-        if (t.logits) t.logits[row * (size_t)t.n_max + j] = v;
-        if (v == v) {
-          val[u] = v;
-          id[u] = g;
-        }
-      }
+  for (int u = 0; u < 4; ++u) ask(u, t.n_max);
+  NS_ISSUE_FENCE();
+  n = n < 0 ? 0 : (n > t.n_max ? t.n_max : n);
+  const bool final_here = n <= CHUNK;
+  if (final_here && c > 0) return;
+  const int lim = n - j0 < CHUNK ? n - j0 : CHUNK;       // <= 0 where nothing is live
+  if (U > 4) {
+    const int end = n > 0 ? n : 1;
+#pragma unroll
+    for (int u = 4; u < U; ++u) ask(u, end);
+    NS_ISSUE_FENCE();
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int q = tid + u * kSelectThreads;
+    const bool live = q < lim && id[u] >= 0 && id[u] < t.V;
+    if (live && t.logits) t.logits[row * (size_t)t.n_max + j0 + q] = val[u];
+    if (!live || val[u] != val[u]) {                     // NaN is never selected
+      val[u] = 0.f;
+      id[u] = -1;
     }
   }
-  const int nlive = n > j0 ? (n - j0 < kTopChunk ? n - j0 : kTopChunk) : 0;
+  const int nlive = lim > 0 ? lim : 0;
   if (final_here)
-    block_select_topk<kTopCols>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { put_top(t, row, r, x); });
+    block_select_topk<U>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { put_top(t, row, r, x); });
   else {
     uint64_t* dst = t.cand + (row * gridDim.y + c) * (size_t)t.k;
-    block_select_topk<kTopCols>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { dst[r] = x; });
+    block_select_topk<U>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { dst[r] = x; });
   }
 }
 
@@ -898,7 +939,7 @@ __global__ __launch_bounds__(kSelectThreads) void k_top_keys(Top t, int nk) {
   const int m = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   int n = t.n_dev ? t.n_dev[b] : t.n_max;
   if (n > t.n_max) n = t.n_max;
-  if (n <= kTopChunk) return;
+  if (n <= top_chunk(t.n_max)) return;
   const size_t row = (size_t)b * t.M + m;
   float val[U];
   int id[U];
@@ -925,7 +966,7 @@ struct HeadWs {
 HeadWs head_ws(int B, int n_max, int M, int k, int d) {
   HeadWs w;
   w.ld = ((int64_t)n_max + 3) / 4 * 4;
-  w.chunks = (n_max + kTopChunk - 1) / kTopChunk;
+  w.chunks = (n_max + top_chunk(n_max) - 1) / top_chunk(n_max);
   const size_t rows = (size_t)B * M;
   w.q = 0;
   w.scale = w.q + align256(rows * pitch_of(d));
@@ -1001,8 +1042,9 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;
   const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};
-  hipLaunchKernelGGL(k_top_chunk, dim3((unsigned)M, (unsigned)l.chunks, (unsigned)B), dim3(kSelectThreads), 0, stream,
-                     t);
+  const dim3 chunks((unsigned)M, (unsigned)l.chunks, (unsigned)B);
+  if (top_cols(n_max) == 4) hipLaunchKernelGGL(k_top_chunk<4>, chunks, dim3(kSelectThreads), 0, stream, t);
+  else hipLaunchKernelGGL(k_top_chunk<16>, chunks, dim3(kSelectThreads), 0, stream, t);
   rc = ns_launch_status();
   if (rc != NS_OK || l.chunks == 1) return rc;
   const int nk = l.chunks * k;

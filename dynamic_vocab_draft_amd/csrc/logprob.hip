@@ -325,23 +325,33 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
   const int q1 = part + 1 == a.S ? nvec : (q0 + per < nvec ? q0 + per : nvec);
   Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
   Best best{sh + (TOP ? wv * kBuf : 0), 0, a.k, -INFINITY, true};
+  // Loads are never under a condition, so that the batch in flight behind them
+  // can be counted: past the end they read the part's last vector again, and
+  // `mask` puts -infinity in its place.
   const auto load = [&](int base, u32x4(&x)[kUnroll]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int q = base + u * NS_WAVE + lane;
-      if (q < q1) x[u] = __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)q * 16));
-      else x[u] = minus_inf<ET>();
+      x[u] = __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)(q < q1 ? q : q1 - 1) * 16));
     }
+  };
+  const auto mask = [&](int base, u32x4(&x)[kUnroll]) {
+    if (base + STEP <= q1) return;                         // uniform
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (base + u * NS_WAVE + lane >= q1) x[u] = minus_inf<ET>();
   };
   u32x4 x0[kUnroll], x1[kUnroll];
   if (q0 < q1) load(q0, x0);
   for (int base = q0; base < q1; base += 2 * STEP) {
     load(base + STEP, x1);
     NS_ISSUE_FENCE();
+    mask(base, x0);
     take<ET, TOP>(x0, base, q1, a.c, st, best, lane);
     if (base + STEP >= q1) break;                          // uniform
     load(base + 2 * STEP, x0);
     NS_ISSUE_FENCE();
+    mask(base + STEP, x1);
     take<ET, TOP>(x1, base + STEP, q1, a.c, st, best, lane);
   }
   if (part + 1 == a.S && a.V % EPV != 0) {                 // the last elements, fewer than a vector

@@ -11,7 +11,6 @@
 // and E moves by whole powers of two only, so rescaling S is exact.  All of it
 // is float32.
 #include "common.hpp"
-#include "select.hpp"
 
 namespace {
 
@@ -19,9 +18,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kUnroll = 4;               // 16-byte vectors per lane and batch
 constexpr int kRowWaves = 4;             // waves of a forward block
-constexpr int kMaxParts = 64;            // parts of a row, at most
+constexpr int kMaxParts = 64;            // parts of a row, at most; a power of two of them
 constexpr int kWavesWanted = 2048;       // waves that fill the chip: eight a CU
-constexpr int kBuf = 256;                // candidate keys of a wave
 constexpr float kWide = 1024.f;          // |c max z| from which y is taken relative to the maximum itself
 
 __host__ __device__ constexpr int elem_bytes(int ET) { return ET == NS_FP32 ? 4 : 2; }
@@ -74,12 +72,6 @@ __device__ __forceinline__ float next_up(float v) {
   return __uint_as_float(u & 0x80000000u ? u - 1 : u + 1);
 }
 
-// Orders a wave's own LDS writes before its following reads.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Statistics of a part of a row: y = c (z - ref) - E.
 struct Stat {
   float top, ref, E, S, W;
@@ -103,64 +95,132 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
   return r;
 }
 
+// Orders a wave's own LDS writes before its following reads.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
+}
+
 // ---------------------------------------------------------------------------
-// The best k keys of a wave.  Elements that may still count are appended to
-// an LDS buffer; when it has filled up, the k best are kept, sorted, and `lo`
-// becomes the smallest value that a later element needs.  Ids rise from batch
-// to batch, so a later element that only ties the k-th value loses to it.
+// The best k keys of a wave: lane r holds the r-th (0: none yet).  The
+// elements of a batch that reach the k-th value so far are collected in LDS,
+// then enter the list: a few one by one (a comparison's ballot is the rank,
+// the lanes behind it shift), more in one merge (every lane counts the keys
+// above its own two, which does not wait for each candidate in turn: eight
+// rows of 128256 float32 logits, k = 64, in 64 parts MERGE).  Ids rise from
+// batch to batch, so a later element that only ties the k-th value loses to it.
 // ---------------------------------------------------------------------------
 struct Best {
-  uint64_t* buf;
+  uint64_t* buf;       // NS_WAVE candidates
+  uint64_t key;        // this lane's
   int cnt, k;
-  float lo;        // elements below it cannot be among the k best
-  bool fresh;      // no bound yet
+  float least;         // elements below it cannot be among the k best
+  bool fresh;          // nothing seen yet
 
-  __device__ __forceinline__ void compact(int lane) {
-    wave_sync();
-    uint64_t mine[kBuf / NS_WAVE];
-    int rank[kBuf / NS_WAVE];
-#pragma unroll
-    for (int q = 0; q < kBuf / NS_WAVE; ++q) {
-      const int i = lane + q * NS_WAVE;
-      mine[q] = i < cnt ? buf[i] : 0;
-      rank[q] = 0;
-    }
-    for (int p = 0; p < cnt; ++p) {
-      const uint64_t o = buf[p];
-#pragma unroll
-      for (int q = 0; q < kBuf / NS_WAVE; ++q) rank[q] += o > mine[q];
-    }
-    wave_sync();
-#pragma unroll
-    for (int q = 0; q < kBuf / NS_WAVE; ++q)
-      if (mine[q] != 0 && rank[q] < k) buf[rank[q]] = mine[q];
-    wave_sync();
-    if (cnt >= k) {
-      cnt = k;
-      lo = next_up(ns::key_val(buf[k - 1]));
-    }
+  // c is the same in every lane
+  __device__ __forceinline__ void insert(uint64_t c, int lane) {
+    const int r = __popcll(__ballot(key > c));
+    if (r >= k) return;                                    // uniform
+    // wave_shr:1, the key of the lane before
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)key, 0x138, 0xf, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(key >> 32), 0x138, 0xf, 0xf, false);
+    const uint64_t before = ((uint64_t)hi << 32) | lo;
+    key = lane < r ? key : (lane == r ? c : before);
   }
 
-  __device__ __forceinline__ void add(float v, int id, bool live, float least, int lane) {
-    const bool pass = live && v >= least;
+  // Empties the collected candidates into the list.
+  __device__ __forceinline__ void enter(int lane) {
+    wave_sync();
+    const uint64_t c = lane < cnt ? buf[lane] : 0;
+    if (cnt <= 4) {                                        // uniform
+      for (int p = 0; p < cnt; ++p) insert(lane_u64(c, p), lane);
+    } else {
+      int rk = lane, rc = 0, above = 0;                    // ranks of key and c; list keys above c
+      for (int p = 0; p < cnt; p += 4)                     // those past cnt are 0, above nothing
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t o = lane_u64(c, p + e);
+          const unsigned long long more = __ballot(key > o);
+          rk += key < o;
+          rc += c < o;
+          above = lane == p + e ? __popcll(more) : above;
+        }
+      rc += above;
+      wave_sync();
+      buf[lane] = 0;
+      wave_sync();
+      if (key != 0 && rk < k) buf[rk] = key;
+      if (lane < cnt && rc < k) buf[rc] = c;
+      wave_sync();
+      key = buf[lane];
+    }
+    wave_sync();
+    cnt = 0;
+  }
+
+  // Collects one element of each lane that passes.
+  __device__ __forceinline__ void take(float v, bool pass, int id, int lane) {
     const unsigned long long ball = __ballot(pass);
-    if (!ball) return;
-    if (cnt + NS_WAVE > kBuf) compact(lane);
+    const int n = __popcll(ball);
+    if (cnt + n > NS_WAVE) enter(lane);                    // uniform
     if (pass) buf[cnt + __popcll(ball & ((1ull << lane) - 1))] = ns::make_key(v, id);
-    cnt += __popcll(ball);
+    cnt += n;
   }
 
-  // A bound before any key is held: the k-th largest of the lanes' maxima.
-  __device__ __forceinline__ void start(float lane_max, int lane) {
-    int gt = 0, ge = 0;
-    for (int q = 0; q < NS_WAVE; ++q) {
-      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lane_max), q));
-      gt += o > lane_max;
-      ge += o >= lane_max;
+  // Collects the elements of a lane's vector x, ids from `id`, that reach `least`.
+  template <int ET>
+  __device__ __forceinline__ void take_vector(u32x4 x, int id, bool live, int lane) {
+    constexpr int EPV = per_vec(ET);
+    float v[EPV];
+    widen<ET>(x, v);
+    uint32_t m = 0;                                        // bit EPV - 1 - e: element e passes
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) m = m + m + (v[e] >= least ? 1u : 0u);
+    m = live ? m : 0u;
+#pragma unroll 1
+    while (__ballot(m != 0)) {                             // one turn, as a rule
+      const int e = EPV - 1 - (__ffs(m) - 1) & (EPV - 1);  // of the lanes with any
+      const int word = ET == NS_FP32 ? e : e >> 1;
+      const uint32_t a = word & 1 ? x.y : x.x, b = word & 1 ? x.w : x.z, w = word & 2 ? b : a;
+      const float f = ET == NS_FP32 ? __uint_as_float(w) : elem_of<ET>(w >> (e & 1) * 16, 0);
+      take(f, m != 0, id + e, lane);
+      m &= m - 1;
     }
-    const unsigned long long ball = __ballot(gt < k && ge >= k);
-    lo = ball ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lane_max), __ffsll(ball) - 1)) : -INFINITY;
+  }
+
+  // The bound for the next batch.
+  __device__ __forceinline__ void raise() {
+    const uint32_t h = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), k - 1);
+    if (h != 0) least = next_up(ns::unord_f32(h));
+  }
+
+  // A bound before any key is held, from the lanes' maxima m: a value that at
+  // least k of them reach, by bisection of the ordered bits.  16 halvings come
+  // close to the k-th largest; the exact one would save next to nothing.
+  __device__ __forceinline__ void start(float m, int lane) {
     fresh = false;
+    const uint32_t o = m == m ? ns::ord_f32(m) : 0u;       // NaN: no bound
+    uint32_t lo = 0, hi = 0xFFFFFFFFu;                     // k lanes reach lo, fewer than k reach hi
+    {
+      const uint32_t top = (uint32_t)__builtin_amdgcn_readfirstlane((int)ns::ord_f32(ns::wave_max_f32(m)));
+      hi = top + 1;
+      // most maxima lie within a factor of four of the largest: begin there if k do
+      const uint32_t near = top > (2u << 23) ? top - (2u << 23) : 0u;
+      if (__popcll(__ballot(o >= near)) >= k) lo = near;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      if (__popcll(__ballot(o >= mid)) >= k) lo = mid;
+      else hi = mid;
+    }
+    if (lo >= 0x00800000u) least = ns::unord_f32(lo);      // the least finite value; below it -infinity does
   }
 };
 
@@ -291,18 +351,15 @@ __device__ __forceinline__ void take(const u32x4 (&x)[kUnroll], int q0, int q1, 
   st.W += W;
   if (TOP) {
     if (best.fresh) best.start(lane_max, lane);
-    if (top >= best.lo) {                                  // uniform
-      const float least = best.lo;
+    if (top >= best.least) {                               // uniform
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        if (!__ballot(mx[u] >= least)) continue;
+        if (!__ballot(mx[u] >= best.least)) continue;
         const int q = q0 + u * NS_WAVE + lane;
-        float v[EPV];
-        widen<ET>(x[u], v);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) best.add(v[e], q * EPV + e, q < q1, least, lane);
+        best.take_vector<ET>(x[u], q * EPV, q < q1, lane);
       }
-      if (best.cnt >= best.k + NS_WAVE / 2) best.compact(lane);
+      best.enter(lane);
+      best.raise();
     }
   }
 }
@@ -312,7 +369,7 @@ __device__ __forceinline__ void take(const u32x4 (&x)[kUnroll], int q0, int q1, 
 template <int ET, bool TOP>
 __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
   constexpr int EPV = per_vec(ET), STEP = NS_WAVE * kUnroll;
-  __shared__ uint64_t sh[TOP ? kRowWaves * kBuf : 1];
+  __shared__ uint64_t sh[TOP ? kRowWaves : 1][NS_WAVE];
   const int lane = threadIdx.x & (NS_WAVE - 1), wv = threadIdx.x / NS_WAVE;
   const int64_t item = (int64_t)blockIdx.x * kRowWaves + wv;
   const size_t row = (size_t)(item / a.S);
@@ -320,11 +377,9 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
   if (row >= (size_t)a.L) return;                          // wave-uniform; no block barrier below
   const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
   const int nvec = a.V / EPV;
-  const int per = ((nvec + a.S - 1) / a.S + NS_WAVE - 1) / NS_WAVE * NS_WAVE;
-  const int q0 = part * per < nvec ? part * per : nvec;
-  const int q1 = part + 1 == a.S ? nvec : (q0 + per < nvec ? q0 + per : nvec);
+  const int q0 = (int)((int64_t)nvec * part / a.S), q1 = (int)((int64_t)nvec * (part + 1) / a.S);
   Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
-  Best best{sh + (TOP ? wv * kBuf : 0), 0, a.k, -INFINITY, true};
+  Best best{sh[TOP ? wv : 0], 0, 0, a.k, -INFINITY, true};
   // Loads are never under a condition, so that the batch in flight behind them
   // can be counted: past the end they read the part's last vector again, and
   // `mask` puts -infinity in its place.
@@ -343,16 +398,14 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
   };
   u32x4 x0[kUnroll], x1[kUnroll];
   if (q0 < q1) load(q0, x0);
-  for (int base = q0; base < q1; base += 2 * STEP) {
+#pragma unroll 1
+  for (int base = q0; base < q1; base += STEP) {
     load(base + STEP, x1);
     NS_ISSUE_FENCE();
     mask(base, x0);
     take<ET, TOP>(x0, base, q1, a.c, st, best, lane);
-    if (base + STEP >= q1) break;                          // uniform
-    load(base + 2 * STEP, x0);
-    NS_ISSUE_FENCE();
-    mask(base + STEP, x1);
-    take<ET, TOP>(x1, base + STEP, q1, a.c, st, best, lane);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x0[u] = x1[u];
   }
   if (part + 1 == a.S && a.V % EPV != 0) {                 // the last elements, fewer than a vector
     const int e = nvec * EPV + lane;
@@ -375,17 +428,14 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
     s.W = ns::wave_sum_f32(s.W);
     st = join(st, s, a.c);
     if (TOP) {
-      if (best.fresh) best.start(v, lane);
-      best.add(v, e, live, best.lo, lane);
+      best.take(v, live && v == v, e, lane);
+      best.enter(lane);
     }
   } else {
     st.S = ns::wave_sum_f32(st.S);
     st.W = ns::wave_sum_f32(st.W);
   }
-  if (TOP) {
-    best.compact(lane);
-    wave_sync();
-  }
+  const uint64_t key = best.key;
   if (a.S == 1) {
     const Row r(st, a);
     if (lane == 0) {
@@ -393,58 +443,108 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
       if (a.entropy) a.entropy[row] = r.H;
     }
     if (lane < a.T) put_tokens<ET>(a, r, row, lane);
-    if (TOP && lane < a.k) put_top(a, r, row, lane, lane < best.cnt ? best.buf[lane] : 0);
+    if (TOP && lane < a.k) put_top(a, r, row, lane, key);
   } else {
     if (lane == 0) a.stat[item] = st;
-    if (TOP && lane < a.k) a.keys[item * a.k + lane] = lane < best.cnt ? best.buf[lane] : 0;
+    if (TOP && lane < a.k) a.keys[item * a.k + lane] = key;
   }
 }
 
-// Joins the S parts of a row.
-template <int ET, bool TOP>
-__global__ __launch_bounds__(TOP ? kSelectThreads : NS_WAVE) void k_logprobs_join(Args a) {
-  const size_t row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1);
-  // Every wave joins the parts for itself, in the same order.
-  Stat st = lane < a.S ? a.stat[row * a.S + lane] : Stat{-INFINITY, 0.f, 0.f, 0.f, 0.f};
-  for (int m = 1; m < NS_WAVE; m <<= 1) {
-    Stat o;
-    o.top = __shfl_xor(st.top, m, NS_WAVE);
-    o.ref = __shfl_xor(st.ref, m, NS_WAVE);
-    o.E = __shfl_xor(st.E, m, NS_WAVE);
-    o.S = __shfl_xor(st.S, m, NS_WAVE);
-    o.W = __shfl_xor(st.W, m, NS_WAVE);
-    st = lane & m ? join(o, st, a.c) : join(st, o, a.c);   // the lower part first in both lanes
-  }
-  const Row r(st, a);
-  if (tid == 0) {
-    a.lse[row] = r.lse;
-    if (a.entropy) a.entropy[row] = r.H;
-  }
-  if (tid < a.T) put_tokens<ET>(a, r, row, tid);
-  if constexpr (TOP) {
-    __shared__ SelectSmem sm;
-    const int nk = a.S * a.k;                              // <= 64 * 64
-    float val[4];
-    int id[4];
+// The 64 largest of two sorted lists, one key a lane: a holds one in falling
+// order, b the other in rising order; the larger of each pair is a bitonic
+// sequence, which six exchanges sort.
+__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane) {
+  uint64_t x = a > b ? a : b;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int q = tid + u * kSelectThreads;
-      const uint64_t key = q < nk ? a.keys[row * nk + q] : 0;
-      val[u] = key ? ns::key_val(key) : 0.f;
-      id[u] = key ? ns::key_id(key) : -1;
+  for (int m = NS_WAVE / 2; m >= 1; m >>= 1) {
+    const uint64_t o = ns::shfl_xor_u64(x, m);
+    x = ((lane & m) == 0) == (x > o) ? x : o;
+  }
+  return x;
+}
+
+constexpr int kJoinWaves = 16;
+
+// Joins the S parts of a row: 16 waves merge the parts' lists, four each at
+// most, then one another's; the last wave joins the statistics meanwhile.
+// Takes the same time whatever the keys (a bound on the k-th best, as good as
+// nothing where many logits tie, is not needed).
+template <int ET, bool TOP>
+__global__ __launch_bounds__(TOP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logprobs_join(Args a) {
+  const size_t row = blockIdx.x;
+  const int lane = threadIdx.x & (NS_WAVE - 1), wv = threadIdx.x / NS_WAVE;
+  const bool joins = wv == (TOP ? kJoinWaves - 1 : 0);
+  __shared__ Stat all;
+  // parts, keys and tokens are asked for together
+  constexpr int LISTS = kMaxParts / kJoinWaves;
+  uint64_t list[LISTS] = {};
+  int tok = -1;
+  Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
+  if (joins && lane < a.S) st = a.stat[row * a.S + lane];
+  if (joins && lane < a.T) tok = a.tokens[row * a.T + lane];
+  if (TOP) {
+#pragma unroll
+    for (int i = 0; i < LISTS; ++i) {
+      const int p = wv + i * kJoinWaves, q = i == 0 ? lane : NS_WAVE - 1 - lane;
+      if (p < a.S && q < a.k) list[i] = a.keys[(row * a.S + p) * a.k + q];
     }
-    block_select_topk<4>(val, id, a.k, nk, sm, [&](int i, uint64_t key) { put_top(a, r, row, i, key); });
+  }
+  NS_ISSUE_FENCE();
+  float ztok = 0.f;
+  const bool known = tok >= 0 && tok < a.V;
+  if (known) ztok = one_elem<ET>(a.z, row * (size_t)a.ld + tok);
+  __shared__ uint64_t sh[TOP ? kJoinWaves : 1][NS_WAVE];
+  uint64_t best = list[0];
+  if (TOP) {
+#pragma unroll
+    for (int i = 1; i < LISTS; ++i)
+      if (wv + i * kJoinWaves < a.S) best = merge_lists(best, list[i], lane);
+    sh[wv][lane] = best;
+    __syncthreads();
+  }
+  if (joins) {
+    for (int m = 1; m < a.S; m <<= 1) {
+      Stat o;
+      o.top = __shfl_xor(st.top, m, NS_WAVE);
+      o.ref = __shfl_xor(st.ref, m, NS_WAVE);
+      o.E = __shfl_xor(st.E, m, NS_WAVE);
+      o.S = __shfl_xor(st.S, m, NS_WAVE);
+      o.W = __shfl_xor(st.W, m, NS_WAVE);
+      st = lane & m ? join(o, st, a.c) : join(st, o, a.c);   // the lower part first in both lanes
+    }
+    st.top = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.top)));
+    st.ref = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.ref)));
+    st.E = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.E)));
+    st.S = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.S)));
+    st.W = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.W)));
+    const Row r(st, a);
+    if (lane == 0) {
+      all = st;
+      a.lse[row] = r.lse;
+      if (a.entropy) a.entropy[row] = r.H;
+    }
+    if (lane < a.T) a.logprob[row * a.T + lane] = known ? r.logp(ztok) : 0.f;
+  }
+  if (TOP) {
+#pragma unroll
+    for (int m = kJoinWaves / 2; m >= 1; m >>= 1) {
+      if (wv < m && wv + m < a.S) {                        // wave m .. 2 m - 1 holds something
+        best = merge_lists(best, sh[wv + m][NS_WAVE - 1 - lane], lane);
+        sh[wv][lane] = best;
+      }
+      __syncthreads();
+    }
+    if (wv == 0 && lane < a.k) put_top(a, Row(all, a), row, lane, best);
   }
 }
 
 // Parts of a row: enough waves for the chip, each with a batch at least.
 int parts_of(int L, int V, int dtype) {
   const int batch = NS_WAVE * kUnroll * per_vec(dtype);
-  int s = L >= kWavesWanted ? 1 : (kWavesWanted + L - 1) / (L > 0 ? L : 1);
-  const int most = (V + batch - 1) / batch;
-  s = s > most ? most : s;
-  return s < 1 ? 1 : (s > kMaxParts ? kMaxParts : s);
+  const int wanted = L >= kWavesWanted ? 1 : (kWavesWanted + L - 1) / (L > 0 ? L : 1), most = (V + batch - 1) / batch;
+  int s = 1;
+  while (s < wanted && s * 2 <= most && s < kMaxParts) s *= 2;
+  return s;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -461,7 +561,7 @@ void launch_logprobs(const Args& a, hipStream_t stream) {
   if (a.k > 0) hipLaunchKernelGGL((k_logprobs<ET, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((k_logprobs<ET, false>), grid, block, 0, stream, a);
   if (a.S == 1) return;
-  if (a.k > 0) hipLaunchKernelGGL((k_logprobs_join<ET, true>), dim3((unsigned)a.L), dim3(kSelectThreads), 0, stream, a);
+  if (a.k > 0) hipLaunchKernelGGL((k_logprobs_join<ET, true>), dim3((unsigned)a.L), dim3(kJoinWaves * NS_WAVE), 0, stream, a);
   else hipLaunchKernelGGL((k_logprobs_join<ET, false>), dim3((unsigned)a.L), dim3(NS_WAVE), 0, stream, a);
 }
 

@@ -450,15 +450,52 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
   }
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xf, 0xf, true);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// The value of lane ^ M; within rows of 16 lanes by lane moves, without LDS's latency.
+template <int M>
+__device__ __forceinline__ uint64_t lane_xor_u64(uint64_t v) {
+  if constexpr (M == 1) return dpp_u64<0xB1>(v);           // quad_perm 1 0 3 2
+  else if constexpr (M == 2) return dpp_u64<0x4E>(v);      // quad_perm 2 3 0 1
+  else if constexpr (M == 4) return dpp_u64<0x1B>(dpp_u64<0x141>(v));   // row_half_mirror, quad_perm 3 2 1 0
+  else if constexpr (M == 8) return dpp_u64<0x128>(v);     // row_ror:8
+  else return ns::shfl_xor_u64(v, M);
+}
+
+template <int M>
+__device__ __forceinline__ uint64_t exchange(uint64_t x, int lane) {
+  const uint64_t o = lane_xor_u64<M>(x);
+  return ((lane & M) == 0) == (x > o) ? x : o;
+}
+
 // The 64 largest of two sorted lists, one key a lane: a holds one in falling
 // order, b the other in rising order; the larger of each pair is a bitonic
 // sequence, which six exchanges sort.
 __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane) {
   uint64_t x = a > b ? a : b;
+  x = exchange<32>(x, lane);
+  x = exchange<16>(x, lane);
+  x = exchange<8>(x, lane);
+  x = exchange<4>(x, lane);
+  x = exchange<2>(x, lane);
+  return exchange<1>(x, lane);
+}
+
+// The same for four lists of 16, one in each row of lanes: every row ends with the 16 largest of all.
+__device__ __forceinline__ uint64_t merge_rows(uint64_t x, int lane) {
 #pragma unroll
-  for (int m = NS_WAVE / 2; m >= 1; m >>= 1) {
+  for (int m = 31; m <= 47; m += 16) {                     // the neighbour row, then the next pair's, in rising order
     const uint64_t o = ns::shfl_xor_u64(x, m);
-    x = ((lane & m) == 0) == (x > o) ? x : o;
+    x = x > o ? x : o;
+    x = exchange<8>(x, lane);
+    x = exchange<4>(x, lane);
+    x = exchange<2>(x, lane);
+    x = exchange<1>(x, lane);
   }
   return x;
 }
@@ -468,21 +505,29 @@ constexpr int kJoinWaves = 16;
 // Joins the S parts of a row: 16 waves merge the parts' lists, four each at
 // most, then one another's; the last wave joins the statistics meanwhile.
 // Takes the same time whatever the keys (a bound on the k-th best, as good as
-// nothing where many logits tie, is not needed).
-template <int ET, bool TOP>
-__global__ __launch_bounds__(TOP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logprobs_join(Args a) {
+// nothing where many logits tie, is not needed).  CAP is the length of the
+// lists that are merged, 0 (no alternatives), 16 or 64: with 16 a wave holds
+// four of them at once.
+template <int ET, int CAP>
+__global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logprobs_join(Args a) {
+  constexpr bool TOP = CAP != 0;
   const size_t row = blockIdx.x;
   const int lane = threadIdx.x & (NS_WAVE - 1), wv = threadIdx.x / NS_WAVE;
   const bool joins = wv == (TOP ? kJoinWaves - 1 : 0);
   __shared__ Stat all;
   // parts, keys and tokens are asked for together
   constexpr int LISTS = kMaxParts / kJoinWaves;
+  static_assert(LISTS == 4, "four rows of a wave, or four lists one after the other");
   uint64_t list[LISTS] = {};
   int tok = -1;
   Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
   if (joins && lane < a.S) st = a.stat[row * a.S + lane];
   if (joins && lane < a.T) tok = a.tokens[row * a.T + lane];
-  if (TOP) {
+  if (CAP == 16) {
+    const int p = wv * 4 + lane / 16, q = lane % 16;
+    if (p < a.S && q < a.k) list[0] = a.keys[(row * a.S + p) * a.k + q];
+  }
+  if (CAP == 64) {
 #pragma unroll
     for (int i = 0; i < LISTS; ++i) {
       const int p = wv + i * kJoinWaves, q = i == 0 ? lane : NS_WAVE - 1 - lane;
@@ -495,10 +540,13 @@ __global__ __launch_bounds__(TOP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
   if (known) ztok = one_elem<ET>(a.z, row * (size_t)a.ld + tok);
   __shared__ uint64_t sh[TOP ? kJoinWaves : 1][NS_WAVE];
   uint64_t best = list[0];
-  if (TOP) {
+  if (CAP == 16) best = merge_rows(best, lane);
+  if (CAP == 64) {
 #pragma unroll
     for (int i = 1; i < LISTS; ++i)
       if (wv + i * kJoinWaves < a.S) best = merge_lists(best, list[i], lane);
+  }
+  if (TOP) {
     sh[wv][lane] = best;
     __syncthreads();
   }
@@ -525,7 +573,17 @@ __global__ __launch_bounds__(TOP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
     }
     if (lane < a.T) a.logprob[row * a.T + lane] = known ? r.logp(ztok) : 0.f;
   }
-  if (TOP) {
+  if (CAP == 16) {
+    if (wv < 4) best = merge_rows(sh[wv * 4 + lane / 16][lane % 16], lane);
+    __syncthreads();
+    if (wv < 4) sh[wv][lane] = best;
+    __syncthreads();
+    if (wv == 0) {
+      best = merge_rows(sh[lane / 16][lane % 16], lane);
+      if (lane < a.k) put_top(a, Row(all, a), row, lane, best);
+    }
+  }
+  if (CAP == 64) {
 #pragma unroll
     for (int m = kJoinWaves / 2; m >= 1; m >>= 1) {
       if (wv < m && wv + m < a.S) {                        // wave m .. 2 m - 1 holds something
@@ -561,8 +619,10 @@ void launch_logprobs(const Args& a, hipStream_t stream) {
   if (a.k > 0) hipLaunchKernelGGL((k_logprobs<ET, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((k_logprobs<ET, false>), grid, block, 0, stream, a);
   if (a.S == 1) return;
-  if (a.k > 0) hipLaunchKernelGGL((k_logprobs_join<ET, true>), dim3((unsigned)a.L), dim3(kJoinWaves * NS_WAVE), 0, stream, a);
-  else hipLaunchKernelGGL((k_logprobs_join<ET, false>), dim3((unsigned)a.L), dim3(NS_WAVE), 0, stream, a);
+  const dim3 rows((unsigned)a.L), wide(kJoinWaves * NS_WAVE);
+  if (a.k == 0) hipLaunchKernelGGL((k_logprobs_join<ET, 0>), rows, dim3(NS_WAVE), 0, stream, a);
+  else if (a.k <= 16) hipLaunchKernelGGL((k_logprobs_join<ET, 16>), rows, wide, 0, stream, a);
+  else hipLaunchKernelGGL((k_logprobs_join<ET, 64>), rows, wide, 0, stream, a);
 }
 
 // ---------------------------------------------------------------------------

@@ -500,25 +500,25 @@ __device__ __forceinline__ uint64_t merge_rows(uint64_t x, int lane) {
   return x;
 }
 
-constexpr int kJoinWaves = 16;
+constexpr int kJoinLists = 4;            // parts' lists of a wave
 
-// Joins the S parts of a row: 16 waves merge the parts' lists, four each at
-// most, then one another's; the last wave joins the statistics meanwhile.
+// Joins the S parts of a row: JW waves (one up to four parts, 16 for more)
+// merge the parts' lists, four each at most, then one another's; the last wave
+// joins the statistics meanwhile.
 // Takes the same time whatever the keys (a bound on the k-th best, as good as
 // nothing where many logits tie, is not needed).  CAP is the length of the
 // lists that are merged, 0 (no alternatives), 16 or 64: with 16 a wave holds
 // four of them at once.
-template <int ET, int CAP>
-__global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logprobs_join(Args a) {
+template <int ET, int CAP, int JW>
+__global__ __launch_bounds__(JW* NS_WAVE) void k_logprobs_join(Args a) {
   constexpr bool TOP = CAP != 0;
   const size_t row = blockIdx.x;
   const int lane = threadIdx.x & (NS_WAVE - 1), wv = threadIdx.x / NS_WAVE;
-  const bool joins = wv == (TOP ? kJoinWaves - 1 : 0);
+  const bool joins = wv == JW - 1;
   __shared__ Stat all;
   // parts, keys and tokens are asked for together
-  constexpr int LISTS = kMaxParts / kJoinWaves;
-  static_assert(LISTS == 4, "four rows of a wave, or four lists one after the other");
-  uint64_t list[LISTS] = {};
+  static_assert(16 * kJoinLists == kMaxParts, "16 waves hold every part's list");
+  uint64_t list[kJoinLists] = {};
   int tok = -1;
   Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
   if (joins && lane < a.S) st = a.stat[row * a.S + lane];
@@ -529,8 +529,8 @@ __global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
   }
   if (CAP == 64) {
 #pragma unroll
-    for (int i = 0; i < LISTS; ++i) {
-      const int p = wv + i * kJoinWaves, q = i == 0 ? lane : NS_WAVE - 1 - lane;
+    for (int i = 0; i < kJoinLists; ++i) {
+      const int p = wv + i * JW, q = i == 0 ? lane : NS_WAVE - 1 - lane;
       if (p < a.S && q < a.k) list[i] = a.keys[(row * a.S + p) * a.k + q];
     }
   }
@@ -538,15 +538,15 @@ __global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
   float ztok = 0.f;
   const bool known = tok >= 0 && tok < a.V;
   if (known) ztok = one_elem<ET>(a.z, row * (size_t)a.ld + tok);
-  __shared__ uint64_t sh[TOP ? kJoinWaves : 1][NS_WAVE];
+  __shared__ uint64_t sh[TOP && JW > 1 ? JW : 1][NS_WAVE];
   uint64_t best = list[0];
   if (CAP == 16) best = merge_rows(best, lane);
   if (CAP == 64) {
 #pragma unroll
-    for (int i = 1; i < LISTS; ++i)
-      if (wv + i * kJoinWaves < a.S) best = merge_lists(best, list[i], lane);
+    for (int i = 1; i < kJoinLists; ++i)
+      if (wv + i * JW < a.S) best = merge_lists(best, list[i], lane);
   }
-  if (TOP) {
+  if (TOP && JW > 1) {
     sh[wv][lane] = best;
     __syncthreads();
   }
@@ -566,6 +566,7 @@ __global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
     st.S = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.S)));
     st.W = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st.W)));
     const Row r(st, a);
+    if (TOP && JW == 1 && lane < a.k) put_top(a, r, row, lane, best);
     if (lane == 0) {
       all = st;
       a.lse[row] = r.lse;
@@ -573,7 +574,7 @@ __global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
     }
     if (lane < a.T) a.logprob[row * a.T + lane] = known ? r.logp(ztok) : 0.f;
   }
-  if (CAP == 16) {
+  if (CAP == 16 && JW > 1) {
     if (wv < 4) best = merge_rows(sh[wv * 4 + lane / 16][lane % 16], lane);
     __syncthreads();
     if (wv < 4) sh[wv][lane] = best;
@@ -583,9 +584,9 @@ __global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
       if (lane < a.k) put_top(a, Row(all, a), row, lane, best);
     }
   }
-  if (CAP == 64) {
+  if (CAP == 64 && JW > 1) {
 #pragma unroll
-    for (int m = kJoinWaves / 2; m >= 1; m >>= 1) {
+    for (int m = JW / 2; m >= 1; m >>= 1) {
       if (wv < m && wv + m < a.S) {                        // wave m .. 2 m - 1 holds something
         best = merge_lists(best, sh[wv + m][NS_WAVE - 1 - lane], lane);
         sh[wv][lane] = best;
@@ -596,12 +597,15 @@ __global__ __launch_bounds__(CAP ? kJoinWaves * NS_WAVE : NS_WAVE) void k_logpro
   }
 }
 
-// Parts of a row: enough waves for the chip, each with a batch at least.
+// Parts of a row: doubled until about kWavesWanted waves (three quarters of
+// them at least) run, each with a batch at least, from 512 rows on with two.
+// 1500 rows of 128256 bf16 logits, k = 4: 76 us in two parts, 89 in one; 1000
+// of 50257 33 in two, 34 in four; 1023 of 4000 9.4 in one, 11.1 in two.
 int parts_of(int L, int V, int dtype) {
-  const int batch = NS_WAVE * kUnroll * per_vec(dtype);
-  const int wanted = L >= kWavesWanted ? 1 : (kWavesWanted + L - 1) / (L > 0 ? L : 1), most = (V + batch - 1) / batch;
+  const int batch = NS_WAVE * kUnroll * per_vec(dtype) * (L < 512 ? 1 : 2);
+  const int most = (V + batch - 1) / batch;
   int s = 1;
-  while (s < wanted && s * 2 <= most && s < kMaxParts) s *= 2;
+  while ((int64_t)s * L * 4 < kWavesWanted * 3 && s * 2 <= most && s < kMaxParts) s *= 2;
   return s;
 }
 
@@ -619,10 +623,13 @@ void launch_logprobs(const Args& a, hipStream_t stream) {
   if (a.k > 0) hipLaunchKernelGGL((k_logprobs<ET, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((k_logprobs<ET, false>), grid, block, 0, stream, a);
   if (a.S == 1) return;
-  const dim3 rows((unsigned)a.L), wide(kJoinWaves * NS_WAVE);
-  if (a.k == 0) hipLaunchKernelGGL((k_logprobs_join<ET, 0>), rows, dim3(NS_WAVE), 0, stream, a);
-  else if (a.k <= 16) hipLaunchKernelGGL((k_logprobs_join<ET, 16>), rows, wide, 0, stream, a);
-  else hipLaunchKernelGGL((k_logprobs_join<ET, 64>), rows, wide, 0, stream, a);
+  const dim3 rows((unsigned)a.L);
+  const bool one = a.S <= kJoinLists;
+  if (a.k == 0) hipLaunchKernelGGL((k_logprobs_join<ET, 0, 1>), rows, dim3(NS_WAVE), 0, stream, a);
+  else if (a.k <= 16 && one) hipLaunchKernelGGL((k_logprobs_join<ET, 16, 1>), rows, dim3(NS_WAVE), 0, stream, a);
+  else if (a.k <= 16) hipLaunchKernelGGL((k_logprobs_join<ET, 16, 16>), rows, dim3(16 * NS_WAVE), 0, stream, a);
+  else if (one) hipLaunchKernelGGL((k_logprobs_join<ET, 64, 1>), rows, dim3(NS_WAVE), 0, stream, a);
+  else hipLaunchKernelGGL((k_logprobs_join<ET, 64, 16>), rows, dim3(16 * NS_WAVE), 0, stream, a);
 }
 
 // ---------------------------------------------------------------------------

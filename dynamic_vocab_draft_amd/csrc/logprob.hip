@@ -784,12 +784,14 @@ void launch_grad(const GradArgs& a, hipStream_t stream) {
                      stream, a, per, chunks);
 }
 
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+
 bool known_dtype(int t) { return t == NS_BF16 || t == NS_FP32 || t == NS_FP16; }
 bool elem_aligned(const void* p, int dtype) { return ((uintptr_t)p) % (dtype == NS_FP32 ? 4 : 2) == 0; }
 // NaN fails both comparisons
 bool temp_ok(float t) { return t >= NS_MIN_INV_TEMP && t <= NS_MAX_INV_TEMP; }
 bool dims_ok(int L, int64_t ld, int V, int T) {
-  return L >= 0 && L <= NS_MAX_ROWS && V >= 1 && V <= NS_MAX_V && ld >= V && T >= 0 && T <= NS_MAX_K;
+  return L >= 0 && L <= NS_MAX_ROWS && V >= 1 && V <= NS_MAX_V && ld >= V && ld <= kMaxLd && T >= 0 && T <= NS_MAX_K;
 }
 
 }  // namespace
@@ -841,7 +843,7 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
                                  const float* g_logprob, const float* g_entropy, const float* g_lse, void* dlogits,
                                  int64_t ld_d, hipStream_t stream) {
   if (!known_dtype(dtype)) return NS_EDTYPE;
-  if (!dims_ok(L, ld, V, T) || ld_d < V || !temp_ok(inv_temp)) return NS_EINVAL;
+  if (!dims_ok(L, ld, V, T) || ld_d < V || ld_d > kMaxLd || !temp_ok(inv_temp)) return NS_EINVAL;
   if (L == 0) return NS_OK;
   if (!logits || !lse || !dlogits || (T > 0 && (!tokens || !g_logprob)) || (g_entropy && !entropy)) return NS_EINVAL;
   if (!elem_aligned(logits, dtype) || !elem_aligned(dlogits, dtype)) return NS_EINVAL;

@@ -247,8 +247,8 @@ struct Product {
   const int32_t* ids;       // [B][N] row of column j, or NULL: j
   const int32_t* n_dev;     // [B] live columns, or NULL: N
   int M, N, V, pitch;
-  void* out;                // [B][M] rows, ld_out elements apart
-  int64_t ld_out;
+  void* out;                // [B][M][N], elements of a token `sm` apart for m, `sn` for n
+  int64_t sm, sn;
 };
 
 constexpr int kStageK = 128;                       // bytes of a row in a stage
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     p.x += seq * p.M * p.pitch;
     p.xs += seq * p.M;
     if (p.ids) p.ids += seq * p.N;
-    p.out = (char*)p.out + seq * p.M * (size_t)p.ld_out * (OT == NS_FP32 ? 4 : 2);
+    p.out = (char*)p.out + seq * p.M * (size_t)p.sm * (OT == NS_FP32 ? 4 : 2);
   }
   const int units = (live + ROWS - 1) / ROWS, per_block = (units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
           const int m = u * 16 + g * 4 + r;
           const float v = scaled(acc[t][u][r], xs[u][r] * ws[t]);
           const uint32_t at =
-              m < p.M && j <= last && (ROWS >= 16 || i < ROWS) ? (uint32_t)(((size_t)m * (size_t)p.ld_out + n0 + j) * ESZ) : 0x80000000u;
+              m < p.M && j <= last && (ROWS >= 16 || i < ROWS) ? (uint32_t)(((size_t)m * (size_t)p.sm + (size_t)(n0 + j) * (size_t)p.sn) * ESZ) : 0x80000000u;
           if (OT == NS_FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
           else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)narrow2<OT>(v, 0.f), ro, at, 0, 0);
           acc[t][u][r] = 0;
@@ -694,7 +694,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = scaled(acc[e][u][r], xs * ws[e]);
-        const size_t at = (size_t)m * (size_t)p.ld_out + n;
+        const size_t at = (size_t)m * (size_t)p.sm + n;
         if (stored) store_eight<OT>(p.out, at, v, 8);
         else if (m < p.M && n < p.N) store_eight<OT>(p.out, at, v, p.N - n);
       }
@@ -779,7 +779,7 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
     for (int r = 0; r < 4; ++r) {
       const int m = u * 16 + g * 4 + r;
       if (m < p.M && j0 + i < n)
-        store_out<OT>(p.out, (seq * p.M + m) * (size_t)p.ld_out + j0 + i, scaled(s[r], xs[u][r] * ws));
+        store_out<OT>(p.out, (seq * p.M + m) * (size_t)p.sm + (size_t)(j0 + i) * (size_t)p.sn, scaled(s[r], xs[u][r] * ws));
     }
   }
 }
@@ -800,13 +800,50 @@ void launch_stream(const Product& p, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
+template <int OT, int NMT>
+void launch_few(const Product& p, int B, hipStream_t stream) {
+  hipLaunchKernelGGL((k_product_few<OT, NMT>), dim3((unsigned)((p.N + 15) / 16), (unsigned)B), dim3(512), 0, stream, p);
+}
+
 template <int OT>
-void launch_product(const Product& p, hipStream_t stream) {
-  if (p.M <= 64 && (uint64_t)p.M * (uint64_t)p.ld_out * (OT == NS_FP32 ? 4 : 2) < 0x7FFFFFFFull) {
-    if (p.M <= 16) launch_stream<OT, 1, 16, 7>(p, stream);
-    else if (p.M <= 32) launch_stream<OT, 2, 16, 7>(p, stream);
-    else if (p.M <= 48) launch_stream<OT, 3, 32, 3>(p, stream);
-    else launch_stream<OT, 4, 32, 3>(p, stream);
+void launch_few_of(const Product& p, int B, hipStream_t stream) {
+  if (p.M <= 16) launch_few<OT, 1>(p, B, stream);
+  else if (p.M <= 32) launch_few<OT, 2>(p, B, stream);
+  else if (p.M <= 48) launch_few<OT, 3>(p, B, stream);
+  else launch_few<OT, 4>(p, B, stream);
+}
+
+// Up to 64 tokens: up to 4096 channels (a 16-row block a CU) the kernel for few
+// rows (M = 8, d = 4096: 2048 channels 5.7 us against 10.5 streamed, 4096 6.1
+// against 10.7, 10000 13.3 against 11.4); up to 16384 (one pass of eight-row
+// units) the stream of those (M = 60, d = 3584: 16000 channels 15.0 us against
+// 21.1 with taller units, 30000 28.8 against 23.9); then the taller units.
+// More tokens take tiles, of 128 tokens up to 128 and of 256 beyond
+// (151936 channels, d = 3584: 128 tokens 149 against 168 us, 129 202 against
+// 167).  With at most 64 channels the two sides change places.
+template <int OT>
+void launch_product(Product p, hipStream_t stream) {
+  if (p.M > 64 && p.N <= 64) {
+    p = Product{p.w, p.ws, p.x, p.xs, nullptr, nullptr, p.N, p.M, p.M, p.pitch, p.out, p.sn, p.sm};
+  }
+  const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
+                        (OT == NS_FP32 ? 4 : 2);
+  if (p.M <= 64 && p.N <= 4096) {
+    launch_few_of<OT>(p, 1, stream);
+  } else if (p.M <= 64 && span < 0x7FFFFFFFull) {    // the stream's output offsets have 31 bits
+    if (p.N <= 16384) {
+      if (p.M <= 16) launch_stream<OT, 1, 8, 7>(p, stream);
+      else if (p.M <= 32) launch_stream<OT, 2, 8, 7>(p, stream);
+      else if (p.M <= 48) launch_stream<OT, 3, 8, 7>(p, stream);
+      else launch_stream<OT, 4, 8, 7>(p, stream);
+    } else {
+      if (p.M <= 16) launch_stream<OT, 1, 16, 7>(p, stream);
+      else if (p.M <= 32) launch_stream<OT, 2, 16, 7>(p, stream);
+      else if (p.M <= 48) launch_stream<OT, 3, 32, 3>(p, stream);
+      else launch_stream<OT, 4, 32, 3>(p, stream);
+    }
+  } else if (p.M <= 64) {
+    launch_few_of<OT>(p, 1, stream);
   } else if (p.M > 128) {
     launch_tiled<OT, 4>(p, stream);
   } else {
@@ -824,12 +861,6 @@ void launch_head_stream(const Product& p, int B, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-template <int NMT>
-void launch_head_few(const Product& p, int B, hipStream_t stream) {
-  hipLaunchKernelGGL((k_product_few<NS_FP32, NMT>), dim3((unsigned)((p.N + 15) / 16), (unsigned)B), dim3(512), 0,
-                     stream, p);
-}
-
 // The head's logits, B sequences.  Whole calls, the kernel for few rows
 // against the stream of eight-row units: M = 8, 1000 rows 13.4 against 18.2 us;
 // M = 64, 4000 rows 23.0 against 26.4, 8000 rows 36.5 against 31.4, 15500 rows
@@ -840,10 +871,7 @@ void launch_head_few(const Product& p, int B, hipStream_t stream) {
 void launch_head(const Product& p, int B, hipStream_t stream) {
   const int64_t rows = (int64_t)B * p.N;
   if (rows < 8192 || (uint64_t)p.V * (uint64_t)p.pitch > 0xFFFFFFFFull) {
-    if (p.M <= 16) launch_head_few<1>(p, B, stream);
-    else if (p.M <= 32) launch_head_few<2>(p, B, stream);
-    else if (p.M <= 48) launch_head_few<3>(p, B, stream);
-    else launch_head_few<4>(p, B, stream);
+    launch_few_of<NS_FP32>(p, B, stream);
   } else if (rows <= 65536) {
     if (p.M <= 16) launch_head_stream<1, 8, 7>(p, B, stream);
     else if (p.M <= 32) launch_head_stream<2, 8, 7>(p, B, stream);
@@ -976,6 +1004,8 @@ HeadWs head_ws(int B, int n_max, int M, int k, int d) {
   return w;
 }
 
+constexpr int64_t kMaxLd = (int64_t)1 << 40;       // no product with a row count overflows
+
 bool known_dtype(int t) { return t == NS_BF16 || t == NS_FP32 || t == NS_FP16; }
 bool aligned16(const void* p) { return (((uintptr_t)p) & 15u) == 0; }
 
@@ -993,7 +1023,7 @@ int32_t nanospec_quant_pitch(int32_t d) { return d < 1 || d > NS_MAX_D ? 0 : pit
 int nanospec_quant_rows(const void* x, int64_t ld, int32_t R, int32_t d, int32_t dtype, int8_t* q, float* scale,
                         hipStream_t stream) {
   if (!known_dtype(dtype)) return NS_EDTYPE;
-  if (R < 0 || R > NS_MAX_ROWS || d < 1 || d > NS_MAX_D || ld < d) return NS_EINVAL;
+  if (R < 0 || R > NS_MAX_ROWS || d < 1 || d > NS_MAX_D || ld < d || ld > kMaxLd) return NS_EINVAL;
   if (R == 0) return NS_OK;
   if (!x || !q || !scale || !aligned16(q)) return NS_EINVAL;
   if (((uintptr_t)x) % (dtype == NS_FP32 ? 4 : 2)) return NS_EINVAL;
@@ -1004,12 +1034,14 @@ int nanospec_quant_rows(const void* x, int64_t ld, int32_t R, int32_t d, int32_t
 int nanospec_quant_matmul(const int8_t* xq, const float* xs, int32_t M, const int8_t* wq, const float* ws, int32_t N,
                           int32_t d, void* out, int64_t ld_out, int32_t out_dtype, hipStream_t stream) {
   if (!known_dtype(out_dtype)) return NS_EDTYPE;
-  if (M < 0 || M > NS_MAX_ROWS || N < 1 || N > NS_MAX_V || d < 1 || d > NS_MAX_D || ld_out < N) return NS_EINVAL;
+  if (M < 0 || M > NS_MAX_ROWS || N < 1 || N > NS_MAX_V || d < 1 || d > NS_MAX_D || ld_out < N ||
+      ld_out > kMaxLd)
+    return NS_EINVAL;
   if (M == 0) return NS_OK;
   if (!xq || !xs || !wq || !ws || !out || !aligned16(xq) || !aligned16(wq)) return NS_EINVAL;
   if (((uintptr_t)out) % (out_dtype == NS_FP32 ? 4 : 2)) return NS_EINVAL;
   (void)hipGetLastError();
-  const Product p{xq, xs, wq, ws, nullptr, nullptr, M, N, N, pitch_of(d), out, ld_out};
+  const Product p{xq, xs, wq, ws, nullptr, nullptr, M, N, N, pitch_of(d), out, ld_out, 1};
   if (out_dtype == NS_FP32) launch_product<NS_FP32>(p, stream);
   else if (out_dtype == NS_BF16) launch_product<NS_BF16>(p, stream);
   else launch_product<NS_FP16>(p, stream);
@@ -1037,7 +1069,7 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   float* z = (float*)(base + l.z);
   int rc = quant_rows(h, d, B * M, d, dtype, hq, hs, stream);
   if (rc != NS_OK) return rc;
-  const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld};
+  const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
   launch_head(p, B, stream);
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;

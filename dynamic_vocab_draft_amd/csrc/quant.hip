@@ -66,6 +66,17 @@ struct Eight {
     else if constexpr (ET == NS_BF16) return e & 1 ? ns::bf16_hi(v[0][e >> 1]) : ns::bf16_lo(v[0][e >> 1]);
     else return e & 1 ? ns::fp16_hi(v[0][e >> 1]) : ns::fp16_lo(v[0][e >> 1]);
   }
+  // element e where e is not known to the compiler
+  __device__ __forceinline__ float pick(int e) const {
+    if constexpr (ET == NS_FP32) {
+      const u32x4 h = e & 4 ? v[1] : v[0];
+      const uint32_t a = e & 1 ? h.y : h.x, b = e & 1 ? h.w : h.z;
+      return __uint_as_float(e & 2 ? b : a);
+    } else {
+      const uint32_t a = e & 2 ? v[0].y : v[0].x, b = e & 2 ? v[0].w : v[0].z, w = (e & 4 ? b : a) >> (e & 1) * 16;
+      return ET == NS_BF16 ? ns::bf16_lo(w) : ns::fp16_lo(w);
+    }
+  }
   // The largest magnitude as the type's own bits, which order like the values
   // with infinities and NaN on top; two at once for 16-bit types.
   __device__ __forceinline__ uint32_t top(uint32_t so_far) const {
@@ -100,24 +111,52 @@ __device__ __forceinline__ int quant_exact(float x, float a) {
   return x < 0.f ? -q : q;
 }
 
-// Eight elements to eight bytes.  x * inv + 1.5 * 2^23 has round(x * inv) in
-// its low byte.  inv = 127 / a is off by at most 2^-24 relatively, so 127
-// times that in the product: only where that could reach a half (within
-// 1.6e-5 of one) are the eight decided exactly.
+// Eight elements times `up`, each decided exactly; a loop, since its code is
+// rarely entered and would fill the instruction cache unrolled.
 template <int ET>
-__device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, float inv, float a) {
+__device__ __forceinline__ u32x2 quant_eight_exact(const Eight<ET>& x, float up, float a) {
+  u32x2 r = {0, 0};
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = ((uint32_t)quant_exact(x.pick(e) * up, a) & 0xFFu) << (e & 3) * 8;
+    r.x |= e < 4 ? b : 0u;
+    r.y |= e < 4 ? 0u : b;
+  }
+  return r;
+}
+
+// Eight elements to eight bytes, for a maximum a in [2^-100, 2^100] and rcp =
+// 1 / a.  Adding 1.5 * 2^23 leaves a value rounded to an integer, halves to
+// even, in the low byte.
+// 16-bit types: q = 127 x * rcp is off by 2^-23 relatively at most, its
+// remainder 127 x - q a is exact (one fused multiply-add of terms with at most
+// 18 bits and 24 + 11), and q + remainder * rcp is then the quotient rounded
+// to float32: a half comes out as itself, and whatever lies beside one by at
+// least 2^-20 of its size (254 x and an odd multiple of a differ by a unit of
+// x or a) stays on its side.  No case is left to decide (halves are common:
+// half of all groups of 512 bf16 normals hold one).
+// float32: x * (127 rcp) is off by 2^-22 relatively; only where that could reach a
+// half (within 3.2e-5 of one, which is rare) are the eight decided exactly.
+template <int ET>
+__device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, float rcp, float a) {
   constexpr float kMagic = 12582912.f;
   uint32_t b[8];
-  float off = 0.f;
+  if constexpr (ET == NS_FP32) {
+    const float inv = 127.f * rcp;
+    float off = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float v = x.get(e), f = fmaf(v, inv, kMagic);
-    off = fmaxf(off, fabsf(fmaf(v, inv, kMagic - f)));
-    b[e] = __float_as_uint(f);
-  }
-  if (off > 0.5f - 1.6e-5f) {
+    for (int e = 0; e < 8; ++e) {
+      const float v = x.get(e), f = fmaf(v, inv, kMagic);
+      off = fmaxf(off, fabsf(fmaf(v, inv, kMagic - f)));
+      b[e] = __float_as_uint(f);
+    }
+    if (off > 0.5f - 3.2e-5f) return quant_eight_exact<ET>(x, 1.f, a);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = (uint32_t)quant_exact(x.get(e), a);
+    for (int e = 0; e < 8; ++e) {
+      const float m = 127.f * x.get(e), q = m * rcp;
+      b[e] = __float_as_uint(fmaf(fmaf(-q, a, m), rcp, q) + kMagic);
+    }
   }
   u32x2 r;
 #pragma unroll
@@ -127,6 +166,18 @@ __device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, float inv, floa
     r[h] = lo | hi;
   }
   return r;
+}
+
+// Maximum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);    // quad_perm 1 0 3 2
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);             // quad_perm 2 3 0 1
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);            // row_half_mirror
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true);            // row_mirror
+  return o > v ? o : v;
 }
 
 constexpr int kQuantThreads = 256;
@@ -169,20 +220,23 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_rows(const void* __rest
   const bool bad = m >= 0x7F800000u;
   const float a = __uint_as_float(m);
   int8_t* out = q + (size_t)r * (size_t)pitch;
-  if (bad || a < 0x1p-100f) {                      // uniform over the row; zeros and the smallest magnitudes here
-    // 127 / a would overflow: everything 2^64 times as large, which is exact
+  if (bad || a < 0x1p-100f || a > 0x1p100f) {      // uniform over the row; zeros are here too
+    // 1 / a or 127 x could overflow: everything 2^64 times as large or as
+    // small, exact for all that is not far below a
+    const float by = a > 1.f ? 0x1p-64f : 0x1p64f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int i = (t + g * T) * 8;
-      for (int e = 0; e < 8 && i < pitch; ++e)
-        out[i + e] = bad || m == 0 ? (int8_t)0 : (int8_t)quant_exact(v[g].get(e) * 0x1p64f, a * 0x1p64f);
+      u32x2 r = {0, 0};
+      if (!bad && m != 0) r = quant_eight_exact<ET>(v[g], by, a * by);
+      if (i < pitch) *(u32x2*)(out + i) = r;
     }
   } else {
-    const float inv = 127.f / a;
+    const float rcp = 1.f / a;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int i = (t + g * T) * 8;
-      if (i < pitch) *(u32x2*)(out + i) = quant_eight<ET>(v[g], inv, a);
+      if (i < pitch) *(u32x2*)(out + i) = quant_eight<ET>(v[g], rcp, a);
     }
   }
   if (t == 0) scale[r] = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
@@ -784,6 +838,113 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The head over few rows with the quantisation of its hidden rows in the same
+// launch, for up to 16 of them and 32 KB of 8-bit hidden rows: every block
+// quantises them all into LDS (64 elements a thread at most) while its channel
+// rows are on their way.  A launch less: M = 8, d = 4096, 1000 rows 12.6 -> 12.0
+// us, M = 1 11.8 -> 8.8, 19 sequences of 46 rows, M = 8, d = 320, 12.5 -> 9.8.
+// ---------------------------------------------------------------------------
+constexpr int kFusedBytes = 32768;                 // M * pitch, at most
+constexpr int kFusedPad = 16;                      // between token rows in LDS: no bank is met twice
+
+template <int ET>
+__global__ __launch_bounds__(512) void k_head_few(Product p, const void* __restrict__ h, int d) {
+  constexpr int BATCH = 8, U = kFusedBytes / 8 / 512;
+  __shared__ __attribute__((aligned(16))) char xq[kFusedBytes + 16 * kFusedPad];
+  __shared__ i32x4 sh[8][NS_WAVE];
+  __shared__ uint32_t s_top[16];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const size_t seq = blockIdx.y;
+  const int j0 = (int)blockIdx.x * 16, j = j0 + i < p.N ? j0 + i : p.N - 1;
+  int n = p.n_dev ? p.n_dev[seq] : p.N;
+  int id = p.ids ? p.ids[seq * p.N + j] : j;
+  // Hidden rows in chunks of 128 elements, 16 lanes each, lane c % 16 eight of
+  // them; c / per_row by a product, exact for c * per_row < 2^16.
+  const int per_row = p.pitch / 128, chunks = p.M * per_row, magic = 65536 / per_row + 1;
+  const char* hb = (const char*)h + seq * p.M * (size_t)d * (ET == NS_FP32 ? 4 : 2);
+  Eight<ET> v[U];
+  int tok[U], at[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = (tid >> 4) + u * 32;
+    tok[u] = c < chunks ? c * magic >> 16 : -1;
+    at[u] = (c - tok[u] * per_row) * 128 + (tid & 15) * 8;
+    if (tok[u] >= 0) v[u].load(hb + (size_t)tok[u] * d * (ET == NS_FP32 ? 4 : 2), at[u], d);
+  }
+  if (tid < 16) s_top[tid] = 0;
+  NS_ISSUE_FENCE();
+  n = n < p.N ? n : p.N;
+  if (j0 >= n) return;
+  id = id < 0 || id >= p.V ? 0 : id;
+  const float ws = p.ws[id];
+  const int steps = p.pitch / 64, per = (steps + 7) / 8;
+  const int k0 = w * per, k1 = k0 + per < steps ? k0 + per : steps;
+  const int8_t* wr = p.w + (size_t)id * p.pitch + g * 16;
+  i32x4 a[BATCH];
+  const auto rows = [&](int k) {
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q) a[q] = *(const i32x4*)(wr + (k + q < k1 ? k + q : 0) * 64);
+  };
+  rows(k0);
+  NS_ISSUE_FENCE();
+  const auto sync = [&]() {                          // LDS only: the loads stay out
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  sync();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (tok[u] < 0) continue;                        // whole rows of 16 lanes
+    const uint32_t t = v[u].top(0);
+    float top;
+    if (ET == NS_FP32) top = __uint_as_float(t);
+    else {
+      const uint32_t lo = t & 0xFFFFu, hi = t >> 16, b = lo > hi ? lo : hi;
+      top = ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b);
+    }
+    const uint32_t most = row16_max_u32(__float_as_uint(top));
+    if ((tid & 15) == 0) atomicMax(&s_top[tok[u]], most);
+  }
+  sync();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (tok[u] < 0) continue;
+    const uint32_t m = s_top[tok[u]];
+    const float top = __uint_as_float(m);
+    u32x2 q = {0, 0};
+    if (m < 0x7F800000u && m != 0)
+      q = top < 0x1p-100f   ? quant_eight_exact<ET>(v[u], 0x1p64f, top * 0x1p64f)
+          : top > 0x1p100f ? quant_eight_exact<ET>(v[u], 0x1p-64f, top * 0x1p-64f)
+                           : quant_eight<ET>(v[u], 1.f / top, top);
+    *(u32x2*)(xq + tok[u] * (p.pitch + kFusedPad) + at[u]) = q;
+  }
+  sync();
+  const char* xr = xq + (i < p.M ? i : 0) * (p.pitch + kFusedPad) + g * 16;
+  i32x4 acc = {};
+  for (int k = k0; k < k1; k += BATCH) {
+    if (k > k0) rows(k);
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q)
+      if (k + q < k1) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4*)(xr + (k + q) * 64), a[q], acc, 0, 0, 0);
+  }
+  sh[w][lane] = acc;
+  __syncthreads();
+  if (w != 0) return;
+  i32x4 s = sh[0][lane];
+#pragma unroll
+  for (int q = 1; q < 8; ++q) s += sh[q][lane];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int m = g * 4 + r;
+    if (m >= p.M || j0 + i >= n) continue;
+    const uint32_t t = s_top[m];
+    const float xs = t >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(t) / 127.f;
+    store_out<NS_FP32>(p.out, (seq * p.M + m) * (size_t)p.sm + (size_t)(j0 + i) * (size_t)p.sn, scaled(s[r], xs * ws));
+  }
+}
+
 template <int OT, int TB>
 void launch_tiled(const Product& p, hipStream_t stream) {
   const int tm = (p.M + TB * 64 - 1) / (TB * 64), tn = (p.N + kTileN - 1) / kTileN;
@@ -868,9 +1029,13 @@ void launch_head_stream(const Product& p, int B, hipStream_t stream) {
 // 30.3.  Taller units, with fewer barriers, pay once a CU has several passes
 // of eight-row ones (M = 8, 100000 rows 81.4 against 83.7 us; 15500 rows, M =
 // 64, 39.3 against 33.0).  The stream's 32-bit row addresses reach 4 GB.
+bool few_rows(int B, int n_max, int V, int d) {
+  return (int64_t)B * n_max < 8192 || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
+}
+
 void launch_head(const Product& p, int B, hipStream_t stream) {
   const int64_t rows = (int64_t)B * p.N;
-  if (rows < 8192 || (uint64_t)p.V * (uint64_t)p.pitch > 0xFFFFFFFFull) {
+  if (few_rows(B, p.N, p.V, p.pitch)) {
     launch_few_of<NS_FP32>(p, B, stream);
   } else if (rows <= 65536) {
     if (p.M <= 16) launch_head_stream<1, 8, 7>(p, B, stream);
@@ -889,7 +1054,7 @@ void launch_head(const Product& p, int B, hipStream_t stream) {
 // Top-k over the scaled logits of each hidden row
 // ---------------------------------------------------------------------------
 // Columns of a thread: 4 cover 4096 columns in one block; 16, for more, cover
-// 16384 (64 x 15500: 11.5 us in chunks of 4096 with a join, TOP16 us in one).
+// 16384 (64 x 15500: 11.5 us in chunks of 4096 with a join, 7.8 us in one).
 constexpr int top_cols(int n_max) { return n_max <= 4 * kSelectThreads ? 4 : 16; }
 constexpr int top_chunk(int n_max) { return kSelectThreads * top_cols(n_max); }
 
@@ -1067,10 +1232,19 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   int8_t* hq = (int8_t*)(base + l.q);
   float* hs = (float*)(base + l.scale);
   float* z = (float*)(base + l.z);
-  int rc = quant_rows(h, d, B * M, d, dtype, hq, hs, stream);
+  int rc = NS_OK;
+  const bool fused = few_rows(B, n_max, V, d) && M <= 16 && M * pitch_of(d) <= kFusedBytes;
+  if (!fused) rc = quant_rows(h, d, B * M, d, dtype, hq, hs, stream);
   if (rc != NS_OK) return rc;
   const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
-  launch_head(p, B, stream);
+  if (!fused) {
+    launch_head(p, B, stream);
+  } else {
+    const dim3 grid((unsigned)((n_max + 15) / 16), (unsigned)B), block(512);
+    if (dtype == NS_BF16) hipLaunchKernelGGL(k_head_few<NS_BF16>, grid, block, 0, stream, p, h, d);
+    else if (dtype == NS_FP16) hipLaunchKernelGGL(k_head_few<NS_FP16>, grid, block, 0, stream, p, h, d);
+    else hipLaunchKernelGGL(k_head_few<NS_FP32>, grid, block, 0, stream, p, h, d);
+  }
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;
   const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};

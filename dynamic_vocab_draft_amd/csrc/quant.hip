@@ -378,7 +378,7 @@ __device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v
 }
 
 // ---------------------------------------------------------------------------
-// The product for up to 64 token rows: bound by the bytes of the channel rows,
+// The product for up to 128 token rows: bound by the bytes of the channel rows,
 // each read once.
 //
 // One block of eight waves a CU takes an even share of the 16-row channel
@@ -416,8 +416,9 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
   constexpr int RT = ROWS > 16 ? ROWS / 16 : 1, PROWS = kStreamWaves * ROWS, LR = ROWS / 8;
   constexpr int XOFF = PROWS * kStageK, SOFF = XOFF + NMT * 16 * kStageK;
   constexpr int STAGE = SOFF + kStreamWaves * 256;   // channel rows, token rows, channel scales
-  constexpr int LW = LR + (NMT == 4 ? 1 : NMT);  // loads of a wave and stage
-  constexpr int STORES = RT * NMT * 4;
+  constexpr int XL = NMT % 4 == 0 ? NMT / 4 : NMT, LW = LR + XL;   // loads of a wave and stage
+  // stores behind a pass that the waits allow for (vmcnt counts to 63)
+  constexpr int STORES = RT * NMT * 4 < 63 - (R - 2) * LW ? RT * NMT * 4 : 63 - (R - 2) * LW;
   static_assert((R - 2) * LW + STORES < 64, "vmcnt range");
   __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
   __shared__ int s_id[IDS ? kStreamIds : 1];
@@ -459,10 +460,13 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     __syncthreads();
   }
   // token rows past the end read the last one and are not stored
-  uint32_t xo[NMT == 4 ? 1 : NMT];
-  if (NMT == 4) {
-    const int r = w * 8 + (lane >> 3);
-    xo[0] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + ((lane & 7) ^ (lane >> 3)) * 16);
+  uint32_t xo[XL];
+  if (NMT % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < XL; ++v) {
+      const int r = (v * 8 + w) * 8 + (lane >> 3);
+      xo[v] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + ((lane & 7) ^ (lane >> 3)) * 16);
+    }
   } else {
 #pragma unroll
     for (int v = 0; v < NMT; ++v) {                  // two rows a load, a word a lane
@@ -488,8 +492,9 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
     const uint32_t to = base + lb * STAGE;
 #pragma unroll
     for (int v = 0; v < LR; ++v) load_to_lds_once(rw, wo[v], ks, to + (w * LR + v) * 1024);
-    if (NMT == 4) {
-      load_to_lds(rx, xo[0], ks, to + XOFF + w * 1024);
+    if (NMT % 4 == 0) {
+#pragma unroll
+      for (int v = 0; v < XL; ++v) load_to_lds(rx, xo[v], ks, to + XOFF + (v * 8 + w) * 1024);
     } else {
 #pragma unroll
       for (int v = 0; v < NMT; ++v) load_word_to_lds(rx, xo[v], ks, to + XOFF + (v * 8 + w) * 256);
@@ -979,9 +984,12 @@ void launch_few_of(const Product& p, int B, hipStream_t stream) {
 // against 10.7, 10000 13.3 against 11.4); up to 16384 (one pass of eight-row
 // units) the stream of those (M = 60, d = 3584: 16000 channels 15.0 us against
 // 21.1 with taller units, 30000 28.8 against 23.9); then the taller units.
-// More tokens take tiles, of 128 tokens up to 128 and of 256 beyond
-// (151936 channels, d = 3584: 128 tokens 149 against 168 us, 129 202 against
-// 167).  With at most 64 channels the two sides change places.
+// Up to 128 tokens over more than 65536 channels the stream still is the faster
+// (151936 channels, d = 3584: 65 tokens 128 against 144 us in tiles, 128 138
+// against 151; d = 4096: 128 tokens, 128256 channels 109 against 138, 60000 as
+// fast, 20000 40 against 32).  More tokens take tiles, of 128 tokens up to 128
+// and of 256 beyond (151936 channels, d = 3584: 128 tokens 149 against 168 us,
+// 129 202 against 167).  With at most 64 channels the two sides change places.
 template <int OT>
 void launch_product(Product p, hipStream_t stream) {
   if (p.M > 64 && p.N <= 64) {
@@ -1005,6 +1013,8 @@ void launch_product(Product p, hipStream_t stream) {
     }
   } else if (p.M <= 64) {
     launch_few_of<OT>(p, 1, stream);
+  } else if (p.M <= 128 && p.N > 65536 && span < 0x7FFFFFFFull) {
+    launch_stream<OT, 8, 32, 3>(p, stream);
   } else if (p.M > 128) {
     launch_tiled<OT, 4>(p, stream);
   } else {

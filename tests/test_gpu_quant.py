@@ -162,6 +162,8 @@ MATMUL = [(1, 1, 1, "fp32", None, 0), (1, 17, 130, "bf16", 20, 1), (3, 64, 128, 
           (9, 4097, 256, "bf16", 4099, 1), (20, 9001, 1000, "fp32", None, 0), (40, 16384, 384, "bf16", None, 0),
           (61, 5003, 129, "fp16", 5003, 1), (10, 16390, 512, "fp32", 16401, 3), (31, 17001, 300, "bf16", None, 0),
           (47, 20011, 128, "fp16", 20012, 0), (64, 33333, 640, "bf16", 33333, 1), (64, 16385, 2048, "fp32", None, 0),
+          # up to 128 tokens over many channels
+          (65, 65537, 128, "fp32", None, 0), (100, 70003, 384, "bf16", 70003, 1), (128, 66000, 256, "fp16", None, 0),
           # few channels: the sides change places
           (65, 1, 128, "fp32", None, 0), (300, 7, 200, "bf16", 9, 1), (1000, 64, 512, "fp32", 70, 1),
           (5000, 33, 384, "fp16", None, 0), (20000, 17, 256, "bf16", 17, 0)]

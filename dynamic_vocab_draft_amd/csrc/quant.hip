@@ -778,7 +778,12 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
   constexpr int BATCH = NMT == 1 ? 8 : 4;            // operands of a row in flight
   __shared__ i32x4 sh[8][NMT][NS_WAVE];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int m0 = (int)blockIdx.z * NMT * 16;         // tokens in groups
+  p.x += (size_t)m0 * p.pitch;
+  p.xs += m0;
+  p.out = (char*)p.out + (size_t)m0 * (size_t)p.sm * (OT == NS_FP32 ? 4 : 2);
   const size_t seq = blockIdx.y;
+  const int M = p.M - m0;                            // tokens left, more than 64 of them or not
   const int j0 = (int)blockIdx.x * 16, j = j0 + i < p.N ? j0 + i : p.N - 1;
   // the count, the ids and the scales are asked for together; an id behind
   // the count or a hole reads some row, and nobody reads its output
@@ -790,7 +795,7 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = u * 16 + g * 4 + r;
-      xs[u][r] = p.xs[seq * p.M + (m < p.M ? m : p.M - 1)];
+      xs[u][r] = p.xs[seq * p.M + (m < M ? m : M - 1)];
     }
   NS_ISSUE_FENCE();
   n = n < p.N ? n : p.N;
@@ -803,7 +808,7 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
   const int8_t* xr[NMT];
 #pragma unroll
   for (int u = 0; u < NMT; ++u) {
-    const int m = u * 16 + i < p.M ? u * 16 + i : p.M - 1;
+    const int m = u * 16 + i < M ? u * 16 + i : M - 1;
     xr[u] = p.x + (seq * p.M + m) * p.pitch + g * 16;
   }
   i32x4 acc[NMT] = {};
@@ -837,7 +842,7 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = u * 16 + g * 4 + r;
-      if (m < p.M && j0 + i < n)
+      if (m < M && j0 + i < n)
         store_out<OT>(p.out, (seq * p.M + m) * (size_t)p.sm + (size_t)(j0 + i) * (size_t)p.sn, scaled(s[r], xs[u][r] * ws));
     }
   }
@@ -968,7 +973,8 @@ void launch_stream(const Product& p, hipStream_t stream) {
 
 template <int OT, int NMT>
 void launch_few(const Product& p, int B, hipStream_t stream) {
-  hipLaunchKernelGGL((k_product_few<OT, NMT>), dim3((unsigned)((p.N + 15) / 16), (unsigned)B), dim3(512), 0, stream, p);
+  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)B, (unsigned)((p.M + NMT * 16 - 1) / (NMT * 16)));
+  hipLaunchKernelGGL((k_product_few<OT, NMT>), grid, dim3(512), 0, stream, p);
 }
 
 template <int OT>
@@ -990,6 +996,10 @@ void launch_few_of(const Product& p, int B, hipStream_t stream) {
 // fast, 20000 40 against 32).  More tokens take tiles, of 128 tokens up to 128
 // and of 256 beyond (151936 channels, d = 3584: 128 tokens 149 against 168 us,
 // 129 202 against 167).  With at most 64 channels the two sides change places.
+// Where tiles would leave most CUs idle, more than 64 tokens also go to the
+// kernel for few rows, 64 at a time, up to 640 of its blocks (321 x 184 x 9508
+// 25 against 82 us, 128 x 4096 x 4096, 512 blocks, 23 against 26; 512 x 2048 x
+// 4096, 1024 blocks, 43 against 39).
 template <int OT>
 void launch_product(Product p, hipStream_t stream) {
   if (p.M > 64 && p.N <= 64) {
@@ -997,7 +1007,8 @@ void launch_product(Product p, hipStream_t stream) {
   }
   const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
                         (OT == NS_FP32 ? 4 : 2);
-  if (p.M <= 64 && p.N <= 4096) {
+  const int64_t few = (int64_t)((p.N + 15) / 16) * ((p.M + 63) / 64);   // blocks of the kernel for few rows
+  if ((p.M <= 64 && p.N <= 4096) || (p.M > 64 && few <= 640)) {
     launch_few_of<OT>(p, 1, stream);
   } else if (p.M <= 64 && span < 0x7FFFFFFFull) {    // the stream's output offsets have 31 bits
     if (p.N <= 16384) {

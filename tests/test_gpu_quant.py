@@ -194,6 +194,36 @@ def test_quant_matmul_special_scales(ns, M):
         torch.testing.assert_close(o.cpu(), want, rtol=0, atol=0, equal_nan=True)
 
 
+# more than 64 tokens: groups of 64 for few channels (the last group of one
+# token, or of 64), tiles of 128 and 256 tokens for more
+GROUPS = [(65, 65, 128, "fp32", None, 0), (128, 100, 300, "bf16", 101, 1), (129, 2001, 130, "fp16", 2003, 1),
+          (2305, 70, 200, "fp32", 75, 2), (8192, 80, 129, "bf16", None, 0), (321, 184, 9508, "bf16", 184, 1),
+          (128, 5120, 256, "fp32", None, 0), (128, 5121, 256, "fp32", 5125, 1), (70, 6001, 1000, "bf16", 6001, 1),
+          (127, 65535, 128, "fp16", None, 0), (640, 1030, 129, "fp32", 1033, 1), (129, 3905, 640, "bf16", None, 0),
+          (8193, 81, 384, "fp16", None, 0), (20001, 65, 128, "bf16", 66, 1)]
+
+
+@pytest.mark.parametrize("c", GROUPS, ids=lambda c: "x".join(str(v) for v in c))
+def test_quant_matmul_groups_of_tokens(ns, c):
+    check_matmul(ns, *c)
+
+
+@pytest.mark.parametrize("M,N", [(100, 5500), (300, 4100)])
+def test_quant_matmul_tiles_largest_sums_and_special_scales(ns, M, N):
+    check_matmul(ns, M, N, 2048, "fp32", extreme=True)
+    d = 200
+    xq, wq = int8_rows(M, d, 1), int8_rows(N, d, 2)
+    xs, ws = np.full(M, 0.5, np.float32), np.full(N, 0.25, np.float32)
+    xs[1], xs[M - 1], ws[7], ws[N - 1], ws[9] = np.nan, np.inf, np.nan, 0.0, 1e6
+    dev = lambda a: torch.from_numpy(a).cuda()
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = torch.from_numpy(replica(xq, xs, wq, ws))
+    for out in DT:
+        o = torch.empty((M, N), dtype=DT[out], device="cuda")
+        ns.nanospec_quant_matmul(dev(xq), dev(xs), dev(wq), dev(ws), d, o)
+        torch.testing.assert_close(o.cpu(), want.to(DT[out]), rtol=0, atol=0, equal_nan=True)
+
+
 def test_quant_no_rows(ns):
     z = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device="cuda")
     ns.nanospec_quant_rows(z(0, 64), z(0, 128, t=torch.int8), z(0))

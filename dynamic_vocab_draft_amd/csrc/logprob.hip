@@ -173,16 +173,22 @@ struct Best {
     cnt += n;
   }
 
-  // Collects the elements of a lane's vector x, ids from `id`, that reach `least`.
+  // Bit EPV - 1 - e: element e of a lane's vector reaches `least`.
   template <int ET>
-  __device__ __forceinline__ void take_vector(u32x4 x, int id, bool live, int lane) {
+  __device__ __forceinline__ uint32_t reach(u32x4 x, bool live) const {
     constexpr int EPV = per_vec(ET);
     float v[EPV];
     widen<ET>(x, v);
-    uint32_t m = 0;                                        // bit EPV - 1 - e: element e passes
+    uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < EPV; ++e) m = m + m + (v[e] >= least ? 1u : 0u);
-    m = live ? m : 0u;
+    return live ? m : 0u;
+  }
+
+  // Collects the elements of x that m marks, one of each lane a turn.
+  template <int ET>
+  __device__ __forceinline__ void collect(u32x4 x, int id, uint32_t m, int lane) {
+    constexpr int EPV = per_vec(ET);
 #pragma unroll 1
     while (__ballot(m != 0)) {                             // one turn, as a rule
       const int e = EPV - 1 - (__ffs(m) - 1) & (EPV - 1);  // of the lanes with any
@@ -191,6 +197,30 @@ struct Best {
       const float f = ET == NS_FP32 ? __uint_as_float(w) : elem_of<ET>(w >> (e & 1) * 16, 0);
       take(f, m != 0, id + e, lane);
       m &= m - 1;
+    }
+  }
+
+  // Collects what reaches `least` of the lanes' vectors x, ids from `id`.  Where
+  // that is more than the buffer holds (many equal or masked logits), lanes go
+  // in order of their ids, 64 elements at a time, each group raising the bound
+  // for the next: a row of equal logits costs one merge.
+  template <int ET>
+  __device__ __forceinline__ void take_vector(u32x4 x, int id, bool live, int lane) {
+    uint32_t m = reach<ET>(x, live);
+    const int n = __builtin_amdgcn_readlane(ns::wave_incl_scan(__popc(m), lane), NS_WAVE - 1);
+    if (cnt + n <= NS_WAVE) {                              // uniform
+      collect<ET>(x, id, m, lane);
+      return;
+    }
+    enter(lane);
+    constexpr int GROUP = NS_WAVE / per_vec(ET);
+#pragma unroll 1
+    for (int g = 0; g < NS_WAVE; g += GROUP) {
+      m = reach<ET>(x, live && lane / GROUP * GROUP == g);
+      if (!__ballot(m != 0)) continue;
+      collect<ET>(x, id, m, lane);
+      enter(lane);
+      raise();
     }
   }
 
@@ -228,7 +258,7 @@ struct Args {
   const void* z;
   int64_t ld;
   int L, V, S, k, T;
-  float t, c;                  // inverse temperature, and times log2(e)
+  float t, c, eps;             // inverse temperature, times log2(e), and what rounding took from c, relatively
   const int32_t* tokens;       // [L][T]
   float* logprob;              // [L][T]
   float* lse;
@@ -242,22 +272,26 @@ struct Args {
 // A row's outputs from its statistics.  logp = ln2 (y - log2 S) keeps the
 // digits that a rounded lse would lose.
 struct Row {
-  float t, c, ref, E, l2, lse, H;
+  float t, c, eps, ref, E, l2, lse, H;
   bool bad, none;
-  __device__ __forceinline__ Row(const Stat& s, const Args& a) : t(a.t), c(a.c) {
+  __device__ __forceinline__ Row(const Stat& s, const Args& a) : t(a.t), c(a.c), eps(a.eps) {
     bad = !(s.S < INFINITY) || s.top == INFINITY;
     none = s.S == 0.f;
     const float nan = __uint_as_float(0x7FC00000u);
     ref = s.ref;
     E = s.E;
-    l2 = log2f(s.S);
+    // c (1 + eps) is what c stands for.  The sum's large terms have c z close
+    // to E (c (z - ref) close to 0), so all of it is 2^(eps E) times as large.
+    const float l = log2f(s.S);
+    l2 = l + eps * E;
     lse = bad ? nan : (none ? -INFINITY : ref * t + kLn2 * (E + l2));
-    H = bad ? nan : (none ? 0.f : fmaxf(kLn2 * (l2 - s.W / s.S), 0.f));
+    H = bad ? nan : (none ? 0.f : fmaxf(kLn2 * (l - s.W / s.S), 0.f));
   }
   __device__ __forceinline__ float logp(float z) const {
     if (bad) return __uint_as_float(0x7FC00000u);
     if (none || z == -INFINITY) return -INFINITY;
-    const float y = ref == 0.f ? fmaf(z, c, -E) : (z - ref) * c - E;
+    const float y0 = ref == 0.f ? fmaf(z, c, -E) : (z - ref) * c - E;
+    const float y = y0 + eps * (y0 + E);
     // far from the rest (a mask of the type's lowest value) y's last digits
     // are nothing, but c z may overflow where t z does not
     return fabsf(y) < 0x1p24f ? kLn2 * (y - l2) : z * t - lse;
@@ -644,7 +678,7 @@ struct GradArgs {
   const void* z;
   int64_t ld;
   int L, V, T;
-  float t, c;
+  float t, c, eps;             // as in Args
   const int32_t* tokens;
   const float* lse;
   const float* entropy;        // or NULL
@@ -715,7 +749,8 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(GradArgs a, int 
   // a row without logits, or whose float32 lse no longer resolves probabilities
   s.zero = fabsf(lse) > 0x1p24f;
   s.L = lse * kLog2e;
-  const float low = (float)((double)lse * 1.4426950408889634 - (double)s.L);
+  // (c z is close to L wherever p is not small, so c's own rounding is eps L)
+  const float low = (float)((double)lse * 1.4426950408889634 - (double)s.L) - a.eps * s.L;
   const float f = exp2_fast(-low);
   s.B = -a.t * gH * kLn2 * f;
   s.A = a.t * (gl - sum - gH * H) * f - s.B * low;
@@ -827,6 +862,7 @@ int nanospec_token_logprobs(const void* logits, int64_t ld, int32_t L, int32_t V
   a.T = T;
   a.t = inv_temp;
   a.c = (float)((double)inv_temp * 1.4426950408889634);
+  a.eps = (float)((double)inv_temp * 1.4426950408889634 / a.c - 1.0);
   a.tokens = tokens;
   a.logprob = logprob;
   a.lse = lse;
@@ -852,8 +888,9 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
   if (!elem_aligned(logits, dtype) || !elem_aligned(dlogits, dtype)) return NS_EINVAL;
   if (dlogits == logits && ld_d != ld) return NS_EINVAL;
   (void)hipGetLastError();
-  const GradArgs a{logits, ld, L, V, T, inv_temp, (float)((double)inv_temp * 1.4426950408889634), tokens, lse, entropy,
-                   g_logprob, g_entropy, g_lse, dlogits, ld_d};
+  const float c = (float)((double)inv_temp * 1.4426950408889634);
+  const GradArgs a{logits, ld, L, V, T, inv_temp, c, (float)((double)inv_temp * 1.4426950408889634 / c - 1.0), tokens,
+                   lse, entropy, g_logprob, g_entropy, g_lse, dlogits, ld_d};
   if (dtype == NS_BF16) launch_grad<NS_BF16>(a, stream);
   else if (dtype == NS_FP16) launch_grad<NS_FP16>(a, stream);
   else launch_grad<NS_FP32>(a, stream);

@@ -166,6 +166,20 @@ def test_ties_go_to_the_lowest_id(ns, V, k):
         check(ns, z, 1.0, tokens_for(L, V, 1, 3), k, f"rising V={V} k={k} L={L}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [1, 20, 64])
+def test_many_equal_logits(ns, dtype, k):
+    """Runs of equal logits, in rising and falling steps, among masked ones and alone: more reach the bound than fit."""
+    V = 20011
+    rng = np.random.default_rng(k)
+    ids = np.arange(V)
+    rows = [np.full(V, -np.inf), np.full(V, 7.0), ids // 600 * 0.25, -(ids // 600) * 0.25, ids // 70 % 3 * 1.0,
+            np.where(rng.random(V) < 0.5, -np.inf, 1.0), np.where(ids < V - 40, -np.inf, 1.0),
+            np.where(rng.random(V) < 0.002, 2.0, 1.0), np.where(ids % 8 == 7, 3.0, -1.0), np.where(ids % 512 < 100, 4.0, 4.25)]
+    z = torch.from_numpy(np.stack(rows * 230 if k == 20 else rows).astype(np.float32)).to(DT[dtype]).cuda()
+    check(ns, z, 1.0, tokens_for(z.shape[0], V, 2, 5), k, f"equal logits {dtype} k={k}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("L", [6, 2104])
 @pytest.mark.parametrize("V", [70, 4100, 9001])

@@ -107,14 +107,75 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
   return ((uint64_t)hi << 32) | lo;
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xf, 0xf, true);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// The value of lane ^ M; within rows of 16 lanes by lane moves, without LDS's latency.
+template <int M>
+__device__ __forceinline__ uint64_t lane_xor_u64(uint64_t v) {
+  if constexpr (M == 1) return dpp_u64<0xB1>(v);           // quad_perm 1 0 3 2
+  else if constexpr (M == 2) return dpp_u64<0x4E>(v);      // quad_perm 2 3 0 1
+  else if constexpr (M == 4) return dpp_u64<0x1B>(dpp_u64<0x141>(v));   // row_half_mirror, quad_perm 3 2 1 0
+  else if constexpr (M == 8) return dpp_u64<0x128>(v);     // row_ror:8
+  else return ns::shfl_xor_u64(v, M);
+}
+
+template <int M>
+__device__ __forceinline__ uint64_t exchange(uint64_t x, int lane) {
+  const uint64_t o = lane_xor_u64<M>(x);
+  return ((lane & M) == 0) == (x > o) ? x : o;
+}
+
+// The 64 largest of two sorted lists, one key a lane: a holds one in falling
+// order, b the other in rising order; the larger of each pair is a bitonic
+// sequence, which six exchanges sort.
+__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane) {
+  uint64_t x = a > b ? a : b;
+  x = exchange<32>(x, lane);
+  x = exchange<16>(x, lane);
+  x = exchange<8>(x, lane);
+  x = exchange<4>(x, lane);
+  x = exchange<2>(x, lane);
+  return exchange<1>(x, lane);
+}
+
+// The value of lane ^ (2 M - 1).
+template <int M>
+__device__ __forceinline__ uint64_t lane_mirror_u64(uint64_t v) {
+  if constexpr (M == 1) return dpp_u64<0xB1>(v);           // quad_perm 1 0 3 2
+  else if constexpr (M == 2) return dpp_u64<0x1B>(v);      // quad_perm 3 2 1 0
+  else if constexpr (M == 4) return dpp_u64<0x141>(v);     // row_half_mirror
+  else if constexpr (M == 8) return dpp_u64<0x140>(v);     // row_mirror
+  else return ns::shfl_xor_u64(v, 2 * M - 1);
+}
+
+// Two sorted runs of M lanes, side by side, to one of 2 M.
+template <int M>
+__device__ __forceinline__ uint64_t join_runs(uint64_t x, int lane) {
+  const uint64_t o = lane_mirror_u64<M>(x);
+  x = ((lane & M) == 0) == (x > o) ? x : o;
+  if constexpr (M >= 32) x = exchange<16>(x, lane);
+  if constexpr (M >= 16) x = exchange<8>(x, lane);
+  if constexpr (M >= 8) x = exchange<4>(x, lane);
+  if constexpr (M >= 4) x = exchange<2>(x, lane);
+  if constexpr (M >= 2) x = exchange<1>(x, lane);
+  return x;
+}
+
 // ---------------------------------------------------------------------------
 // The best k keys of a wave: lane r holds the r-th (0: none yet).  The
 // elements of a batch that reach the k-th value so far are collected in LDS,
-// then enter the list: a few one by one (a comparison's ballot is the rank,
-// the lanes behind it shift), more in one merge (every lane counts the keys
-// above its own two, which does not wait for each candidate in turn: eight
-// rows of 128256 float32 logits, k = 64, 78 -> 59 us a call).  Ids rise from
-// batch to batch, so a later element that only ties the k-th value loses to it.
+// one of each lane a turn, then enter the list: one or two in turn, up to 16 by
+// counting (every lane counts the keys above its own two; no candidate waits
+// for the one before it), more by sorting them and merging the two lists (eight
+// rows of 128256 float32 logits, k = 64, 37 -> 31 us a call, 700 of 4000 40 ->
+// 30).  The turns run over a whole batch at once, not over each vector (eight
+// rows, k = 8, 13.5 -> 12.4).  Ids rise from batch to batch, so a later element
+// that only ties the k-th value loses to it.
 // ---------------------------------------------------------------------------
 struct Best {
   uint64_t* buf;       // NS_WAVE candidates
@@ -123,35 +184,47 @@ struct Best {
   float least;         // elements below it cannot be among the k best
   bool fresh;          // nothing seen yet
 
-  // c is the same in every lane
-  __device__ __forceinline__ void insert(uint64_t c, int lane) {
-    const int r = __popcll(__ballot(key > c));
-    if (r >= k) return;                                    // uniform
-    // wave_shr:1, the key of the lane before
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)key, 0x138, 0xf, 0xf, false);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(key >> 32), 0x138, 0xf, 0xf, false);
-    const uint64_t before = ((uint64_t)hi << 32) | lo;
-    key = lane < r ? key : (lane == r ? c : before);
+  // Enters the keys c of the lanes of `ball`, each in turn: a ballot is the rank,
+  // the lanes behind it shift.
+  __device__ __forceinline__ void insert(unsigned long long ball, uint64_t c, int lane) {
+#pragma unroll 1
+    while (ball) {                                         // uniform
+      const uint64_t o = lane_u64(c, __ffsll(ball) - 1);
+      ball &= ball - 1;
+      const int r = __popcll(__ballot(key > o));
+      // wave_shr:1, the key of the lane before
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)key, 0x138, 0xf, 0xf, false);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(key >> 32), 0x138, 0xf, 0xf, false);
+      const uint64_t before = ((uint64_t)hi << 32) | lo;
+      key = lane < r ? key : (lane == r ? o : before);
+    }
   }
 
   // Empties the collected candidates into the list.
   __device__ __forceinline__ void enter(int lane) {
     wave_sync();
-    const uint64_t c = lane < cnt ? buf[lane] : 0;
-    if (cnt <= 4) {                                        // uniform
-      for (int p = 0; p < cnt; ++p) insert(lane_u64(c, p), lane);
+    uint64_t c = lane < cnt ? buf[lane] : 0;
+    if (cnt <= 2) {                                        // uniform
+      insert((1ull << cnt) - 1, c, lane);
+    } else if (cnt > 16) {
+      c = join_runs<1>(c, lane);
+      c = join_runs<2>(c, lane);
+      c = join_runs<4>(c, lane);
+      c = join_runs<8>(c, lane);
+      c = join_runs<16>(c, lane);
+      c = join_runs<32>(c, lane);
+      key = merge_lists(key, ns::shfl_xor_u64(c, NS_WAVE - 1), lane);
     } else {
-      int rk = lane, rc = 0, above = 0;                    // ranks of key and c; list keys above c
+      int rk = lane, rc = 0;                               // ranks of key and c
+#pragma unroll 1
       for (int p = 0; p < cnt; p += 4)                     // those past cnt are 0, above nothing
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint64_t o = lane_u64(c, p + e);
-          const unsigned long long more = __ballot(key > o);
+          const int above = __popcll(__ballot(key > o));   // list keys above candidate p + e
           rk += key < o;
-          rc += c < o;
-          above = lane == p + e ? __popcll(more) : above;
+          rc += (c < o) + (lane == p + e ? above : 0);
         }
-      rc += above;
       wave_sync();
       buf[lane] = 0;
       wave_sync();
@@ -164,63 +237,87 @@ struct Best {
     cnt = 0;
   }
 
-  // Collects one element of each lane that passes.
-  __device__ __forceinline__ void take(float v, bool pass, int id, int lane) {
-    const unsigned long long ball = __ballot(pass);
-    const int n = __popcll(ball);
-    if (cnt + n > NS_WAVE) enter(lane);                    // uniform
-    if (pass) buf[cnt + __popcll(ball & ((1ull << lane) - 1))] = ns::make_key(v, id);
-    cnt += n;
-  }
-
-  // Bit EPV - 1 - e: element e of a lane's vector reaches `least`.
+  // Bit u * EPV + e: element e of a lane's vector u reaches `least`.
   template <int ET>
-  __device__ __forceinline__ uint32_t reach(u32x4 x, bool live) const {
+  __device__ __forceinline__ uint32_t reach(const u32x4 (&x)[kUnroll], const float (&mx)[kUnroll], int q, int q1) const {
     constexpr int EPV = per_vec(ET);
-    float v[EPV];
-    widen<ET>(x, v);
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) m = m + m + (v[e] >= least ? 1u : 0u);
-    return live ? m : 0u;
+    for (int u = kUnroll - 1; u >= 0; --u) {
+      float v[EPV];
+      widen<ET>(x[u], v);
+      m <<= EPV;
+      if (!__ballot(mx[u] >= least)) continue;             // uniform
+      uint32_t part = 0;
+#pragma unroll
+      for (int e = EPV - 1; e >= 0; --e) part = part + part + (v[e] >= least ? 1u : 0u);
+      m |= part;
+    }
+    // vectors past the end are of the part's last lanes and rounds
+    const int n = (q1 - q + NS_WAVE - 1) / NS_WAVE;        // vectors of this lane, q its first
+    return n >= kUnroll ? m : (n <= 0 ? 0u : m & ((1u << n * EPV) - 1));
   }
 
-  // Collects the elements of x that m marks, one of each lane a turn.
+  // One turn: collects the lowest marked element of each lane.
   template <int ET>
-  __device__ __forceinline__ void collect(u32x4 x, int id, uint32_t m, int lane) {
+  __device__ __forceinline__ void collect(const u32x4 (&x)[kUnroll], int q, uint32_t& m, unsigned long long ball, int lane) {
     constexpr int EPV = per_vec(ET);
-#pragma unroll 1
-    while (__ballot(m != 0)) {                             // one turn, as a rule
-      const int e = EPV - 1 - (__ffs(m) - 1) & (EPV - 1);  // of the lanes with any
-      const int word = ET == NS_FP32 ? e : e >> 1;
-      const uint32_t a = word & 1 ? x.y : x.x, b = word & 1 ? x.w : x.z, w = word & 2 ? b : a;
-      const float f = ET == NS_FP32 ? __uint_as_float(w) : elem_of<ET>(w >> (e & 1) * 16, 0);
-      take(f, m != 0, id + e, lane);
-      m &= m - 1;
+    const int b = (__ffs(m) - 1) & (kUnroll * EPV - 1), word = ET == NS_FP32 ? b : b >> 1;
+    uint32_t w[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t lo = word & 1 ? x[u].y : x[u].x, hi = word & 1 ? x[u].w : x[u].z;
+      w[u] = word & 2 ? hi : lo;
     }
+    const uint32_t lo = word & 4 ? w[1] : w[0], hi = word & 4 ? w[3] : w[2], v = word & 8 ? hi : lo;
+    const float f = ET == NS_FP32 ? __uint_as_float(v) : elem_of<ET>(v >> (b & 1) * 16, 0);
+    if (m != 0) buf[cnt + __popcll(ball & ((1ull << lane) - 1))] = ns::make_key(f, (q + b / EPV * NS_WAVE) * EPV + b % EPV);
+    cnt += __popcll(ball);
+    m &= m - 1;
   }
 
-  // Collects what reaches `least` of the lanes' vectors x, ids from `id`.  Where
-  // that is more than the buffer holds (many equal or masked logits), lanes go
-  // in order of their ids, 64 elements at a time, each group raising the bound
-  // for the next: a row of equal logits costs one merge.
+  // Takes what reaches `least` of a batch's vectors, q the lane's first.
+  // Where that is more than the buffer holds (many equal or masked logits, a
+  // first batch with a large k), lanes go in order of their ids, 64 elements at
+  // a time, each group raising the bound for the next: a row of equal logits
+  // costs one merge.
   template <int ET>
-  __device__ __forceinline__ void take_vector(u32x4 x, int id, bool live, int lane) {
-    uint32_t m = reach<ET>(x, live);
-    const int n = __builtin_amdgcn_readlane(ns::wave_incl_scan(__popc(m), lane), NS_WAVE - 1);
-    if (cnt + n <= NS_WAVE) {                              // uniform
-      collect<ET>(x, id, m, lane);
-      return;
-    }
-    enter(lane);
-    constexpr int GROUP = NS_WAVE / per_vec(ET);
+  __device__ __forceinline__ void take_batch(const u32x4 (&x)[kUnroll], const float (&mx)[kUnroll], int q, int q1, int lane) {
+    constexpr int EPV = per_vec(ET), GROUP = NS_WAVE / EPV;
+    uint32_t m = reach<ET>(x, mx, q, q1);
+    bool fits = true;
 #pragma unroll 1
-    for (int g = 0; g < NS_WAVE; g += GROUP) {
-      m = reach<ET>(x, live && lane / GROUP * GROUP == g);
-      if (!__ballot(m != 0)) continue;
-      collect<ET>(x, id, m, lane);
-      enter(lane);
+    while (true) {
+      const unsigned long long ball = __ballot(m != 0);
+      if (!ball) break;
+      fits = cnt + __popcll(ball) <= NS_WAVE;              // uniform
+      if (!fits) break;
+      collect<ET>(x, q, m, ball, lane);
+    }
+    if (!fits) cnt = 0;
+    int u = fits ? kUnroll : 0, from = 0;                  // next: the lanes from `from` on of vector u
+#pragma unroll 1
+    while (true) {
+      if (u < kUnroll) {
+        m = lane >= from ? reach<ET>(x, mx, q, q1) & (((1u << EPV) - 1) << u * EPV) : 0u;
+        const int n = __builtin_amdgcn_readlane(ns::wave_incl_scan(__popc(m), lane), NS_WAVE - 1);
+        const bool all = cnt + n <= NS_WAVE;
+        if (all || cnt == 0) {
+          if (!all && lane >= from + GROUP) m = 0;
+#pragma unroll 1
+          while (true) {
+            const unsigned long long ball = __ballot(m != 0);
+            if (!ball) break;
+            collect<ET>(x, q, m, ball, lane);
+          }
+          from = all ? 0 : (from + GROUP) & (NS_WAVE - 1);
+          u += from == 0;
+          if (all) continue;
+        }
+      }
+      if (cnt > 0) enter(lane);
       raise();
+      if (u == kUnroll) break;
     }
   }
 
@@ -231,8 +328,8 @@ struct Best {
   }
 
   // A bound before any key is held, from the lanes' maxima m: a value that at
-  // least k of them reach, by bisection of the ordered bits.  16 halvings come
-  // close to the k-th largest; the exact one would save next to nothing.
+  // least k of them reach, by bisection of the ordered bits.  It ends within a
+  // hundredth of the k-th largest; the exact one would save next to nothing.
   __device__ __forceinline__ void start(float m, int lane) {
     fresh = false;
     const uint32_t o = m == m ? ns::ord_f32(m) : 0u;       // NaN: no bound
@@ -245,7 +342,7 @@ struct Best {
       if (__popcll(__ballot(o >= near)) >= k) lo = near;
     }
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
+    for (int i = lo != 0 ? 8 : 16; i > 0; --i) {
       const uint32_t mid = lo + (hi - lo) / 2;
       if (__popcll(__ballot(o >= mid)) >= k) lo = mid;
       else hi = mid;
@@ -385,16 +482,7 @@ __device__ __forceinline__ void take(const u32x4 (&x)[kUnroll], int q0, int q1, 
   st.W += W;
   if (TOP) {
     if (best.fresh) best.start(lane_max, lane);
-    if (top >= best.least) {                               // uniform
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (!__ballot(mx[u] >= best.least)) continue;
-        const int q = q0 + u * NS_WAVE + lane;
-        best.take_vector<ET>(x[u], q * EPV, q < q1, lane);
-      }
-      best.enter(lane);
-      best.raise();
-    }
+    if (top >= best.least) best.take_batch<ET>(x, mx, q0 + lane, q1, lane);   // uniform
   }
 }
 
@@ -462,8 +550,7 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
     s.W = ns::wave_sum_f32(s.W);
     st = join(st, s, a.c);
     if (TOP) {
-      best.take(v, live && v == v, e, lane);
-      best.enter(lane);
+      best.insert(__ballot(live && v >= best.least), ns::make_key(v, e), lane);
     }
   } else {
     st.S = ns::wave_sum_f32(st.S);
@@ -482,42 +569,6 @@ __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
     if (lane == 0) a.stat[item] = st;
     if (TOP && lane < a.k) a.keys[item * a.k + lane] = key;
   }
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xf, 0xf, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xf, 0xf, true);
-  return ((uint64_t)hi << 32) | lo;
-}
-
-// The value of lane ^ M; within rows of 16 lanes by lane moves, without LDS's latency.
-template <int M>
-__device__ __forceinline__ uint64_t lane_xor_u64(uint64_t v) {
-  if constexpr (M == 1) return dpp_u64<0xB1>(v);           // quad_perm 1 0 3 2
-  else if constexpr (M == 2) return dpp_u64<0x4E>(v);      // quad_perm 2 3 0 1
-  else if constexpr (M == 4) return dpp_u64<0x1B>(dpp_u64<0x141>(v));   // row_half_mirror, quad_perm 3 2 1 0
-  else if constexpr (M == 8) return dpp_u64<0x128>(v);     // row_ror:8
-  else return ns::shfl_xor_u64(v, M);
-}
-
-template <int M>
-__device__ __forceinline__ uint64_t exchange(uint64_t x, int lane) {
-  const uint64_t o = lane_xor_u64<M>(x);
-  return ((lane & M) == 0) == (x > o) ? x : o;
-}
-
-// The 64 largest of two sorted lists, one key a lane: a holds one in falling
-// order, b the other in rising order; the larger of each pair is a bitonic
-// sequence, which six exchanges sort.
-__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane) {
-  uint64_t x = a > b ? a : b;
-  x = exchange<32>(x, lane);
-  x = exchange<16>(x, lane);
-  x = exchange<8>(x, lane);
-  x = exchange<4>(x, lane);
-  x = exchange<2>(x, lane);
-  return exchange<1>(x, lane);
 }
 
 // The same for four lists of 16, one in each row of lanes: every row ends with the 16 largest of all.

@@ -766,8 +766,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
 }
 
 // ---------------------------------------------------------------------------
-// The product for few channel rows and up to 64 token rows: bound by latency.
-// A block of eight waves owns 16 channel rows and all token rows; each wave
+// The product for few channel rows: bound by latency.  A block of eight waves
+// owns 16 channel rows and up to 64 token rows (blockIdx.z of them); each wave
 // takes an eighth of the row's bytes, asks for all of its operands at once
 // and multiplies; the eight sums are joined in LDS.  One block pulls 64 KB of
 // a 4096-byte row set in about a microsecond, and 63 blocks of a thousand
@@ -783,7 +783,7 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
   p.xs += m0;
   p.out = (char*)p.out + (size_t)m0 * (size_t)p.sm * (OT == NS_FP32 ? 4 : 2);
   const size_t seq = blockIdx.y;
-  const int M = p.M - m0;                            // tokens left, more than 64 of them or not
+  const int M = p.M - m0;                            // tokens from here on
   const int j0 = (int)blockIdx.x * 16, j = j0 + i < p.N ? j0 + i : p.N - 1;
   // the count, the ids and the scales are asked for together; an id behind
   // the count or a hole reads some row, and nobody reads its output

@@ -589,8 +589,9 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
 // A block of eight waves owns 256 channel rows and TB * 64 token rows of the
 // output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
 // token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
-// in stages of 128 bytes a row, two in LDS (64 KB each with TB = 4), filled by
-// direct global-to-LDS loads.  While one half of a stage (64 bytes a row) is
+// in stages of 128 bytes a row, two in LDS (68 KB each with TB = 4), three with
+// TB = 1, whose short stages end before a load does (256 x 16384 x 4096, a tile
+// a CU: 29.5 -> 25.3 us), filled by direct global-to-LDS loads.  While one half of a stage (64 bytes a row) is
 // multiplied, the next half is read into a second set of registers; once a
 // wave holds a stage's second half and the next stage has landed, one block
 // barrier frees the stage's place for the stage after next.
@@ -613,6 +614,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
 // ---------------------------------------------------------------------------
 constexpr int kTileN = 256;                        // channel rows of a block
 constexpr int kTileThreads = 512;
+constexpr int tile_stages(int tb) { return tb == 1 ? 3 : 2; }   // in LDS
 constexpr int kEightRows = 9 * kStageK;            // eight channel rows in LDS and 128 bytes between them and the next
 
 template <int OT, int TB>
@@ -621,7 +623,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
   constexpr int XOFF = kTileN / 8 * kEightRows, STAGE = XOFF + TM * kStageK;
   constexpr int LA = kTileN / 64, LB = TM / 64;    // loads of a wave and stage: 8 rows each
   constexpr int STORES = TB * 4 * (OT == NS_FP32 ? 2 : 1);   // of a wave and whole tile
-  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE + 2 * 2048];
+  constexpr int R = tile_stages(TB), AHEAD = (R - 2) * (LA + LB);   // loads that may be out when a stage must be here
+  static_assert(AHEAD + STORES < 64, "vmcnt range");
+  // scales of the tile that is multiplied and, with one stage a tile, of R more
+  __shared__ __attribute__((aligned(16))) char lds[R * STAGE + (R + 1) * 2048];
   const int total = tiles_m * tiles_n, per = (total + 7) / 8, slots = (int)(gridDim.x >> 3);
   const int first = (int)(blockIdx.x & 7) * per, end = first + per < total ? first + per : total;
   int tile = first + (int)(blockIdx.x >> 3);
@@ -637,7 +642,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
   const uint32_t base = lds_offset(lds);
 
   // The stream of loads: stage `lk` of tile `lt` comes next.
-  int lt = tile, lk = 0, parity = 0;
+  int lt = tile, lk = 0, to_scales = 0;
   u32x4 ra, rb, rs;
   int last_a, last_b, last_s;                      // rows past the end read the last one and are not stored
   const auto aim = [&]() {
@@ -666,8 +671,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
       int l = lane;
       asm volatile("" : "+v"(l));
       const int q = (w & 3) * 64 + l;
-      load_word_to_lds(rs, (uint32_t)(q < last_s ? q : last_s) * 4, 0, base + 2 * STAGE + parity * 2048 + w * 256);
-      parity ^= 1;
+      load_word_to_lds(rs, (uint32_t)(q < last_s ? q : last_s) * 4, 0, base + R * STAGE + to_scales * 2048 + w * 256);
+      to_scales = to_scales == R ? 0 : to_scales + 1;
     }
     if (++lk == S) {                               // behind the last tile the stream reads that tile again,
       lk = 0;                                      // which spares every load a question
@@ -690,12 +695,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
   const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
   aim();
 #pragma unroll
-  for (int buf = 0; buf < 2; ++buf) {
+  for (int buf = 0; buf < R; ++buf) {
 #pragma unroll
     for (int u = 0; u < LA + LB; ++u) load(u, buf);
     advance();
   }
-  wait_loads<0>();
+  wait_loads<AHEAD + LA + LB>();
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -728,21 +733,22 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
     for (int s = 0; s < S; ++s) {
       step(0, b * STAGE + place1, false, 0);
       __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0): this wave has read the stage
-      if (s == 0 && stored) wait_loads<STORES>();
-      else wait_loads<0>();
+      if (s == 0 && stored) wait_loads<AHEAD + STORES>();
+      else wait_loads<AHEAD>();
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      step(1, (1 - b) * STAGE + place0, true, b);
+      const int next = b + 1 == R ? 0 : b + 1;
+      step(1, next * STAGE + place0, true, b);
       advance();
-      b ^= 1;
+      b = next;
     }
     int m0, n0, l = lane;
     asm volatile("" : "+v"(l));                    // as in issue
     const int ni = (l & 15) * 8, mg = (l >> 4) * 4;
     origin(tile, m0, n0);
-    const float* sw = (const float*)(lds + 2 * STAGE + scales * 2048) + wr * 128 + ni;
-    const float* sx = (const float*)(lds + 2 * STAGE + scales * 2048) + 256 + wc * TB * 16 + mg;
-    scales ^= 1;
+    const float* sw = (const float*)(lds + R * STAGE + scales * 2048) + wr * 128 + ni;
+    const float* sx = (const float*)(lds + R * STAGE + scales * 2048) + 256 + wc * TB * 16 + mg;
+    scales = scales == R ? 0 : scales + 1;
     float ws[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) ws[e] = sw[e];
@@ -997,13 +1003,16 @@ void launch_few_of(const Product& p, int B, hipStream_t stream) {
 // Up to 128 tokens over more than 65536 channels the stream still is the faster
 // (151936 channels, d = 3584: 65 tokens 128 against 144 us in tiles, 128 138
 // against 151; d = 4096: 128 tokens, 128256 channels 109 against 138, 60000 as
-// fast, 20000 40 against 32).  More tokens take tiles, of 128 tokens up to 128
-// and of 256 beyond (151936 channels, d = 3584: 128 tokens 149 against 168 us,
-// 129 202 against 167).  With at most 64 channels the two sides change places.
-// Where tiles would leave most CUs idle, more than 64 tokens also go to the
-// kernel for few rows, 64 at a time, up to 640 of its blocks (321 x 184 x 9508
-// 25 against 82 us, 128 x 4096 x 4096, 512 blocks, 23 against 26; 512 x 2048 x
-// 4096, 1024 blocks, 43 against 39).
+// fast, 20000 40 against 32).  With at most 64 channels the
+// two sides change places.  More than 64 tokens over few channels also go to
+// the kernel for few rows, 64 at a time, up to a block a CU (321 x 184 x 9508
+// 25 us against 82 in tiles of 256 tokens; 100 x 2000 x 16384, 250 blocks, 39
+// against 98; 128 x 2560 x 4096, 320 blocks, 21.9 against 20.0 in tiles of 64).
+// The rest takes tiles of 256, 128 or 64 tokens.  Blocks take one tile each a
+// round, and a round takes about 42, 30 and 22 us at d = 4096 (256 x 16384,
+// one round each: 43.1, 31.6, 25.3); the sum over the rounds decides (1000 x
+// 8000 x 4096, rounds 1, 1 and 2: 48.4, 37.1, 46.9; 3000 x 10000 x 500, rounds
+// 2, 4 and 8: 24.8, 26.9, 35.6; 4096 x 128256 x 4096 1665, 2073, 2694).
 template <int OT>
 void launch_product(Product p, hipStream_t stream) {
   if (p.M > 64 && p.N <= 64) {
@@ -1012,7 +1021,7 @@ void launch_product(Product p, hipStream_t stream) {
   const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
                         (OT == NS_FP32 ? 4 : 2);
   const int64_t few = (int64_t)((p.N + 15) / 16) * ((p.M + 63) / 64);   // blocks of the kernel for few rows
-  if ((p.M <= 64 && p.N <= 4096) || (p.M > 64 && few <= 640)) {
+  if ((p.M <= 64 && p.N <= 4096) || (p.M > 64 && few <= 256)) {
     launch_few_of<OT>(p, 1, stream);
   } else if (p.M <= 64 && span < 0x7FFFFFFFull) {    // the stream's output offsets have 31 bits
     if (p.N <= 16384) {
@@ -1030,10 +1039,15 @@ void launch_product(Product p, hipStream_t stream) {
     launch_few_of<OT>(p, 1, stream);
   } else if (p.M <= 128 && p.N > 65536 && span < 0x7FFFFFFFull) {
     launch_stream<OT, 8, 32, 3>(p, stream);
-  } else if (p.M > 128) {
-    launch_tiled<OT, 4>(p, stream);
   } else {
-    launch_tiled<OT, 2>(p, stream);
+    const auto time = [&](int tb, int round) {
+      const int64_t tiles = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.M + tb * 64 - 1) / (tb * 64));
+      return (tiles + 255) / 256 * round;
+    };
+    const int64_t t4 = time(4, 21), t2 = time(2, 15), t1 = time(1, 11);
+    if (t4 <= t2 && t4 <= t1) launch_tiled<OT, 4>(p, stream);
+    else if (t2 <= t1) launch_tiled<OT, 2>(p, stream);
+    else launch_tiled<OT, 1>(p, stream);
   }
 }
 

@@ -203,6 +203,18 @@ GROUPS = [(65, 65, 128, "fp32", None, 0), (128, 100, 300, "bf16", 101, 1), (129,
           (8193, 81, 384, "fp16", None, 0), (20001, 65, 128, "bf16", 66, 1)]
 
 
+# tiles of 64, 128 and 256 tokens, one a block and several, with sums of one, two, three and more stages
+TILES = [(300, 70000, 128, "bf16", None, 0), (513, 33001, 100, "fp32", None, 0), (2049, 9000, 128, "fp16", 9001, 1),
+         (1500, 12000, 256, "bf16", None, 0), (700, 20000, 384, "fp32", 20003, 3), (256, 16384, 128, "fp32", None, 0),
+         (129, 20000, 300, "bf16", None, 0), (200, 60000, 200, "bf16", 60000, 0), (66, 17000, 640, "fp16", None, 0),
+         (1000, 8000, 130, "fp32", None, 0), (4097, 4099, 64, "bf16", 4101, 1), (150, 150000, 128, "bf16", None, 0)]
+
+
+@pytest.mark.parametrize("c", TILES, ids=lambda c: "x".join(str(v) for v in c))
+def test_quant_matmul_rounds_of_tiles(ns, c):
+    check_matmul(ns, *c)
+
+
 @pytest.mark.parametrize("c", GROUPS, ids=lambda c: "x".join(str(v) for v in c))
 def test_quant_matmul_groups_of_tokens(ns, c):
     check_matmul(ns, *c)

@@ -39,43 +39,39 @@ template <int ET>
 struct Eight {
   u32x4 v[ET == NS_FP32 ? 2 : 1];
 
-  // elements i .. i + 7 of a row, zeros at or past d
-  __device__ __forceinline__ void load(const char* row, int i, int d) {
+  // elements i .. i + 7 of a row, or i .. i + 3 and `step` on, zeros at or past
+  // d.  `tail` is d rounded down to a vector's elements, `rest` what follows in
+  // the row.  The loads stand under no condition that differs from lane to lane.
+  __device__ __forceinline__ void load(const char* row, int i, int step, int tail, u32x4 rest) {
     constexpr int N = ET == NS_FP32 ? 2 : 1;
-    if (i + 8 <= d) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) v[n] = __builtin_nontemporal_load((const u32x4_any*)(row + (size_t)i * (2 * N) + n * 16));
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w = 0;
-          if (ET == NS_FP32) {
-            if (i + n * 4 + c < d) w = load_bits<ET>(row, i + n * 4 + c);
-          } else {
-            if (i + c * 2 < d) w = load_bits<ET>(row, i + c * 2);
-            if (i + c * 2 + 1 < d) w |= load_bits<ET>(row, i + c * 2 + 1) << 16;
-          }
-          v[n][c] = w;
-        }
+    for (int n = 0; n < N; ++n) {
+      const int at = i + n * step;
+      u32x4 x = {0, 0, 0, 0};
+      if (tail > 0) x = __builtin_nontemporal_load((const u32x4_any*)(row + (size_t)(at < tail ? at : 0) * (2 * N)));
+      v[n] = at < tail ? x : (at == tail ? rest : u32x4{0, 0, 0, 0});
     }
+  }
+  // Elements tail .. d - 1, fewer than a vector's, and zeros.
+  static __device__ __forceinline__ u32x4 rest_of(const char* row, int tail, int d) {
+    u32x4 r = {0, 0, 0, 0};
+    if (tail < d) {                                // uniform
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (ET == NS_FP32) {
+          if (tail + c < d) r[c] = load_bits<ET>(row, tail + c);
+        } else {
+          if (tail + c * 2 < d) r[c] = load_bits<ET>(row, tail + c * 2);
+          if (tail + c * 2 + 1 < d) r[c] |= load_bits<ET>(row, tail + c * 2 + 1) << 16;
+        }
+      }
+    }
+    return r;
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (ET == NS_FP32) return __uint_as_float(v[e >> 2][e & 3]);
     else if constexpr (ET == NS_BF16) return e & 1 ? ns::bf16_hi(v[0][e >> 1]) : ns::bf16_lo(v[0][e >> 1]);
     else return e & 1 ? ns::fp16_hi(v[0][e >> 1]) : ns::fp16_lo(v[0][e >> 1]);
-  }
-  // element e where e is not known to the compiler
-  __device__ __forceinline__ float pick(int e) const {
-    if constexpr (ET == NS_FP32) {
-      const u32x4 h = e & 4 ? v[1] : v[0];
-      const uint32_t a = e & 1 ? h.y : h.x, b = e & 1 ? h.w : h.z;
-      return __uint_as_float(e & 2 ? b : a);
-    } else {
-      const uint32_t a = e & 2 ? v[0].y : v[0].x, b = e & 2 ? v[0].w : v[0].z, w = (e & 4 ? b : a) >> (e & 1) * 16;
-      return ET == NS_BF16 ? ns::bf16_lo(w) : ns::fp16_lo(w);
-    }
   }
   // The largest magnitude as the type's own bits, which order like the values
   // with infinities and NaN on top; two at once for 16-bit types.
@@ -98,64 +94,53 @@ struct Eight {
   }
 };
 
-// round(127 |x| / a), halves to even, decided without a rounding: 254 |x| and
-// (2 f + 1) a are exact in float64 (24 + 8 bits).
-__device__ __forceinline__ int quant_exact(float x, float a) {
-  const float t = fabsf(x) * (127.f / a);
-  const float f = floorf(t), r = t - f;
-  int q = (int)f + (r > 0.5f);
-  if (fabsf(r - 0.5f) < 4e-5f) {
-    const double l = 254.0 * (double)fabsf(x), h = (2.0 * (double)f + 1.0) * (double)a;
-    q = l > h ? (int)f + 1 : (l < h ? (int)f : (int)f + ((int)f & 1));
+// How a row is quantised: 0 for one of zeros or with a value that is not
+// finite (q = 0), otherwise values times `up`, a = up max |x|, rcp = 1 / a.
+// `up` brings the maximum into [2^-100, 2^100], where 1 / a and 127 a are far
+// from overflow; it is exact for all that is not far below the maximum.
+struct Scaling {
+  float up, a, rcp;
+  bool ok;
+  __device__ __forceinline__ explicit Scaling(uint32_t m) {   // the maximum's float32 bits
+    const float top = __uint_as_float(m);
+    ok = m != 0 && m < 0x7F800000u;
+    up = top < 0x1p-100f ? 0x1p64f : (top > 0x1p100f ? 0x1p-64f : 1.f);
+    a = top * up;
+    rcp = 1.f / a;
   }
-  return x < 0.f ? -q : q;
-}
+};
 
-// Eight elements times `up`, each decided exactly; a loop, since its code is
-// rarely entered and would fill the instruction cache unrolled.
-template <int ET>
-__device__ __forceinline__ u32x2 quant_eight_exact(const Eight<ET>& x, float up, float a) {
-  u32x2 r = {0, 0};
-#pragma unroll 1
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = ((uint32_t)quant_exact(x.pick(e) * up, a) & 0xFFu) << (e & 3) * 8;
-    r.x |= e < 4 ? b : 0u;
-    r.y |= e < 4 ? 0u : b;
-  }
-  return r;
-}
-
-// Eight elements to eight bytes, for a maximum a in [2^-100, 2^100] and rcp =
-// 1 / a.  Adding 1.5 * 2^23 leaves a value rounded to an integer, halves to
-// even, in the low byte.
+// Eight elements to eight bytes, round(127 x / a), halves to even, decided
+// exactly and without a branch.  Adding 1.5 * 2^23 leaves a value rounded to an
+// integer, halves to even, in the low byte.
 // 16-bit types: q = 127 x * rcp is off by 2^-23 relatively at most, its
 // remainder 127 x - q a is exact (one fused multiply-add of terms with at most
 // 18 bits and 24 + 11), and q + remainder * rcp is then the quotient rounded
 // to float32: a half comes out as itself, and whatever lies beside one by at
 // least 2^-20 of its size (254 x and an odd multiple of a differ by a unit of
-// x or a) stays on its side.  No case is left to decide (halves are common:
-// half of all groups of 512 bf16 normals hold one).
-// float32: x * (127 rcp) is off by 2^-22 relatively; only where that could reach a
-// half (within 3.2e-5 of one, which is rare) are the eight decided exactly.
+// x or a) stays on its side.
+// float32: 127 x = m + rest exactly in two floats.  n, m * rcp rounded to an
+// integer, is the quotient's rounding or, next to a half, perhaps the integer
+// beyond; r = m - n a is exact, and so is |r| - a / 2 next to a half, so `over`
+// has the sign of the true remainder's excess over a / 2: above 0, or 0 with n
+// odd (no float but 0 is below the smallest positive one), n moves by one
+// towards r.  (Elements next to a half in a rarely entered branch, which held
+// them in scratch memory: 30000 x 4096 float32 262 us, 99 like this.)
 template <int ET>
-__device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, float rcp, float a) {
+__device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, const Scaling& s) {
   constexpr float kMagic = 12582912.f;
   uint32_t b[8];
-  if constexpr (ET == NS_FP32) {
-    const float inv = 127.f * rcp;
-    float off = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = x.get(e), f = fmaf(v, inv, kMagic);
-      off = fmaxf(off, fabsf(fmaf(v, inv, kMagic - f)));
-      b[e] = __float_as_uint(f);
-    }
-    if (off > 0.5f - 3.2e-5f) return quant_eight_exact<ET>(x, 1.f, a);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = 127.f * x.get(e), q = m * rcp;
-      b[e] = __float_as_uint(fmaf(fmaf(-q, a, m), rcp, q) + kMagic);
+  for (int e = 0; e < 8; ++e) {
+    const float v = x.get(e) * s.up, m = 127.f * v;
+    if constexpr (ET == NS_FP32) {
+      const float rest = fmaf(127.f, v, -m), f = fmaf(m, s.rcp, kMagic), r = fmaf(kMagic - f, s.a, m);
+      const uint32_t u = __float_as_uint(f), neg = __float_as_uint(r) & 0x80000000u;
+      const float over = fmaf(-0.5f, s.a, fabsf(r)) + __uint_as_float(__float_as_uint(rest) ^ neg);
+      b[e] = u + (over >= __uint_as_float(~u & 1u) ? ((int32_t)neg >> 31) | 1 : 0);
+    } else {
+      const float q = m * s.rcp;
+      b[e] = __float_as_uint(fmaf(fmaf(-q, s.a, m), s.rcp, q) + kMagic);
     }
   }
   u32x2 r;
@@ -163,9 +148,14 @@ __device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, float rcp, floa
   for (int h = 0; h < 2; ++h) {
     const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0C0C0400u);
     const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000C0Cu);
-    r[h] = lo | hi;
+    r[h] = s.ok ? lo | hi : 0u;
   }
   return r;
+}
+
+// The row's scale from its maximum's float32 bits.
+__device__ __forceinline__ float scale_of(uint32_t m) {
+  return m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.f;
 }
 
 // Maximum over the 16 lanes of a row, in every lane.
@@ -182,20 +172,34 @@ __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
 
 constexpr int kQuantThreads = 256;
 
-// T lanes (a wave or the block) take a row, G groups of eight elements each.
+// T lanes (16, a wave or the block) take a row, G groups of eight elements each.
 template <int ET, int T, int G>
 __global__ __launch_bounds__(kQuantThreads) void k_quant_rows(const void* __restrict__ x, int64_t ld, int R, int d,
                                                               int8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ uint32_t sh[kQuantThreads / NS_WAVE];
   const int tid = threadIdx.x, t = tid & (T - 1);
   const int64_t r = (int64_t)blockIdx.x * (kQuantThreads / T) + tid / T;
-  if (r >= R) return;                              // whole waves, where a wave takes a row
+  if (r >= R) return;                              // whole rows
   const int pitch = pitch_of(d);
   const char* row = (const char*)x + (size_t)r * (size_t)ld * (ET == NS_FP32 ? 4 : 2);
+  int8_t* out = q + (size_t)r * (size_t)pitch;
+  // a load of all lanes covers one run of the row: float32 takes two runs a group
+  const auto first = [&](int g) { return ET == NS_FP32 ? (t + 2 * g * T) * 4 : (t + g * T) * 8; };
+  const auto put = [&](int g, u32x2 b) {
+    const int i = first(g);
+    if (ET == NS_FP32) {
+      if (i < pitch) *(uint32_t*)(out + i) = b.x;
+      if (i + T * 4 < pitch) *(uint32_t*)(out + i + T * 4) = b.y;
+    } else if (i < pitch) {
+      *(u32x2*)(out + i) = b;
+    }
+  };
+  const int tail = d & ~(ET == NS_FP32 ? 3 : 7);
+  const u32x4 rest = Eight<ET>::rest_of(row, tail, d);
   Eight<ET> v[G];
   uint32_t m = 0;
 #pragma unroll
-  for (int g = 0; g < G; ++g) v[g].load(row, (t + g * T) * 8, d);
+  for (int g = 0; g < G; ++g) v[g].load(row, first(g), T * 4, tail, rest);
   NS_ISSUE_FENCE();
 #pragma unroll
   for (int g = 0; g < G; ++g) m = v[g].top(m);
@@ -206,10 +210,14 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_rows(const void* __rest
     top = ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b);
   }
   m = __float_as_uint(top);                        // float32 bits order the same way
+  if (T == 16) {
+    m = row16_max_u32(m);
+  } else {
 #pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) {
-    const uint32_t o = __shfl_xor(m, s, NS_WAVE);
-    m = o > m ? o : m;
+    for (int s = 32; s >= 1; s >>= 1) {
+      const uint32_t o = __shfl_xor(m, s, NS_WAVE);
+      m = o > m ? o : m;
+    }
   }
   if (T > NS_WAVE) {
     if ((tid & 63) == 0) sh[tid / NS_WAVE] = m;
@@ -217,42 +225,28 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_rows(const void* __rest
 #pragma unroll
     for (int w = 0; w < T / NS_WAVE; ++w) m = sh[w] > m ? sh[w] : m;
   }
-  const bool bad = m >= 0x7F800000u;
-  const float a = __uint_as_float(m);
-  int8_t* out = q + (size_t)r * (size_t)pitch;
-  if (bad || a < 0x1p-100f || a > 0x1p100f) {      // uniform over the row; zeros are here too
-    // 1 / a or 127 x could overflow: everything 2^64 times as large or as
-    // small, exact for all that is not far below a
-    const float by = a > 1.f ? 0x1p-64f : 0x1p64f;
+  const Scaling how(m);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int i = (t + g * T) * 8;
-      u32x2 r = {0, 0};
-      if (!bad && m != 0) r = quant_eight_exact<ET>(v[g], by, a * by);
-      if (i < pitch) *(u32x2*)(out + i) = r;
-    }
-  } else {
-    const float rcp = 1.f / a;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int i = (t + g * T) * 8;
-      if (i < pitch) *(u32x2*)(out + i) = quant_eight<ET>(v[g], rcp, a);
-    }
-  }
-  if (t == 0) scale[r] = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
+  for (int g = 0; g < G; ++g) put(g, quant_eight<ET>(v[g], how));
+  if (t == 0) scale[r] = scale_of(m);
 }
 
 template <int ET>
 int quant_rows_of(const void* x, int64_t ld, int R, int d, int8_t* q, float* scale, hipStream_t stream) {
   const int groups = pitch_of(d) / 8;
-  // A wave takes a row where it can hold it and the rows fill the chip
-  // without a block each.
-  const bool wave = groups <= 8 * NS_WAVE && (R >= 1024 || groups <= NS_WAVE);
-  const int T = wave ? NS_WAVE : kQuantThreads, g = (groups + T - 1) / T;
+  // 16 lanes take a row of up to 512 elements (120811 x 87 bf16 in 14 us, 43 with
+  // a wave a row; 50000 x 500 16 against 23; 30000 x 1024 20 against 17), a wave
+  // one that it can hold if the rows fill the chip without a block each.
+  const bool wave = groups <= 8 * NS_WAVE && (R >= 1024 || groups <= NS_WAVE), part = groups <= 64;
+  const int T = part ? 16 : (wave ? NS_WAVE : kQuantThreads), g = (groups + T - 1) / T;
   const dim3 grid((unsigned)((R + kQuantThreads / T - 1) / (kQuantThreads / T))), block(kQuantThreads);
 #define NS_LAUNCH_QUANT(TT, G) \
   hipLaunchKernelGGL((k_quant_rows<ET, TT, G>), grid, block, 0, stream, x, ld, R, d, q, scale)
-  if (wave) {
+  if (part) {
+    if (g <= 1) NS_LAUNCH_QUANT(16, 1);
+    else if (g <= 2) NS_LAUNCH_QUANT(16, 2);
+    else NS_LAUNCH_QUANT(16, 4);
+  } else if (wave) {
     if (g <= 1) NS_LAUNCH_QUANT(NS_WAVE, 1);
     else if (g <= 2) NS_LAUNCH_QUANT(NS_WAVE, 2);
     else if (g <= 4) NS_LAUNCH_QUANT(NS_WAVE, 4);
@@ -860,17 +854,18 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
 
 // ---------------------------------------------------------------------------
 // The head over few rows with the quantisation of its hidden rows in the same
-// launch, for up to 16 of them and 32 KB of 8-bit hidden rows: every block
-// quantises them all into LDS (64 elements a thread at most) while its channel
-// rows are on their way.  A launch less: M = 8, d = 4096, 1000 rows 12.6 -> 12.0
-// us, M = 1 11.8 -> 8.8, 19 sequences of 46 rows, M = 8, d = 320, 12.5 -> 9.8.
+// launch, for up to 16 of them, 32 KB of 8-bit hidden rows and d % 8 = 0: every
+// block quantises them all into LDS (U groups of eight elements a thread) while
+// its channel rows are on their way.  A launch less: M = 8, d = 4096, 1000 rows
+// 12.6 -> 12.0 us, M = 1 11.8 -> 8.8, 19 sequences of 46 rows, M = 8, d = 320,
+// 12.5 -> 9.8.
 // ---------------------------------------------------------------------------
 constexpr int kFusedBytes = 32768;                 // M * pitch, at most
 constexpr int kFusedPad = 16;                      // between token rows in LDS: no bank is met twice
 
-template <int ET>
+template <int ET, int U>
 __global__ __launch_bounds__(512) void k_head_few(Product p, const void* __restrict__ h, int d) {
-  constexpr int BATCH = 8, U = kFusedBytes / 8 / 512;
+  constexpr int BATCH = 8;
   __shared__ __attribute__((aligned(16))) char xq[kFusedBytes + 16 * kFusedPad];
   __shared__ i32x4 sh[8][NS_WAVE];
   __shared__ uint32_t s_top[16];
@@ -890,7 +885,8 @@ __global__ __launch_bounds__(512) void k_head_few(Product p, const void* __restr
     const int c = (tid >> 4) + u * 32;
     tok[u] = c < chunks ? c * magic >> 16 : -1;
     at[u] = (c - tok[u] * per_row) * 128 + (tid & 15) * 8;
-    if (tok[u] >= 0) v[u].load(hb + (size_t)tok[u] * d * (ET == NS_FP32 ? 4 : 2), at[u], d);
+    // a group past the last row reads the first, and nobody reads it
+    v[u].load(hb + (size_t)(tok[u] < 0 ? 0 : tok[u]) * d * (ET == NS_FP32 ? 4 : 2), at[u], 4, d, u32x4{0, 0, 0, 0});
   }
   if (tid < 16) s_top[tid] = 0;
   NS_ISSUE_FENCE();
@@ -931,13 +927,7 @@ __global__ __launch_bounds__(512) void k_head_few(Product p, const void* __restr
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (tok[u] < 0) continue;
-    const uint32_t m = s_top[tok[u]];
-    const float top = __uint_as_float(m);
-    u32x2 q = {0, 0};
-    if (m < 0x7F800000u && m != 0)
-      q = top < 0x1p-100f   ? quant_eight_exact<ET>(v[u], 0x1p64f, top * 0x1p64f)
-          : top > 0x1p100f ? quant_eight_exact<ET>(v[u], 0x1p-64f, top * 0x1p-64f)
-                           : quant_eight<ET>(v[u], 1.f / top, top);
+    const u32x2 q = quant_eight<ET>(v[u], Scaling(s_top[tok[u]]));
     *(u32x2*)(xq + tok[u] * (p.pitch + kFusedPad) + at[u]) = q;
   }
   sync();
@@ -959,10 +949,16 @@ __global__ __launch_bounds__(512) void k_head_few(Product p, const void* __restr
   for (int r = 0; r < 4; ++r) {
     const int m = g * 4 + r;
     if (m >= p.M || j0 + i >= n) continue;
-    const uint32_t t = s_top[m];
-    const float xs = t >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(t) / 127.f;
+    const float xs = scale_of(s_top[m]);
     store_out<NS_FP32>(p.out, (seq * p.M + m) * (size_t)p.sm + (size_t)(j0 + i) * (size_t)p.sn, scaled(s[r], xs * ws));
   }
+}
+
+template <int ET>
+void launch_head_few(const Product& p, int B, const void* h, int d, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)B), block(512);
+  if (p.M * p.pitch <= kFusedBytes / 4) hipLaunchKernelGGL((k_head_few<ET, 2>), grid, block, 0, stream, p, h, d);
+  else hipLaunchKernelGGL((k_head_few<ET, 8>), grid, block, 0, stream, p, h, d);
 }
 
 template <int OT, int TB>
@@ -1272,17 +1268,16 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   float* hs = (float*)(base + l.scale);
   float* z = (float*)(base + l.z);
   int rc = NS_OK;
-  const bool fused = few_rows(B, n_max, V, d) && M <= 16 && M * pitch_of(d) <= kFusedBytes;
+  const bool fused = few_rows(B, n_max, V, d) && M <= 16 && M * pitch_of(d) <= kFusedBytes && d % 8 == 0;
   if (!fused) rc = quant_rows(h, d, B * M, d, dtype, hq, hs, stream);
   if (rc != NS_OK) return rc;
   const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
   if (!fused) {
     launch_head(p, B, stream);
   } else {
-    const dim3 grid((unsigned)((n_max + 15) / 16), (unsigned)B), block(512);
-    if (dtype == NS_BF16) hipLaunchKernelGGL(k_head_few<NS_BF16>, grid, block, 0, stream, p, h, d);
-    else if (dtype == NS_FP16) hipLaunchKernelGGL(k_head_few<NS_FP16>, grid, block, 0, stream, p, h, d);
-    else hipLaunchKernelGGL(k_head_few<NS_FP32>, grid, block, 0, stream, p, h, d);
+    if (dtype == NS_BF16) launch_head_few<NS_BF16>(p, B, h, d, stream);
+    else if (dtype == NS_FP16) launch_head_few<NS_FP16>(p, B, h, d, stream);
+    else launch_head_few<NS_FP32>(p, B, h, d, stream);
   }
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;

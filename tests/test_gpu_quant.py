@@ -114,6 +114,33 @@ def test_quant_borders(ns, dtype, d):
     check_quant(ns, t, f"borders {dtype} {d}")
 
 
+# rows that 16 lanes, a wave or a block take, with every remainder of a vector
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("R,d", [(1, 3), (17, 9), (5000, 30), (33, 121), (1025, 255), (2000, 260), (50, 505), (1030, 511),
+                                 (1100, 514), (40, 517), (1500, 1023), (1030, 4091), (20, 4090), (1100, 4100), (9, 10007)])
+def test_quant_rows_in_parts(ns, R, d, dtype):
+    rng = np.random.default_rng(d)
+    x = torch.from_numpy(rng.standard_normal((R, d + 1)).astype(np.float32)).to(DT[dtype]).cuda()
+    check_quant(ns, x[:, 1:], f"{R} x {d} {dtype}")
+
+
+@pytest.mark.parametrize("d", [60, 512, 1000, 5000])
+def test_quant_next_to_halves(ns, d):
+    """float32 values at and beside (n + 1/2) a / 127 for maxima a of every size, down to subnormal ones."""
+    R = 1200
+    rng = np.random.default_rng(d)
+    a = np.exp2(rng.uniform(-148, 127.9, (R, 1))).astype(np.float32)
+    a[:400] = np.exp2(rng.uniform(-3, 3, (400, 1))).astype(np.float32)
+    h = (2 * rng.integers(0, 127, (R, d)) + 1) / 254.0 * a.astype(np.float64)
+    x = h.astype(np.float32)
+    for _ in range(2):
+        to = np.where(rng.random((R, d)) < 0.5, np.float32(0), np.float32(np.inf))
+        x = np.where(rng.random((R, d)) < 0.4, np.nextafter(x, to), x)
+    x = np.minimum(x, a) * np.where(rng.random((R, d)) < 0.5, np.float32(-1), np.float32(1))
+    x[:, d // 2] = a[:, 0]
+    check_quant(ns, torch.from_numpy(x.astype(np.float32)).cuda(), f"next to halves {d}")
+
+
 def int8_rows(n, d, seed, extreme=False):
     rng = np.random.default_rng(seed)
     q = np.zeros((n, pitch(d)), np.int8)

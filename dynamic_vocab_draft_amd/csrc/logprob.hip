@@ -487,7 +487,10 @@ __device__ __forceinline__ void take(const u32x4 (&x)[kUnroll], int q0, int q1, 
 }
 
 // Forward.  A wave owns part `part` of S of one row and streams it once with
-// 16-byte loads, two register batches in turn.
+// 16-byte loads, two register batches in turn.  Bound by its bytes over many
+// rows (4096 x 128256 bf16 164 us, 6.4 TB/s; with k = 4 171 to 177), by the
+// latency of the selection over few (8 x 128256 float32, both launches 7.6 us;
+// with k = 8 12.4).
 template <int ET, bool TOP>
 __global__ __launch_bounds__(kRowWaves* NS_WAVE) void k_logprobs(Args a) {
   constexpr int EPV = per_vec(ET), STEP = NS_WAVE * kUnroll;
@@ -769,8 +772,9 @@ struct Slope {
   }
 };
 
-// dlogits may be logits: a block reads its part of the row, and the logits of
-// the tokens in it, before it writes them.
+// One pass, bound by its bytes (4096 x 128256 bf16 353 us, 5.95 TB/s read and
+// written).  dlogits may be logits: a block reads its part of the row, and the
+// logits of the tokens in it, before it writes them.
 template <int ET>
 __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(GradArgs a, int per, int chunks) {
   constexpr int EPV = per_vec(ET);

@@ -360,6 +360,18 @@ def test_quant_head_ties_and_nan(ns, n_max):
     check_head(ns, (wq, ws, h, I, n), 20, what=f"ties n={n_max}")
 
 
+@pytest.mark.parametrize("k", [33, 64])
+@pytest.mark.parametrize("levels", [0, 3, 40])
+def test_quant_head_many_candidates(ns, k, levels):
+    """Counts around those where every logit is a candidate, where waves of them are merged, and where they no longer fit."""
+    counts = [63, 64, 65, 100, 128, 129, 500, 513, 1000, 1008, 1009, 1023, 1024, 1025, 1100, 2000, 2200]
+    wq, ws, h, I, n = head_case(len(counts), 2200, 3, 64, 2500, "bf16", 11, counts, holes=0.01)
+    if levels:                                            # few different logits: many tie
+        wq[:] = wq[np.arange(len(wq)) % levels]
+        ws[:] = 0.5
+    check_head(ns, (wq, ws, h, I, n), k, what=f"candidates k={k} levels={levels}")
+
+
 def test_quant_head_reuses_a_workspace(ns):
     """A larger call's leavings in the workspace do not reach a smaller one."""
     big, small = head_case(1, 6000, 16, 512, 8000, "bf16", 1, [6000]), head_case(1, 40, 3, 128, 90, "bf16", 2, [33])

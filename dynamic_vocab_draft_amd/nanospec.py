@@ -601,10 +601,12 @@ def _matrix(t, where: str, name: str):
     if not (isinstance(t, torch.Tensor) and t.get_device() >= 0 and t.dtype in _FLOATS and t.dim() == 2):
         _misfit(t, where, name, _FLOATS, None, t.get_device() if isinstance(t, torch.Tensor) else -1)
     (rows, cols), (ld, step) = t.shape, t.stride()
-    _want(cols >= 1 and (step == 1 or cols == 1), where, f"{name} is no matrix of contiguous rows")
+    if cols < 1 or (step != 1 and cols != 1):             # messages are made only when they are raised
+        _want(False, where, f"{name} is no matrix of contiguous rows")
     if rows <= 1:
         ld = cols
-    _want(ld >= cols, where, f"the rows of {name} overlap")
+    if ld < cols:
+        _want(False, where, f"the rows of {name} overlap")
     return rows, cols, ld, _FLOATS[t.dtype], t.get_device()
 
 
@@ -686,10 +688,12 @@ def nanospec_token_logprobs_workspace_bytes(L: int, V: int, k: int) -> int:
 
 def _pair(a, b, where: str, names: str) -> int:
     """Columns of a matrix that is given with another of its shape, or not at all (0)."""
-    _want((a is None) == (b is None), where, f"{names} go together")
+    if (a is None) != (b is None):
+        _want(False, where, f"{names} go together")
     if a is None:
         return 0
-    _want(isinstance(a, torch.Tensor) and a.dim() == 2, where, f"{names}: no matrix")
+    if not (isinstance(a, torch.Tensor) and a.dim() == 2):
+        _want(False, where, f"{names}: no matrix")
     return a.shape[1]
 
 
@@ -722,8 +726,10 @@ def nanospec_token_logprobs_grad(logits: torch.Tensor, inv_temp: float, tokens: 
     where = "nanospec_token_logprobs_grad"
     L, V, ld, code, dev = _matrix(logits, where, "logits")
     L_d, V_d, ld_d, code_d, dev_d = _matrix(dlogits, where, "dlogits")
-    _want((L_d, V_d, dev_d) == (L, V, dev), where, f"dlogits is {(L_d, V_d)} on device {dev_d}, not {(L, V)} on {dev}")
-    _want(code_d == code, where, f"dlogits has dtype {dlogits.dtype}, not {logits.dtype}", NS_EDTYPE)
+    if L_d != L or V_d != V or dev_d != dev:
+        _want(False, where, f"dlogits is {(L_d, V_d)} on device {dev_d}, not {(L, V)} on {dev}")
+    if code_d != code:
+        _want(False, where, f"dlogits has dtype {dlogits.dtype}, not {logits.dtype}", NS_EDTYPE)
     T = _pair(tokens, g_logprob, where, "tokens and g_logprob")
     _launch(where, _lib.nanospec_token_logprobs_grad, dev, stream, logits.data_ptr(), ld, L, V, code, inv_temp,
             None if tokens is None else _tensor(tokens, where, "tokens", _INT32, (L, T), dev), T,

@@ -561,8 +561,8 @@ def head_probe(torch, ns, Ms, V=151936, d=4096, k=16):
 
 
 DRAFT_SOURCES = ("dynamic_vocab_draft_amd/csrc/draft.hip", "dynamic_vocab_draft_amd/csrc/select.hpp",
-                 "dynamic_vocab_draft_amd/csrc/common.hpp", "dynamic_vocab_draft_amd/csrc/state_fast.hpp",
-                 "dynamic_vocab_draft_amd/csrc/state_internal.hpp")
+                 "dynamic_vocab_draft_amd/csrc/lists.hpp", "dynamic_vocab_draft_amd/csrc/common.hpp",
+                 "dynamic_vocab_draft_amd/csrc/state_fast.hpp", "dynamic_vocab_draft_amd/csrc/state_internal.hpp")
 
 
 PREFILL_SOURCES = ("dynamic_vocab_draft_amd/csrc/prefill.hip", "dynamic_vocab_draft_amd/csrc/common.hpp")

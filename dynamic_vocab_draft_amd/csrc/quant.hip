@@ -305,29 +305,32 @@ constexpr int kStageK = 128;                       // bytes of a row in a stage
 
 // 16 bytes a lane from a buffer straight into LDS at byte `lds` (the same
 // for the wave) + 16 * lane.  The compiler does not count these loads: the
-// waits below do.  m0 holds the LDS address; nothing else in these kernels
-// uses it.
+// waits below do.  m0 holds the LDS address.  The compiler does not see a
+// memory instruction here either, so the asm keeps the distances itself: the
+// move and the no-ops are the five wait states from a vector instruction that
+// wrote an SGPR (v_readlane, as for a spilled one) to a memory instruction that
+// reads it, and more than the one from the move to the load.
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
                : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-               : "memory");
+               : "memory", "m0");
 }
 
 // The same for bytes that are read once: the caches need not keep them.
 __device__ __forceinline__ void load_to_lds_once(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
                :
                : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-               : "memory");
+               : "memory", "m0");
 }
 
 // The same for four bytes a lane.
 __device__ __forceinline__ void load_word_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :
                : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-               : "memory");
+               : "memory", "m0");
 }
 
 __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {

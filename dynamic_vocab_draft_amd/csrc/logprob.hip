@@ -663,6 +663,13 @@ void launch_logprobs(const Args& a, hipStream_t stream) {
 // With y_j = log2 p_j the first part is p_j (A + B y_j), A = t (G - g_H H),
 // B = -t g_H ln2.  log2(e) lse is taken in two floats; the small one goes
 // into A, B and a common factor.
+//
+// lse is a float32 and half a step of it passes into every p_j: 2^-15 at 1024,
+// 2^-5 at 10^6 (shifted logits, a row with nothing but fp16's lowest value as a
+// mask).  Beyond kNear the row's first block takes the whole row, sums
+// 2^(c (z_j - ref)) itself, ref = lse / t (next to lse those differences are
+// exact), and takes y_j = c (z_j - ref) - log2 of the sum.  It has read the
+// whole row before it writes any of it, so dlogits may be logits there too.
 // ---------------------------------------------------------------------------
 struct GradArgs {
   const void* z;
@@ -698,15 +705,48 @@ __device__ __forceinline__ void put_elem(void* d, size_t i, float v) {
   else ((uint16_t*)d)[i] = (uint16_t)narrow2<ET>(v, 0.f);
 }
 
+constexpr float kNear = 1024.f;          // |lse| up to which probabilities come from lse itself
+constexpr float kFar = 0x1p24f;          // |lse| beyond which a row's gradient is 0
+
 struct Slope {
-  float c, L, A, B;
+  float c, ref, L, A, B;
   bool zero;
   // p (A + B y) of a logit
   __device__ __forceinline__ float at(float z) const {
-    const float y = fmaf(z, c, -L);
+    const float y = fmaf(z - ref, c, -L);
     return exp2_fast(y) * fmaf(B, fmaxf(y, -200.f), A);
   }
 };
+
+// Sum of 2^(c (z_j - ref)) over a row, by all threads of a block in the same
+// order each time; a batch is summed by itself first.
+template <int ET>
+__device__ __forceinline__ float sum_of_row(const char* zrow, int V, float ref, float c, float* sh) {
+  constexpr int EPV = per_vec(ET);
+  const int tid = threadIdx.x, nvec = V / EPV, tail = nvec * EPV + tid;
+  float S = tail < V ? exp2_fast((one_elem<ET>(zrow, tail) - ref) * c) : 0.f;
+  for (int base = 0; base < nvec; base += kGradThreads * kGradUnroll) {
+    float batch = 0.f;
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      const int q = base + u * kGradThreads + tid;
+      if (q < nvec) {
+        float v[EPV];
+        widen<ET>(*(const u32x4_any*)(zrow + (size_t)q * 16), v);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) batch += exp2_fast((v[e] - ref) * c);
+      }
+    }
+    S += batch;
+  }
+  S = ns::wave_sum_f32(S);
+  if ((tid & (NS_WAVE - 1)) == 0) sh[tid / NS_WAVE] = S;
+  __syncthreads();
+  S = sh[0];
+#pragma unroll
+  for (int w = 1; w < kGradThreads / NS_WAVE; ++w) S += sh[w];
+  return S;
+}
 
 // One pass, bound by its bytes (4096 x 128256 bf16 353 us, 5.95 TB/s read and
 // written).  dlogits may be logits: a block reads its part of the row, and the
@@ -716,6 +756,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(GradArgs a, int 
   constexpr int EPV = per_vec(ET);
   __shared__ int32_t s_tok[NS_MAX_K];
   __shared__ float s_g[NS_MAX_K];
+  __shared__ float s_sum[kGradThreads / NS_WAVE];
   const size_t row = blockIdx.x / (unsigned)chunks;
   const int chunk = (int)(blockIdx.x % (unsigned)chunks);
   const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1);
@@ -723,8 +764,8 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(GradArgs a, int 
   char* drow = (char*)a.dz + row * (size_t)a.ld_d * elem_bytes(ET);
   const int nvec = a.V / EPV;
   const int q0 = chunk * per;
-  const int q1 = q0 + per < nvec ? q0 + per : nvec;
-  const bool last = chunk + 1 == chunks;
+  int q1 = q0 + per < nvec ? q0 + per : nvec;
+  bool last = chunk + 1 == chunks;
   // every wave sums the tokens' gradients for itself, in the same order
   int tok = -1;
   float g = 0.f;
@@ -737,11 +778,19 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(GradArgs a, int 
   const float H = a.g_entropy ? a.entropy[row] : 0.f, gl = a.g_lse ? a.g_lse[row] : 0.f;
   Slope s;
   s.c = a.c;
-  // a row without logits, or whose float32 lse no longer resolves probabilities
-  s.zero = fabsf(lse) > 0x1p24f;
+  s.zero = fabsf(lse) > kFar;
+  s.ref = 0.f;
   s.L = lse * kLog2e;
   // (c z is close to L wherever p is not small, so c's own rounding is eps L)
-  const float low = (float)((double)lse * 1.4426950408889634 - (double)s.L) - a.eps * s.L;
+  float low = (float)((double)lse * 1.4426950408889634 - (double)s.L) - a.eps * s.L;
+  if (fabsf(lse) > kNear && !s.zero) {                     // uniform over the row's blocks
+    if (chunk > 0) return;
+    q1 = nvec;
+    last = true;
+    s.ref = lse / a.t;
+    s.L = log2f(sum_of_row<ET>(zrow, a.V, s.ref, a.c, s_sum));
+    low = 0.f;
+  }
   const float f = exp2_fast(-low);
   s.B = -a.t * gH * kLn2 * f;
   s.A = a.t * (gl - sum - gH * H) * f - s.B * low;

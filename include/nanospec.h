@@ -656,8 +656,12 @@ int nanospec_token_logprobs(const void* logits, int64_t ld, int32_t L, int32_t V
  *   dlogits      : L rows of `dtype`, ld_d >= V elements apart; either the
  *                  logits themselves (ld_d = ld), which it then replaces, or
  *                  memory apart from them.  What lies between rows is untouched.
- * A row whose lse is -INFINITY, or so large (over 2^24) that float32 no longer
- * resolves probabilities from it, has gradient 0; one whose lse is NaN, NaN.
+ * Probabilities come from lse, whose own rounding passes into them: half a step
+ * of it, 2^-15 relatively at |lse| = 1024.  For a row beyond that (shifted
+ * logits, nothing left but fp16's lowest value) the sum is taken from the logits
+ * anew, with float32's usual error whatever the shift.
+ * A row whose lse is -INFINITY, or over 2^24 in size (nothing left but float32's
+ * or bfloat16's lowest value), has gradient 0; one whose lse is NaN, NaN.
  * Errors: NS_EINVAL, NS_EDTYPE, NS_EHIP. */
 int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int32_t V, int32_t dtype,
                                  float inv_temp, const int32_t* tokens, int32_t T, const float* lse,

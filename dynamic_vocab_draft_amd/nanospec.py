@@ -596,6 +596,12 @@ def _tensor(t, where: str, name: str, dtype, shape, dev: int):
     return t.data_ptr()
 
 
+def _workspace(t, where: str, dev: int):
+    """(address, bytes) of a workspace."""
+    size = t.numel() if isinstance(t, torch.Tensor) else 0
+    return _tensor(t, where, "work", _UINT8, (size,), dev), size
+
+
 def _matrix(t, where: str, name: str):
     """(rows, columns, row stride in elements, dtype code, device) of a device matrix whose rows are contiguous."""
     if not (isinstance(t, torch.Tensor) and t.get_device() >= 0 and t.dtype in _FLOATS and t.dim() == 2):
@@ -679,7 +685,7 @@ def nanospec_quant_logits_topk(wq: torch.Tensor, wscale: torch.Tensor, row_ids: 
             None if logits is None else _tensor(logits, where, "logits", _F32, (B, M, n_max), dev),
             _tensor(topk_ids, where, "topk_ids", _INT32, (B, M, k), dev),
             _tensor(topk_vals, where, "topk_vals", _F32, (B, M, k), dev),
-            _tensor(work, where, "work", _UINT8, (work.numel(),), dev), work.numel())
+            *_workspace(work, where, dev))
 
 
 def nanospec_token_logprobs_workspace_bytes(L: int, V: int, k: int) -> int:
@@ -714,7 +720,7 @@ def nanospec_token_logprobs(logits: torch.Tensor, inv_temp: float, tokens: Optio
             None if entropy is None else _tensor(entropy, where, "entropy", _F32, (L,), dev),
             None if top_ids is None else _tensor(top_ids, where, "top_ids", _INT32, (L, k), dev),
             None if top_ids is None else _tensor(top_logprobs, where, "top_logprobs", _F32, (L, k), dev),
-            _tensor(work, where, "work", _UINT8, (work.numel(),), dev), work.numel())
+            *_workspace(work, where, dev))
 
 
 def nanospec_token_logprobs_grad(logits: torch.Tensor, inv_temp: float, tokens: Optional[torch.Tensor],

@@ -239,7 +239,7 @@ int quant_rows_of(const void* x, int64_t ld, int R, int d, int8_t* q, float* sca
   // 16 lanes take a row of up to 512 elements (120811 x 87 bf16 in 14 us, 43 with
   // a wave a row; 50000 x 500 16 against 23; 30000 x 1024 20 against 17), a wave
   // one that it can hold if the rows fill the chip without a block each.
-  const bool wave = groups <= 8 * NS_WAVE && (R >= 1024 || groups <= NS_WAVE), part = groups <= 64;
+  const bool part = groups <= 64, wave = groups <= 8 * NS_WAVE && R >= 1024;
   const int T = part ? 16 : (wave ? NS_WAVE : kQuantThreads), g = (groups + T - 1) / T;
   const dim3 grid((unsigned)((R + kQuantThreads / T - 1) / (kQuantThreads / T))), block(kQuantThreads);
 #define NS_LAUNCH_QUANT(TT, G) \
@@ -248,9 +248,8 @@ int quant_rows_of(const void* x, int64_t ld, int R, int d, int8_t* q, float* sca
     if (g <= 1) NS_LAUNCH_QUANT(16, 1);
     else if (g <= 2) NS_LAUNCH_QUANT(16, 2);
     else NS_LAUNCH_QUANT(16, 4);
-  } else if (wave) {
-    if (g <= 1) NS_LAUNCH_QUANT(NS_WAVE, 1);
-    else if (g <= 2) NS_LAUNCH_QUANT(NS_WAVE, 2);
+  } else if (wave) {                               // more than 64 groups: two a lane at least
+    if (g <= 2) NS_LAUNCH_QUANT(NS_WAVE, 2);
     else if (g <= 4) NS_LAUNCH_QUANT(NS_WAVE, 4);
     else NS_LAUNCH_QUANT(NS_WAVE, 8);
   } else {
@@ -1300,9 +1299,10 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   if (rc != NS_OK || l.chunks == 1) return rc;
   const int nk = l.chunks * k;
   const dim3 grid((unsigned)M, (unsigned)B), block(kSelectThreads);
+  static_assert((NS_MAX_V + top_chunk(NS_MAX_V) - 1) / top_chunk(NS_MAX_V) * NS_MAX_K <= 4 * kSelectThreads,
+                "k_top_keys<4> holds every chunk's keys");
   if (nk <= kSelectThreads) hipLaunchKernelGGL(k_top_keys<1>, grid, block, 0, stream, t, nk);
-  else if (nk <= 4 * kSelectThreads) hipLaunchKernelGGL(k_top_keys<4>, grid, block, 0, stream, t, nk);
-  else hipLaunchKernelGGL(k_top_keys<16>, grid, block, 0, stream, t, nk);
+  else hipLaunchKernelGGL(k_top_keys<4>, grid, block, 0, stream, t, nk);
   return ns_launch_status();
 }
 

@@ -308,7 +308,11 @@ constexpr int kStageK = 128;                       // bytes of a row in a stage
 // memory instruction here either, so the asm keeps the distances itself: the
 // move and the no-ops are the five wait states from a vector instruction that
 // wrote an SGPR (v_readlane, as for a spilled one) to a memory instruction that
-// reads it, and more than the one from the move to the load.
+// reads it, and more than the one from the move to the load.  m0 is a register
+// that the compiler reserves and writes before each use of its own, so it warns
+// of the clobber, which tells it that the value is gone.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
@@ -331,6 +335,8 @@ __device__ __forceinline__ void load_word_to_lds(u32x4 rsrc, uint32_t voff, uint
                : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
                : "memory", "m0");
 }
+
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
   const uint64_t a = (uint64_t)p;

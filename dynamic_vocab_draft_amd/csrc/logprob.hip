@@ -635,10 +635,14 @@ int parts_of(int L, int V, int dtype) {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Room for the parts of L rows or any fewer, so that the largest call's
+// workspace fits a loop's smaller ones: a row has at most the parts of a single
+// one (of float32, which has the smallest batches), and rows in parts come to
+// less than 3/2 kWavesWanted of them together.
 size_t logprobs_ws(int L, int V, int k) {
-  // fp32 has the smallest batches, so the most parts
-  const size_t s = (size_t)parts_of(L, V, NS_FP32), l = (size_t)(L > 0 ? L : 1);
-  return align256(l * s * sizeof(Stat)) + align256(l * s * (size_t)k * 8) + 256;
+  const size_t l = (size_t)(L > 0 ? L : 1), most = l * (size_t)parts_of(1, V, NS_FP32);
+  const size_t split = most < kWavesWanted * 3 / 2 ? most : kWavesWanted * 3 / 2, n = l > split ? l : split;
+  return align256(n * sizeof(Stat)) + align256(n * (size_t)k * 8) + 256;
 }
 
 template <int ET>

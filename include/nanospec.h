@@ -628,8 +628,10 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
  *             asc) with their log-probabilities; k in [0, min(64, V)]; NULL
  *             allowed when k = 0.
  *   ws      : >= nanospec_token_logprobs_workspace_bytes(L, V, k) bytes,
- *             256-byte aligned, no initialisation needed.  Calls sharing a
- *             workspace must be ordered (two captured graphs among them).
+ *             256-byte aligned, no initialisation needed.  The size never falls
+ *             as L, V or k grows: one for the largest call fits the others.
+ *             Calls sharing a workspace must be ordered (two captured graphs
+ *             among them).
  * A logit of -INFINITY (masked) has probability 0 and log-probability
  * -INFINITY.  A row with nothing else has lse -INFINITY, entropy 0 and every
  * log-probability -INFINITY.  A row with a NaN or +INFINITY has no

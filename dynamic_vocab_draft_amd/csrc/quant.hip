@@ -388,9 +388,10 @@ __device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v
 // One block of eight waves a CU takes an even share of the 16-row channel
 // units and runs through it in passes of 8 RT units, RT a wave, in stages of
 // 128 bytes a row.  A ring of stages in LDS is filled by direct
-// global-to-LDS loads, R - 1 stages (64 to 96 KB a CU) ahead, across the
-// ends of passes; channel rows are private to their wave, token rows shared by
-// the block, so one barrier a stage orders the ring.  Waits count the loads
+// global-to-LDS loads, R - 1 stages ahead (72 to 132 KB a CU, 48 to 96 KB of
+// them channel rows), across the ends of passes; channel rows are private to
+// their wave, token rows shared by the block, so one barrier a stage orders the
+// ring.  Waits count the loads
 // that may still be out; outputs leave by buffer stores, which out-of-range
 // lanes take part in without effect, so the stores behind a pass are as many
 // for every pass and the waits can allow for them.
@@ -595,10 +596,10 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
 // token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
 // in stages of 128 bytes a row, two in LDS (68 KB each with TB = 4), three with
 // TB = 1, whose short stages end before a load does (256 x 16384 x 4096, a tile
-// a CU: 29.5 -> 25.3 us), filled by direct global-to-LDS loads.  While one half of a stage (64 bytes a row) is
-// multiplied, the next half is read into a second set of registers; once a
-// wave holds a stage's second half and the next stage has landed, one block
-// barrier frees the stage's place for the stage after next.
+// a CU: 29.5 -> 25.3 us), filled by direct global-to-LDS loads.  While one half
+// of a stage (64 bytes a row) is multiplied, the next half is read into a second
+// set of registers; once a wave holds a stage's second half and the next stage
+// has landed, one block barrier frees the stage's place for the stage after next.
 //
 // Blocks stay: each takes one tile after the other, and the stages of all its
 // tiles (with the tiles' scales) are one stream of loads, so the next tile's
@@ -612,15 +613,15 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
 // lanes covers 128 of them, without a detour through LDS.
 //
 // 4096 x 128256 x 4096 takes 1655 to 1730 us (2.5 to 2.6 POP/s): the matrix units
-// are busy for 77 % of the cycles, and the clock gives way under the load.
+// are busy for 74 % of the cycles, and the clock gives way under the load.
 // Products of 32 x 32 x 32 (1841 us) and four stages of 64 bytes (1911) were
 // slower.
-//  Place c of row r
-// in LDS holds 16-byte chunk c ^ (r / 8 % 8) of channel rows and c ^ (r % 8)
-// of token rows, and eight channel rows stand 128 bytes from the next eight, so
-// that lanes i and i + 1 read from different halves of the 64 banks: no bank is
-// met twice (without that 128 bytes a fifth of the cycles were conflicts; 1024 x
-// 128256 x 4096 482 -> 467 us).
+//
+// Place c of row r in LDS holds 16-byte chunk c ^ (r / 8 % 8) of channel rows and
+// c ^ (r % 8) of token rows, and eight channel rows stand 128 bytes from the next
+// eight, so that lanes i and i + 1 read from different halves of the 64 banks: no
+// bank is met twice (without that 128 bytes a fifth of the cycles were conflicts;
+// 1024 x 128256 x 4096 482 -> 467 us).
 // ---------------------------------------------------------------------------
 constexpr int kTileN = 256;                        // channel rows of a block
 constexpr int kTileThreads = 512;
@@ -753,7 +754,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tiled(Product p, in
       b = next;
     }
     int m0, n0, l = lane;
-    asm volatile("" : "+v"(l));                    // as in issue
+    asm volatile("" : "+v"(l));                    // as in load
     const int ni = (l & 15) * 8, mg = (l >> 4) * 4;
     origin(tile, m0, n0);
     const float* sw = (const float*)(lds + R * STAGE + scales * 2048) + wr * 128 + ni;
@@ -874,7 +875,9 @@ __global__ __launch_bounds__(512) void k_product_few(Product p) {
 // block quantises them all into LDS (U groups of eight elements a thread) while
 // its channel rows are on their way.  A launch less: M = 8, d = 4096, 1000 rows
 // 12.6 -> 12.0 us, M = 1 11.8 -> 8.8, 19 sequences of 46 rows, M = 8, d = 320,
-// 12.5 -> 9.8.
+// 12.5 -> 9.8.  Bound by latency and by that quantisation: at 1000 rows and d =
+// 4096 the kernel takes 8.5 us with M = 8, 5.0 with M = 1, k_product_few over rows
+// quantised before 5.7 and 4.7.
 // ---------------------------------------------------------------------------
 constexpr int kFusedBytes = 32768;                 // M * pitch, at most
 constexpr int kFusedPad = 16;                      // between token rows in LDS: no bank is met twice

@@ -696,6 +696,9 @@ struct GradArgs {
 constexpr int kGradThreads = 256;
 constexpr int kGradUnroll = 4;
 
+// Two results to a 16-bit type.  The compiler may round an fp16 product at once,
+// without a float32 between: one rounding less, and nothing compares these bit
+// for bit with a form that has both.
 template <int ET>
 __device__ __forceinline__ uint32_t narrow2(float a, float b) {
   if (ET == NS_BF16) {

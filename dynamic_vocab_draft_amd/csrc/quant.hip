@@ -564,6 +564,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_product_stream(Pro
           acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x1, f[t][1], acc[t][u], 0, 0, 0);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);             // no read moves behind the wait
       __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): this wave has read the stage
       b = b + 1 == R ? 0 : b + 1;
     }

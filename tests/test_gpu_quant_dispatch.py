@@ -66,7 +66,8 @@ def test_selection_of_many_chunks_that_tie(ns):  # noqa: F811
     check_head(ns, (wq, ws, h, I, n), 64, False, what="many chunks, ties")
 
 
-@pytest.mark.parametrize("M,N,out", [(3, 5000, "fp32"), (20, 4100, "bf16"), (64, 16400, "fp16"), (100, 66000, "bf16"), (128, 65537, "fp32")])
+@pytest.mark.parametrize("M,N,out", [(3, 5000, "fp32"), (20, 4100, "bf16"), (64, 16400, "fp16"), (100, 66000, "bf16"), (128, 65537, "fp32"),
+                                       (5000, 7, "bf16"), (70, 64, "fp32")])
 def test_outputs_past_31_bits(ns, M, N, out):  # noqa: F811
     say("quant_matmul past 31 bits", M, N, out)
     d = 130

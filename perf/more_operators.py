@@ -88,8 +88,9 @@ def draw(rng):
         return dict(op=op, b=b, m=m, k=rng.randint(1, 64), n_max=n_max, live=live, v=v, d=d, dtype=dtype, logits=logits)
     rows = _log(rng, 1, 4096)
     v = _log(rng, 64, max(64, min(152000, WHOLE // (2 * rows))))
-    return dict(op=op, rows=rows, v=v, ld=v + rng.choice((0, 0, 1, 24)), dtype=dtype, grad=rng.random() < 0.7, ref=rng.random() < 0.8,
-                temp=rng.choice((1.0, 1.0, 0.7, 1.5)), kl=rng.choice((0.0, 0.02, 0.1)), ent=rng.choice((0.0, 0.0, 0.01)), skip=rng.choice((0.0, 0.3)),
+    ref = rng.random() < 0.8
+    return dict(op=op, rows=rows, v=v, ld=v + rng.choice((0, 0, 1, 24)), dtype=dtype, grad=rng.random() < 0.7, ref=ref,
+                temp=rng.choice((1.0, 1.0, 0.7, 1.5)), kl=rng.choice((0.0, 0.02, 0.1)) if ref else 0.0, ent=rng.choice((0.0, 0.0, 0.01)), skip=rng.choice((0.0, 0.3)),
                 masked=rng.choice((0.0, 0.0, 0.5)), empty=rows > 2 and rng.random() < 0.3)
 
 

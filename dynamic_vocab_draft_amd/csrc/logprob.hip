@@ -12,88 +12,19 @@
 // is float32.
 #include "common.hpp"
 #include "lists.hpp"
+#include "logits.hpp"
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kUnroll = 4;               // 16-byte vectors per lane and batch
 constexpr int kRowWaves = 4;             // waves of a forward block
 constexpr int kMaxParts = 64;            // parts of a row, at most; a power of two of them
 constexpr int kWavesWanted = 2048;       // waves that fill the chip: eight a CU
-constexpr float kWide = 1024.f;          // |c max z| from which y is taken relative to the maximum itself
-
-__host__ __device__ constexpr int elem_bytes(int ET) { return ET == NS_FP32 ? 4 : 2; }
-__host__ __device__ constexpr int per_vec(int ET) { return 16 / elem_bytes(ET); }
-
-// 16 bytes at the element type's own alignment: rows of an odd vocabulary
-// start anywhere, and the memory system takes such loads whole.
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
-template <int ET>
-__device__ __forceinline__ float elem_of(uint32_t w, int e) {
-  if (ET == NS_BF16) return e ? ns::bf16_hi(w) : ns::bf16_lo(w);
-  return e ? ns::fp16_hi(w) : ns::fp16_lo(w);
-}
-
-template <int ET>
-__device__ __forceinline__ void widen(u32x4 x, float (&v)[per_vec(ET)]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (ET == NS_FP32) v[i] = __uint_as_float(w[i]);
-    else {
-      v[2 * i] = elem_of<ET>(w[i], 0);
-      v[2 * i + 1] = elem_of<ET>(w[i], 1);
-    }
-  }
-}
-
-template <int ET>
-__device__ __forceinline__ u32x4 minus_inf() {
-  const uint32_t w = ET == NS_BF16 ? 0xFF80FF80u : (ET == NS_FP16 ? 0xFC00FC00u : 0xFF800000u);
-  return u32x4{w, w, w, w};
-}
-
-template <int ET>
-__device__ __forceinline__ float one_elem(const void* z, size_t i) {
-  if (ET == NS_FP32) return ((const float*)z)[i];
-  const uint32_t w = ((const uint16_t*)z)[i];
-  return elem_of<ET>(w, 0);
-}
-
-__device__ __forceinline__ float exp2_fast(float y) { return __builtin_amdgcn_exp2f(y); }
-
 // The smallest float above v (NaN above +infinity, which nothing reaches).
 __device__ __forceinline__ float next_up(float v) {
   const uint32_t u = __float_as_uint(v);
   if (v == INFINITY) return __uint_as_float(0x7FC00000u);
   if ((u & 0x7FFFFFFFu) == 0) return __uint_as_float(1u);
   return __uint_as_float(u & 0x80000000u ? u - 1 : u + 1);
-}
-
-// Statistics of a part of a row: y = c (z - ref) - E.
-struct Stat {
-  float top, ref, E, S, W;
-};
-
-// b joined to a, both with some finite value or none (top = -inf, S = 0).
-// A NaN or an infinite sum stays one.
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
-  const bool first = a.top >= b.top;
-  Stat r = first ? a : b;
-  const Stat o = first ? b : a;
-  const float shift = c * (o.ref - r.ref) + (o.E - r.E);
-  const float f = exp2_fast(shift);
-  if (o.S == 0.f) return r;
-  if (f > 0.f) {
-    r.S += f * o.S;
-    r.W += f * (o.W + o.S * shift);
-  } else if (!(o.S < INFINITY)) {
-    r.S = o.S;
-  }
-  return r;
 }
 
 // Orders a wave's own LDS writes before its following reads.
@@ -349,73 +280,8 @@ __device__ __forceinline__ void put_top(const Args& a, const Row& r, size_t row,
 template <int ET, bool TOP>
 __device__ __forceinline__ void take(const u32x4 (&x)[kUnroll], int q0, int q1, float c, Stat& st, Best& best,
                                      int lane) {
-  constexpr int EPV = per_vec(ET);
-  float mx[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    float v[EPV];
-    widen<ET>(x[u], v);
-    float m = v[0];
-#pragma unroll
-    for (int e = 1; e < EPV; ++e) m = fmaxf(m, v[e]);
-    mx[u] = m;
-  }
-  float lane_max = mx[0];
-#pragma unroll
-  for (int u = 1; u < kUnroll; ++u) lane_max = fmaxf(lane_max, mx[u]);
-  const float top = ns::wave_max_f32(lane_max);
-  if (top > st.top) {                                      // uniform
-    const bool had = st.top != -INFINITY;
-    st.top = top;
-    if (fabsf(top * c) < kWide) {
-      const float E = rintf(top * c);
-      if (!had || st.ref != 0.f || E > st.E + 4.f) {
-        const float shift = had ? c * st.ref + (st.E - E) : 0.f;
-        const float f = exp2_fast(shift);
-        st.W = f > 0.f ? f * (st.W + st.S * shift) : 0.f;
-        st.S *= f;
-        st.ref = 0.f;
-        st.E = E;
-      }
-    } else {
-      const float shift = had ? c * (st.ref - top) + st.E : 0.f;
-      const float f = exp2_fast(shift);
-      st.W = f > 0.f ? f * (st.W + st.S * shift) : 0.f;
-      st.S *= f;
-      st.ref = top;
-      st.E = 0.f;
-    }
-  }
-  // A batch is summed by itself first: shorter chains of roundings.
-  float S = 0.f, W = 0.f;
-  const float E = st.E, ref = st.ref;
-  if (ref == 0.f) {                                        // uniform
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float v[EPV];
-      widen<ET>(x[u], v);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) {
-        const float y = fmaf(v[e], c, -E), p = exp2_fast(y);
-        S += p;
-        W = fmaf(p, fmaxf(y, -200.f), W);                  // 2^y is 0 for masked logits: no 0 * inf
-      }
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float v[EPV];
-      widen<ET>(x[u], v);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) {
-        const float y = (v[e] - ref) * c, p = exp2_fast(y);
-        S += p;
-        W = fmaf(p, fmaxf(y, -200.f), W);
-      }
-    }
-  }
-  st.S += S;
-  st.W += W;
+  float mx[kUnroll], lane_max;
+  const float top = add_batch<ET>(x, c, st, mx, lane_max);
   if (TOP) {
     if (best.fresh) best.start(lane_max, lane);
     if (top >= best.least) best.take_batch<ET>(x, mx, q0 + lane, q1, lane);   // uniform
@@ -695,25 +561,6 @@ struct GradArgs {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradUnroll = 4;
-
-// Two results to a 16-bit type.  The compiler may round an fp16 product at once,
-// without a float32 between: one rounding less, and nothing compares these bit
-// for bit with a form that has both.
-template <int ET>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
-  if (ET == NS_BF16) {
-    const __bf16 x = (__bf16)a, y = (__bf16)b;
-    return (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
-  }
-  const _Float16 x = (_Float16)a, y = (_Float16)b;
-  return (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
-}
-
-template <int ET>
-__device__ __forceinline__ void put_elem(void* d, size_t i, float v) {
-  if (ET == NS_FP32) ((float*)d)[i] = v;
-  else ((uint16_t*)d)[i] = (uint16_t)narrow2<ET>(v, 0.f);
-}
 
 constexpr float kNear = 1024.f;          // |lse| up to which probabilities come from lse itself
 constexpr float kFar = 0x1p24f;          // |lse| beyond which a row's gradient is 0

@@ -1,0 +1,392 @@
+// 4-bit rows: microscaled floating point.  Quantisation, rows read back, the
+// product, and the restricted LM head over 4-bit rows.
+//
+// 32 consecutive elements share a power of two.  With a = max |x_i| of a block
+//     e = floor(log2 a) - 2  (at least -127; -127 for a block of zeros),
+//     q_i = x_i / 2^e to E2M1 (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives),
+//           nearest, halfway cases to the even code, 6 beyond 6,
+// and the scale is kept as the byte e + 127, 255 for a block with a NaN or an
+// infinity, whose products are NaN.  The product
+//     out[m, n] = sum_b 2^(ex[m, b] + ew[n, b]) sum_{i in b} xq[m, i] wq[n, i]
+// is one scaled matrix instruction for every 128 elements.  Products of two
+// codes are quarters of integers, and a float32 sum stays exact while its terms'
+// scales lie within some 2^10 of one another (d = 4096), which those of usual
+// rows do; results then do not depend on how the sum was split.
+#include "common.hpp"
+#include "head_top.hpp"
+#include "lds_loads.hpp"
+#include "rows.hpp"
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 256;                        // elements: 128 bytes of codes, 8 scales
+constexpr int kChunkBytes = kChunk / 2, kChunkScales = kChunk / 32;
+__host__ __device__ constexpr int chunks_of(int d) { return (d + kChunk - 1) / kChunk; }
+__host__ __device__ constexpr int pitch_of(int d) { return chunks_of(d) * kChunkBytes; }
+
+// ---------------------------------------------------------------------------
+// Quantisation: one pass.  A lane takes eight elements, four lanes a block, so
+// a row's 256-element chunk is half a wave's.
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256;
+constexpr int kRowUnits = 4;                       // chunks of a half wave
+
+// c / d for c < 2^26 and d <= 64, from 2^32 / d rounded up: the product is over
+// by less than c d / 2^32 < 1 / d.  0 stands for 2^32.
+__host__ __device__ __forceinline__ uint32_t reciprocal_of(uint32_t d) { return d == 1 ? 0u : 0xFFFFFFFFu / d + 1u; }
+__device__ __forceinline__ uint32_t divided(uint32_t c, uint32_t rcp) { return rcp == 0 ? c : __umulhi(c, rcp); }
+
+// The largest value of four lanes.
+__device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);    // quad_perm 1 0 3 2
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);             // quad_perm 2 3 0 1
+  return o > v ? o : v;
+}
+
+// The scale byte from the float32 bits of the block's largest magnitude.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  const uint32_t e = top >> 23;                    // biased; 255 for infinities and NaN
+  return e == 255 ? 255u : (e > 2 ? e - 2 : 0u);
+}
+
+// 2^(byte - 127) as a float, the smallest one a subnormal; not for 255.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+
+// Eight elements to eight codes, the first in the lowest bits.
+template <int ET>
+__device__ __forceinline__ uint32_t quant_eight(const Eight<ET>& x, uint32_t byte) {
+  const float s = scale_value(byte);
+  uint32_t r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x.get(0), x.get(1), s, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x.get(2), x.get(3), s, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x.get(4), x.get(5), s, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x.get(6), x.get(7), s, 3);
+  return byte == 255 ? 0u : r;
+}
+
+// The block's largest magnitude, as float32 bits, from what a lane holds of it.
+template <int ET>
+__device__ __forceinline__ uint32_t block_top(const Eight<ET>& x) {
+  const uint32_t m = x.top(0);
+  float top;
+  if (ET == NS_FP32) top = __uint_as_float(m);
+  else {
+    const uint32_t lo = m & 0xFFFFu, hi = m >> 16, b = lo > hi ? lo : hi;
+    top = ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b);
+  }
+  return quad_max_u32(__float_as_uint(top));       // float32 bits order the same way
+}
+
+template <int ET>
+__global__ __launch_bounds__(kRowThreads) void k_mx4_rows(const void* __restrict__ x, int64_t ld, int R, int d,
+                                                          uint32_t rcp, uint8_t* __restrict__ q,
+                                                          uint8_t* __restrict__ scale) {
+  const int per_row = chunks_of(d), total = R * per_row;   // below 2^26
+  const int l = threadIdx.x & 31, c0 = (int)blockIdx.x * (kRowThreads / 32 * kRowUnits) + (threadIdx.x >> 5);
+  const int tail = d & ~(ET == NS_FP32 ? 3 : 7);
+  Eight<ET> v[kRowUnits];
+#pragma unroll
+  for (int u = 0; u < kRowUnits; ++u) {
+    const int c = c0 + u * (kRowThreads / 32), cc = c < total ? c : total - 1;
+    const int r = (int)divided((uint32_t)cc, rcp);
+    const char* row = (const char*)x + (size_t)r * (size_t)ld * (ET == NS_FP32 ? 4 : 2);
+    v[u].load(row, (cc - r * per_row) * kChunk + l * 8, 4, tail, Eight<ET>::rest_of(row, tail, d));
+  }
+  NS_ISSUE_FENCE();
+#pragma unroll
+  for (int u = 0; u < kRowUnits; ++u) {
+    const int c = c0 + u * (kRowThreads / 32);
+    if (c >= total) continue;                      // whole half waves
+    const uint32_t byte = scale_byte(block_top<ET>(v[u]));
+    *(uint32_t*)(q + (size_t)c * kChunkBytes + l * 4) = quant_eight<ET>(v[u], byte);
+    if ((l & 3) == 0) scale[(size_t)c * kChunkScales + (l >> 2)] = (uint8_t)byte;
+  }
+}
+
+int mx4_rows(const void* x, int64_t ld, int R, int d, int dtype, uint8_t* q, uint8_t* scale, hipStream_t stream) {
+  constexpr int per_block = kRowThreads / 32 * kRowUnits;
+  const int total = R * chunks_of(d);
+  const uint32_t rcp = reciprocal_of((uint32_t)chunks_of(d));
+  const dim3 grid((unsigned)((total + per_block - 1) / per_block)), block(kRowThreads);
+  if (dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_rows<NS_BF16>, grid, block, 0, stream, x, ld, R, d, rcp, q, scale);
+  else if (dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_rows<NS_FP16>, grid, block, 0, stream, x, ld, R, d, rcp, q, scale);
+  else hipLaunchKernelGGL(k_mx4_rows<NS_FP32>, grid, block, 0, stream, x, ld, R, d, rcp, q, scale);
+  return ns_launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Rows read back: out[j, :] = values of row ids[j].
+// ---------------------------------------------------------------------------
+// Eight codes to eight values.
+__device__ __forceinline__ void values_of(uint32_t codes, uint32_t byte, float (&v)[8]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const float s = scale_value(byte), nan = __uint_as_float(0x7FC00000u);
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 3);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y; v[4] = c.x; v[5] = c.y; v[6] = e.x; v[7] = e.y;
+  if (byte == 255) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = nan;
+  }
+}
+
+template <int OT>
+__global__ __launch_bounds__(kRowThreads) void k_mx4_gather(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                                                            int V, int d, uint32_t rcp, const int32_t* __restrict__ ids,
+                                                            const int32_t* __restrict__ n_dev, int n_max,
+                                                            void* __restrict__ out, int64_t ld) {
+  const int per_row = chunks_of(d);
+  int n = n_dev ? *n_dev : n_max;
+  n = n < 0 ? 0 : (n > n_max ? n_max : n);
+  const int total = n * per_row;                   // below 2^26
+  const int l = threadIdx.x & 31, c0 = (int)blockIdx.x * (kRowThreads / 32 * kRowUnits) + (threadIdx.x >> 5);
+  uint32_t codes[kRowUnits], byte[kRowUnits];
+  int row[kRowUnits], at[kRowUnits];
+#pragma unroll
+  for (int u = 0; u < kRowUnits; ++u) {
+    const int c = c0 + u * (kRowThreads / 32);
+    row[u] = -1;
+    if (c >= total) continue;
+    const int j = (int)divided((uint32_t)c, rcp), id = ids ? ids[j] : j;
+    at[u] = c - j * per_row;
+    if (id < 0 || id >= V) continue;
+    const size_t from = (size_t)id * per_row + at[u];
+    codes[u] = *(const uint32_t*)(q + from * kChunkBytes + l * 4);
+    byte[u] = scale[from * kChunkScales + (l >> 2)];
+    at[u] = at[u] * kChunk + l * 8;
+    row[u] = j;
+  }
+#pragma unroll
+  for (int u = 0; u < kRowUnits; ++u) {
+    if (row[u] < 0 || at[u] >= d) continue;
+    float v[8];
+    values_of(codes[u], byte[u], v);
+    store_eight<OT>(out, (size_t)row[u] * (size_t)ld + at[u], v, d - at[u]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product
+// ---------------------------------------------------------------------------
+struct Product {
+  const uint8_t* x;         // [B][M][pitch]
+  const uint8_t* xs;        // [B][M][pitch / 16]
+  const uint8_t* w;         // [rows][pitch]
+  const uint8_t* ws;        // [rows][pitch / 16]
+  const int32_t* ids;       // [B][N] row of column j, or NULL: j
+  const int32_t* n_dev;     // [B] live columns, or NULL: N
+  int M, N, V, pitch;
+  void* out;                // [B][M][N], elements of a token `sm` apart for m, `sn` for n
+  int64_t sm, sn;
+};
+
+// 16 x 16 outputs over 128 elements.  Lane (i, g) holds 32 elements of row i of
+// each operand, one block, and byte `STEP` of sa and sb is that block's scale;
+// which elements a place holds is free as long as both operands agree.
+template <int STEP>
+__device__ __forceinline__ f32x4 product128(i32x4 a, i32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+  const i32x8 x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, STEP, (int)sa, STEP, (int)sb);
+}
+
+// ---------------------------------------------------------------------------
+// A block of eight waves owns 16 channel rows and up to 64 token rows
+// (blockIdx.z of them); each wave takes an eighth of the row's chunks and the
+// eight sums are joined in LDS.  Lane (i, g) reads 32 bytes of a chunk, blocks
+// 2 g and 2 g + 1.
+// ---------------------------------------------------------------------------
+template <int OT, int NMT>
+__global__ __launch_bounds__(512) void k_mx4_few(Product p) {
+  __shared__ f32x4 sh[8][NMT][NS_WAVE];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int m0 = (int)blockIdx.z * NMT * 16;         // tokens in groups
+  const size_t seq = blockIdx.y;
+  const int M = p.M - m0, spitch = p.pitch / 16;     // tokens from here on
+  const int j0 = (int)blockIdx.x * 16, j = j0 + i < p.N ? j0 + i : p.N - 1;
+  int n = p.n_dev ? p.n_dev[seq] : p.N;
+  int id = p.ids ? p.ids[seq * p.N + j] : j;
+  n = n < p.N ? n : p.N;
+  if (j0 >= n) return;
+  id = id < 0 || id >= p.V ? 0 : id;                 // a hole reads row 0; nobody reads its output
+  const int chunks = p.pitch / kChunkBytes, per = (chunks + 7) / 8;
+  const int k0 = w * per, k1 = k0 + per < chunks ? k0 + per : chunks;
+  const uint8_t* wr = p.w + (size_t)id * p.pitch + g * 32;
+  const uint8_t* wsr = p.ws + (size_t)id * spitch + g * 2;
+  const uint8_t* xr[NMT];
+  const uint8_t* xsr[NMT];
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) {
+    const size_t m = seq * p.M + m0 + (u * 16 + i < M ? u * 16 + i : M - 1);
+    xr[u] = p.x + m * p.pitch + g * 32;
+    xsr[u] = p.xs + m * spitch + g * 2;
+  }
+  f32x4 acc[NMT] = {};
+  for (int k = k0; k < k1; ++k) {
+    const i32x4 a0 = *(const i32x4*)(wr + (size_t)k * kChunkBytes), a1 = *(const i32x4*)(wr + (size_t)k * kChunkBytes + 16);
+    const uint32_t sa = *(const uint16_t*)(wsr + k * kChunkScales);
+#pragma unroll
+    for (int u = 0; u < NMT; ++u) {
+      const i32x4 b0 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes), b1 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes + 16);
+      const uint32_t sb = *(const uint16_t*)(xsr[u] + k * kChunkScales);
+      acc[u] = product128<0>(b0, a0, acc[u], sb, sa);
+      acc[u] = product128<1>(b1, a1, acc[u], sb, sa);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) sh[w][u][lane] = acc[u];
+  __syncthreads();
+  // wave u joins token operand u; lane (i, g) holds tokens 4 g .. 4 g + 3 of channel i
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) {
+    if (u != w) continue;
+    f32x4 s = sh[0][u][lane];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += sh[q][u][lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = u * 16 + g * 4 + r;
+      if (m < M && j0 + i < n)
+        store_out<OT>(p.out, (seq * p.M + m0 + m) * (size_t)p.sm + (size_t)(j0 + i) * (size_t)p.sn, s[r]);
+    }
+  }
+}
+
+template <int OT, int NMT>
+void launch_few(const Product& p, int B, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)B, (unsigned)((p.M + NMT * 16 - 1) / (NMT * 16)));
+  hipLaunchKernelGGL((k_mx4_few<OT, NMT>), grid, dim3(512), 0, stream, p);
+}
+
+template <int OT>
+void launch_few_of(const Product& p, int B, hipStream_t stream) {
+  if (p.M <= 16) launch_few<OT, 1>(p, B, stream);
+  else if (p.M <= 32) launch_few<OT, 2>(p, B, stream);
+  else if (p.M <= 48) launch_few<OT, 3>(p, B, stream);
+  else launch_few<OT, 4>(p, B, stream);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Workspace of the restricted head: the quantised hidden rows and their
+// scales, the logits, and the chunks' keys.
+struct HeadWs {
+  size_t q, scale, z, cand, bytes;
+  int64_t ld;
+  int chunks;
+};
+
+HeadWs head_ws(int B, int n_max, int M, int k, int d) {
+  HeadWs w;
+  w.ld = ((int64_t)n_max + 3) / 4 * 4;
+  w.chunks = (n_max + top_chunk(n_max) - 1) / top_chunk(n_max);
+  const size_t rows = (size_t)B * M;
+  w.q = 0;
+  w.scale = w.q + align256(rows * pitch_of(d));
+  w.z = w.scale + align256(rows * (pitch_of(d) / 16));
+  w.cand = w.z + align256(rows * (size_t)w.ld * 4);
+  w.bytes = w.cand + (w.chunks > 1 ? align256(rows * w.chunks * (size_t)k * 8) : 0);
+  return w;
+}
+
+constexpr int64_t kMaxLd = (int64_t)1 << 40;       // no product with a row count overflows
+
+bool known_dtype(int t) { return t == NS_BF16 || t == NS_FP32 || t == NS_FP16; }
+bool aligned(const void* p, int to) { return (((uintptr_t)p) & (uintptr_t)(to - 1)) == 0; }
+bool elem_aligned(const void* p, int dtype) { return aligned(p, dtype == NS_FP32 ? 4 : 2); }
+// Codes are read 16 bytes at a time, scales up to eight.
+bool rows_aligned(const void* q, const void* scale) { return aligned(q, 16) && aligned(scale, 8); }
+
+bool head_dims_ok(int B, int n_max, int M, int k, int d) {
+  return B >= 1 && B <= NS_MAX_BATCH && n_max >= 1 && n_max <= NS_MAX_V && M >= 1 && M <= NS_MAX_M && k >= 1 &&
+         k <= NS_MAX_K && d >= 1 && d <= NS_MAX_D;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t nanospec_mx4_pitch(int32_t d) { return d < 1 || d > NS_MAX_D ? 0 : pitch_of(d); }
+
+int nanospec_mx4_rows(const void* x, int64_t ld, int32_t R, int32_t d, int32_t dtype, uint8_t* q, uint8_t* scale,
+                      hipStream_t stream) {
+  if (!known_dtype(dtype)) return NS_EDTYPE;
+  if (R < 0 || R > NS_MAX_ROWS || d < 1 || d > NS_MAX_D || ld < d || ld > kMaxLd) return NS_EINVAL;
+  if (R == 0) return NS_OK;
+  if (!x || !q || !scale || !rows_aligned(q, scale) || !elem_aligned(x, dtype)) return NS_EINVAL;
+  (void)hipGetLastError();
+  return mx4_rows(x, ld, R, d, dtype, q, scale, stream);
+}
+
+int nanospec_mx4_gather_rows(const uint8_t* q, const uint8_t* scale, int32_t V, int32_t d, const int32_t* ids,
+                             const int32_t* n_dev, int32_t n_max, void* out, int64_t ld_out, int32_t out_dtype,
+                             hipStream_t stream) {
+  if (!known_dtype(out_dtype)) return NS_EDTYPE;
+  if (V < 1 || V > NS_MAX_V || n_max < 0 || n_max > NS_MAX_ROWS || (!ids && n_max > V) || d < 1 || d > NS_MAX_D ||
+      ld_out < d || ld_out > kMaxLd)
+    return NS_EINVAL;
+  if (n_max == 0) return NS_OK;
+  if (!q || !scale || !out || !rows_aligned(q, scale) || !elem_aligned(out, out_dtype)) return NS_EINVAL;
+  (void)hipGetLastError();
+  constexpr int per_block = kRowThreads / 32 * kRowUnits;
+  const uint32_t rcp = reciprocal_of((uint32_t)chunks_of(d));
+  const dim3 grid((unsigned)((n_max * chunks_of(d) + per_block - 1) / per_block)), block(kRowThreads);
+  if (out_dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_gather<NS_BF16>, grid, block, 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld_out);
+  else if (out_dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_gather<NS_FP16>, grid, block, 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld_out);
+  else hipLaunchKernelGGL(k_mx4_gather<NS_FP32>, grid, block, 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld_out);
+  return ns_launch_status();
+}
+
+int nanospec_mx4_matmul(const uint8_t* xq, const uint8_t* xs, int32_t M, const uint8_t* wq, const uint8_t* ws, int32_t N,
+                        int32_t d, void* out, int64_t ld_out, int32_t out_dtype, hipStream_t stream) {
+  if (!known_dtype(out_dtype)) return NS_EDTYPE;
+  if (M < 0 || M > NS_MAX_ROWS || N < 1 || N > NS_MAX_V || d < 1 || d > NS_MAX_D || ld_out < N ||
+      ld_out > kMaxLd)
+    return NS_EINVAL;
+  if (M == 0) return NS_OK;
+  if (!xq || !xs || !wq || !ws || !out || !rows_aligned(xq, xs) || !rows_aligned(wq, ws)) return NS_EINVAL;
+  if (!elem_aligned(out, out_dtype)) return NS_EINVAL;
+  (void)hipGetLastError();
+  const Product p{xq, xs, wq, ws, nullptr, nullptr, M, N, N, pitch_of(d), out, ld_out, 1};
+  if (out_dtype == NS_FP32) launch_few_of<NS_FP32>(p, 1, stream);
+  else if (out_dtype == NS_BF16) launch_few_of<NS_BF16>(p, 1, stream);
+  else launch_few_of<NS_FP16>(p, 1, stream);
+  return ns_launch_status();
+}
+
+size_t nanospec_mx4_logits_workspace_bytes(int32_t B, int32_t n_max, int32_t M, int32_t k, int32_t d) {
+  return head_dims_ok(B, n_max, M, k, d) ? head_ws(B, n_max, M, k, d).bytes : 0;
+}
+
+int nanospec_mx4_logits_topk(const uint8_t* wq, const uint8_t* wscale, const int32_t* row_ids, const int32_t* n_dev,
+                             int32_t n_max, int32_t B, int32_t V, int32_t d, const void* h, int32_t dtype, int32_t M,
+                             int32_t k, float* logits, int32_t* topk_ids, float* topk_vals, void* ws,
+                             size_t ws_bytes, hipStream_t stream) {
+  if (!known_dtype(dtype)) return NS_EDTYPE;
+  if (!head_dims_ok(B, n_max, M, k, d) || V < 1 || V > NS_MAX_V || (!row_ids && n_max > V)) return NS_EINVAL;
+  if (!wq || !wscale || !h || !topk_ids || !topk_vals || !ws) return NS_EINVAL;
+  if (!rows_aligned(wq, wscale) || !aligned(ws, 256) || !elem_aligned(h, dtype)) return NS_EINVAL;
+  const HeadWs l = head_ws(B, n_max, M, k, d);
+  if (ws_bytes < l.bytes) return NS_ECAPACITY;
+  (void)hipGetLastError();
+  char* base = (char*)ws;
+  uint8_t* hq = (uint8_t*)(base + l.q);
+  uint8_t* hs = (uint8_t*)(base + l.scale);
+  float* z = (float*)(base + l.z);
+  int rc = mx4_rows(h, d, B * M, d, dtype, hq, hs, stream);
+  if (rc != NS_OK) return rc;
+  const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
+  launch_few_of<NS_FP32>(p, B, stream);
+  rc = ns_launch_status();
+  if (rc != NS_OK) return rc;
+  const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};
+  return launch_top(t, l.chunks, B, stream);
+}
+
+}  // extern "C"

@@ -11,7 +11,9 @@
 // rounded once to the output type, so results do not depend on how the sum
 // was split, and two runs agree bit for bit.
 #include "common.hpp"
-#include "select.hpp"
+#include "head_top.hpp"
+#include "lds_loads.hpp"
+#include "rows.hpp"
 
 namespace {
 
@@ -26,76 +28,6 @@ __host__ __device__ constexpr int pitch_of(int d) { return (d + kPitch - 1) / kP
 // the rounding (128256 x 4096 bf16 269 us, 5.9 TB/s read and written; 30000 x
 // 4096 float32 99 us, 6.2).
 // ---------------------------------------------------------------------------
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x4 u32x4_any __attribute__((aligned(2)));   // rows start at any element
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-
-template <int ET>
-__device__ __forceinline__ uint32_t load_bits(const void* x, size_t i) {
-  return ET == NS_FP32 ? ((const uint32_t*)x)[i] : ((const uint16_t*)x)[i];
-}
-
-// Eight elements as they are stored: 16-bit types in one vector, float32 in two.
-template <int ET>
-struct Eight {
-  u32x4 v[ET == NS_FP32 ? 2 : 1];
-
-  // elements i .. i + 7 of a row, or i .. i + 3 and `step` on, zeros at or past
-  // d.  `tail` is d rounded down to a vector's elements, `rest` what follows in
-  // the row.  The loads stand under no condition that differs from lane to lane.
-  __device__ __forceinline__ void load(const char* row, int i, int step, int tail, u32x4 rest) {
-    constexpr int N = ET == NS_FP32 ? 2 : 1;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int at = i + n * step;
-      u32x4 x = {0, 0, 0, 0};
-      if (tail > 0) x = __builtin_nontemporal_load((const u32x4_any*)(row + (size_t)(at < tail ? at : 0) * (2 * N)));
-      v[n] = at < tail ? x : (at == tail ? rest : u32x4{0, 0, 0, 0});
-    }
-  }
-  // Elements tail .. d - 1, fewer than a vector's, and zeros.
-  static __device__ __forceinline__ u32x4 rest_of(const char* row, int tail, int d) {
-    u32x4 r = {0, 0, 0, 0};
-    if (tail < d) {                                // uniform
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (ET == NS_FP32) {
-          if (tail + c < d) r[c] = load_bits<ET>(row, tail + c);
-        } else {
-          if (tail + c * 2 < d) r[c] = load_bits<ET>(row, tail + c * 2);
-          if (tail + c * 2 + 1 < d) r[c] |= load_bits<ET>(row, tail + c * 2 + 1) << 16;
-        }
-      }
-    }
-    return r;
-  }
-  __device__ __forceinline__ float get(int e) const {
-    if constexpr (ET == NS_FP32) return __uint_as_float(v[e >> 2][e & 3]);
-    else if constexpr (ET == NS_BF16) return e & 1 ? ns::bf16_hi(v[0][e >> 1]) : ns::bf16_lo(v[0][e >> 1]);
-    else return e & 1 ? ns::fp16_hi(v[0][e >> 1]) : ns::fp16_lo(v[0][e >> 1]);
-  }
-  // The largest magnitude as the type's own bits, which order like the values
-  // with infinities and NaN on top; two at once for 16-bit types.
-  __device__ __forceinline__ uint32_t top(uint32_t so_far) const {
-    if constexpr (ET == NS_FP32) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t u = v[n][c] & 0x7FFFFFFFu;
-          so_far = u > so_far ? u : so_far;
-        }
-      return so_far;
-    } else {
-      u16x2 m = __builtin_bit_cast(u16x2, so_far);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[0][c] & 0x7FFF7FFFu));
-      return __builtin_bit_cast(uint32_t, m);
-    }
-  }
-};
-
 // How a row is quantised: 0 for one of zeros or with a value that is not
 // finite (q = 0), otherwise values times `up`, a = up max |x|, rcp = 1 / a.
 // `up` brings the maximum into [2^-100, 2^100], where 1 / a and 127 a are far
@@ -158,18 +90,6 @@ __device__ __forceinline__ u32x2 quant_eight(const Eight<ET>& x, const Scaling& 
 // The row's scale from its maximum's float32 bits.
 __device__ __forceinline__ float scale_of(uint32_t m) {
   return m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.f;
-}
-
-// Maximum over the 16 lanes of a row, in every lane.
-__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
-  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);    // quad_perm 1 0 3 2
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);             // quad_perm 2 3 0 1
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);            // row_half_mirror
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true);            // row_mirror
-  return o > v ? o : v;
 }
 
 constexpr int kQuantThreads = 256;
@@ -274,20 +194,6 @@ int quant_rows(const void* x, int64_t ld, int R, int d, int dtype, int8_t* q, fl
 // Scaled value of an exact integer sum.
 __device__ __forceinline__ float scaled(int acc, float s) { return (float)acc * s; }
 
-// A float32 value as it is: without this the compiler forms mixed-precision
-// multiplies that round a product to fp16 at once.
-__device__ __forceinline__ float as_float32(float v) {
-  asm("" : "+v"(v));
-  return v;
-}
-
-template <int OT>
-__device__ __forceinline__ void store_out(void* out, size_t i, float v) {
-  if (OT == NS_FP32) ((float*)out)[i] = v;
-  else if (OT == NS_BF16) ((__bf16*)out)[i] = (__bf16)v;
-  else ((_Float16*)out)[i] = (_Float16)as_float32(v);
-}
-
 struct Product {
   const int8_t* x;          // [B][M][pitch]
   const float* xs;          // [B][M]
@@ -301,85 +207,6 @@ struct Product {
 };
 
 constexpr int kStageK = 128;                       // bytes of a row in a stage
-
-// 16 bytes a lane from a buffer straight into LDS at byte `lds` (the same
-// for the wave) + 16 * lane.  The compiler does not count these loads: the
-// waits below do.  m0 holds the LDS address.  The compiler does not see a
-// memory instruction here either, so the asm keeps the distances itself: the
-// move and the no-ops are the five wait states from a vector instruction that
-// wrote an SGPR (v_readlane, as for a spilled one) to a memory instruction that
-// reads it, and more than the one from the move to the load.  m0 is a register
-// that the compiler reserves and writes before each use of its own, so it warns
-// of the clobber, which tells it that the value is gone.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :
-               : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-               : "memory", "m0");
-}
-
-// The same for bytes that are read once: the caches need not keep them.
-__device__ __forceinline__ void load_to_lds_once(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-               :
-               : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-               : "memory", "m0");
-}
-
-// The same for four bytes a lane.
-__device__ __forceinline__ void load_word_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :
-               : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-               : "memory", "m0");
-}
-
-#pragma clang diagnostic pop
-
-__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
-  const uint64_t a = (uint64_t)p;
-  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00027000u};
-}
-
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
-template <int OT>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
-  if (OT == NS_BF16) {
-    const __bf16 x = (__bf16)a, y = (__bf16)b;
-    return (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
-  }
-  const _Float16 x = (_Float16)as_float32(a), y = (_Float16)as_float32(b);
-  return (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
-}
-
-// Eight consecutive outputs, n of them inside the row.
-template <int OT>
-__device__ __forceinline__ void store_eight(void* out, size_t i, const float (&v)[8], int n) {
-  if (n >= 8) {
-    if (OT == NS_FP32) {
-      u32x4_any* d = (u32x4_any*)((float*)out + i);
-      d[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-      d[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
-    } else {
-      *(u32x4_any*)((uint16_t*)out + i) = u32x4{narrow2<OT>(v[0], v[1]), narrow2<OT>(v[2], v[3]),
-                                                narrow2<OT>(v[4], v[5]), narrow2<OT>(v[6], v[7])};
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) store_out<OT>(out, i + e, v[e]);
-  }
-}
 
 // ---------------------------------------------------------------------------
 // The product for up to 128 token rows: bound by the bytes of the channel rows,
@@ -1105,102 +932,6 @@ void launch_head(const Product& p, int B, hipStream_t stream) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// Top-k over the scaled logits of each hidden row
-// ---------------------------------------------------------------------------
-// Columns of a thread: 4 cover 4096 columns in one block; 16, for more, cover
-// 16384 (64 x 15500: 11.5 us in chunks of 4096 with a join, 7.8 us in one).
-constexpr int top_cols(int n_max) { return n_max <= 4 * kSelectThreads ? 4 : 16; }
-constexpr int top_chunk(int n_max) { return kSelectThreads * top_cols(n_max); }
-
-struct Top {
-  const float* z;           // [B][M] rows, ld floats apart
-  int64_t ld;
-  const int32_t* ids;
-  const int32_t* n_dev;
-  int n_max, V, M, k;
-  float* logits;            // [B][M][n_max] or NULL
-  int32_t* out_ids;
-  float* out_vals;
-  uint64_t* cand;           // [B][M][chunks][k]
-};
-
-__device__ __forceinline__ void put_top(const Top& t, size_t row, int r, uint64_t key) {
-  t.out_ids[row * t.k + r] = key ? ns::key_id(key) : -1;
-  t.out_vals[row * t.k + r] = key ? ns::key_val(key) : -INFINITY;
-}
-
-// Block (m, c, b): the k best of chunk c of hidden row m of sequence b.
-template <int U>
-__global__ __launch_bounds__(kSelectThreads) void k_top_chunk(Top t) {
-  constexpr int CHUNK = U * kSelectThreads;
-  __shared__ SelectSmem sm;
-  const int m = blockIdx.x, c = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const size_t row = (size_t)b * t.M + m;
-  const int j0 = c * CHUNK;
-  int n = t.n_dev ? t.n_dev[b] : t.n_max;
-  // Every column is asked for before the first is looked at; the first four of
-  // a thread together with the count, live or not.
-  float val[U];
-  int id[U];
-  const auto ask = [&](int u, int end) {
-    const int q = j0 + tid + u * kSelectThreads, j = q < end ? q : end - 1;
-    val[u] = t.z[row * (size_t)t.ld + j];
-    id[u] = t.ids ? t.ids[(size_t)b * t.n_max + j] : j;
-  };
-#pragma unroll
-  for (int u = 0; u < 4; ++u) ask(u, t.n_max);
-  NS_ISSUE_FENCE();
-  n = n < 0 ? 0 : (n > t.n_max ? t.n_max : n);
-  const bool final_here = n <= CHUNK;
-  if (final_here && c > 0) return;
-  const int lim = n - j0 < CHUNK ? n - j0 : CHUNK;       // <= 0 where nothing is live
-  if (U > 4) {
-    const int end = n > 0 ? n : 1;
-#pragma unroll
-    for (int u = 4; u < U; ++u) ask(u, end);
-    NS_ISSUE_FENCE();
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int q = tid + u * kSelectThreads;
-    const bool live = q < lim && id[u] >= 0 && id[u] < t.V;
-    if (live && t.logits) t.logits[row * (size_t)t.n_max + j0 + q] = val[u];
-    if (!live || val[u] != val[u]) {                     // NaN is never selected
-      val[u] = 0.f;
-      id[u] = -1;
-    }
-  }
-  const int nlive = lim > 0 ? lim : 0;
-  if (final_here)
-    block_select_topk<U>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { put_top(t, row, r, x); });
-  else {
-    uint64_t* dst = t.cand + (row * gridDim.y + c) * (size_t)t.k;
-    block_select_topk<U>(val, id, t.k, nlive, sm, [&](int r, uint64_t x) { dst[r] = x; });
-  }
-}
-
-// Block (m, b): the k best of the nk = chunks * k keys of its chunks.
-template <int U>
-__global__ __launch_bounds__(kSelectThreads) void k_top_keys(Top t, int nk) {
-  __shared__ SelectSmem sm;
-  const int m = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  int n = t.n_dev ? t.n_dev[b] : t.n_max;
-  if (n > t.n_max) n = t.n_max;
-  if (n <= top_chunk(t.n_max)) return;
-  const size_t row = (size_t)b * t.M + m;
-  float val[U];
-  int id[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int q = tid + u * kSelectThreads;
-    const uint64_t key = q < nk ? t.cand[row * nk + q] : 0;
-    val[u] = key ? ns::key_val(key) : 0.f;
-    id[u] = key ? ns::key_id(key) : -1;
-  }
-  block_select_topk<U>(val, id, t.k, nk, sm, [&](int r, uint64_t x) { put_top(t, row, r, x); });
-}
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of the restricted head: the quantised hidden rows and their
@@ -1302,18 +1033,7 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;
   const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};
-  const dim3 chunks((unsigned)M, (unsigned)l.chunks, (unsigned)B);
-  if (top_cols(n_max) == 4) hipLaunchKernelGGL(k_top_chunk<4>, chunks, dim3(kSelectThreads), 0, stream, t);
-  else hipLaunchKernelGGL(k_top_chunk<16>, chunks, dim3(kSelectThreads), 0, stream, t);
-  rc = ns_launch_status();
-  if (rc != NS_OK || l.chunks == 1) return rc;
-  const int nk = l.chunks * k;
-  const dim3 grid((unsigned)M, (unsigned)B), block(kSelectThreads);
-  static_assert((NS_MAX_V + top_chunk(NS_MAX_V) - 1) / top_chunk(NS_MAX_V) * NS_MAX_K <= 4 * kSelectThreads,
-                "k_top_keys<4> holds every chunk's keys");
-  if (nk <= kSelectThreads) hipLaunchKernelGGL(k_top_keys<1>, grid, block, 0, stream, t, nk);
-  else hipLaunchKernelGGL(k_top_keys<4>, grid, block, 0, stream, t, nk);
-  return ns_launch_status();
+  return launch_top(t, l.chunks, B, stream);
 }
 
 }  // extern "C"

@@ -134,6 +134,19 @@ _SIGS = {
     "nanospec_quant_logits_workspace_bytes": (c_size, [c_int32] * 5),
     "nanospec_quant_logits_topk": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_int32, c_int32, c_int32, c_int32, c_vp,
                                                   c_int32, c_int32, c_int32, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "nanospec_mx4_pitch": (c_int32, [c_int32]),
+    "nanospec_mx4_rows": (ctypes.c_int, [c_vp, c_int64, c_int32, c_int32, c_int32, c_vp, c_vp, c_vp]),
+    "nanospec_mx4_gather_rows": (ctypes.c_int, [c_vp, c_vp, c_int32, c_int32, c_vp, c_vp, c_int32, c_vp, c_int64,
+                                                c_int32, c_vp]),
+    "nanospec_mx4_matmul": (ctypes.c_int, [c_vp, c_vp, c_int32, c_vp, c_vp, c_int32, c_int32, c_vp, c_int64, c_int32,
+                                           c_vp]),
+    "nanospec_mx4_logits_workspace_bytes": (c_size, [c_int32] * 5),
+    "nanospec_mx4_logits_topk": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_int32, c_int32, c_int32, c_int32, c_vp,
+                                                c_int32, c_int32, c_int32, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "nanospec_policy_loss_workspace_bytes": (c_size, [c_int32] * 2),
+    "nanospec_policy_loss": (ctypes.c_int, [c_vp, c_int64, c_int32, c_int32, c_int32, c_float, c_vp, c_vp, c_vp, c_vp,
+                                            c_vp, c_float, c_float, c_float, c_float, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                            c_int64, c_vp, c_size, c_vp]),
     "nanospec_token_logprobs_workspace_bytes": (c_size, [c_int32] * 3),
     "nanospec_token_logprobs": (ctypes.c_int, [c_vp, c_int64, c_int32, c_int32, c_int32, c_float, c_vp, c_int32,
                                                c_int32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
@@ -562,7 +575,7 @@ def alloc_workspace(n_max: int, M: int, k: int, d: int, device="cuda") -> torch.
 
 
 # ---------------------------------------------------------------------------
-# 8-bit rows and token log-probabilities.  Sizes come from the tensors, so the
+# Quantised rows, token log-probabilities and the policy loss.  Sizes come from the tensors, so the
 # tensors are checked here: device, type, shape and strides.  A small call
 # takes a few microseconds on the GPU, so each check is one expression and the
 # reason is looked for only where it fails.
@@ -688,6 +701,80 @@ def nanospec_quant_logits_topk(wq: torch.Tensor, wscale: torch.Tensor, row_ids: 
             *_workspace(work, where, dev))
 
 
+def nanospec_mx4_pitch(d: int) -> int:
+    return _lib.nanospec_mx4_pitch(d)
+
+
+def _mx4(q, scale, where: str, names: str, rows: int, d: int, dev: int):
+    """The addresses of 4-bit rows and their scales."""
+    pitch = _lib.nanospec_mx4_pitch(d)
+    name = names.split()
+    return (_tensor(q, where, name[0], _UINT8, (rows, pitch), dev),
+            _tensor(scale, where, name[1], _UINT8, (rows, pitch // 16), dev))
+
+
+def nanospec_mx4_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
+    """x [R, d] (rows contiguous, any row stride) -> q [R, pitch], scale [R, pitch / 16] uint8."""
+    where = "nanospec_mx4_rows"
+    R, d, ld, code, dev = _matrix(x, where, "x")
+    _launch(where, _lib.nanospec_mx4_rows, dev, stream, x.data_ptr(), ld, R, d, code,
+            *_mx4(q, scale, where, "q scale", R, d, dev))
+
+
+def nanospec_mx4_gather_rows(q: torch.Tensor, scale: torch.Tensor, ids: Optional[torch.Tensor],
+                             n_dev: Optional[torch.Tensor], out: torch.Tensor, stream=None) -> None:
+    """Rows ids [n] (None: the first n) of q [V, pitch], scale [V, pitch / 16] -> out [n, d] (rows contiguous, any row
+    stride); n_dev [1] or None: all n."""
+    where = "nanospec_mx4_gather_rows"
+    n, d, ld, code, dev = _matrix(out, where, "out")
+    _want(isinstance(q, torch.Tensor) and q.dim() == 2, where, "q is no [V, pitch] tensor")
+    V = q.shape[0]
+    _launch(where, _lib.nanospec_mx4_gather_rows, dev, stream, *_mx4(q, scale, where, "q scale", V, d, dev), V, d,
+            None if ids is None else _tensor(ids, where, "ids", _INT32, (n,), dev),
+            None if n_dev is None else _tensor(n_dev, where, "n_dev", _INT32, (1,), dev), n, out.data_ptr(), ld, code)
+
+
+def nanospec_mx4_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, d: int,
+                        out: torch.Tensor, stream=None) -> None:
+    """xq [M, pitch], wq [N, pitch] with scales xs [M, pitch / 16], ws [N, pitch / 16] -> out [M, N] (rows contiguous, any
+    row stride)."""
+    where = "nanospec_mx4_matmul"
+    M, N, ld, code, dev = _matrix(out, where, "out")
+    x, w = _mx4(xq, xs, where, "xq xs", M, d, dev), _mx4(wq, ws, where, "wq ws", N, d, dev)
+    _launch(where, _lib.nanospec_mx4_matmul, dev, stream, *x, M, *w, N, d, out.data_ptr(), ld, code)
+
+
+def nanospec_mx4_logits_workspace_bytes(B: int, n_max: int, M: int, k: int, d: int) -> int:
+    return _lib.nanospec_mx4_logits_workspace_bytes(B, n_max, M, k, d)
+
+
+def nanospec_mx4_logits_topk(wq: torch.Tensor, wscale: torch.Tensor, row_ids: Optional[torch.Tensor],
+                             n_dev: Optional[torch.Tensor], h: torch.Tensor, k: int, logits: Optional[torch.Tensor],
+                             topk_ids: torch.Tensor, topk_vals: torch.Tensor, work: torch.Tensor,
+                             stream=None) -> None:
+    """The head over 4-bit rows: wq [V, pitch], wscale [V, pitch / 16], h [B, M, d], row_ids [B, n_max] (None: all V
+    rows), n_dev [B] or None."""
+    where = "nanospec_mx4_logits_topk"
+    if not (isinstance(h, torch.Tensor) and h.get_device() >= 0 and h.dtype in _FLOATS and h.dim() == 3
+            and h.is_contiguous()):
+        _misfit(h, where, "h", _FLOATS, None, h.get_device() if isinstance(h, torch.Tensor) else -1)
+    dev = h.get_device()
+    B, M, d = h.shape
+    _want(isinstance(wq, torch.Tensor) and wq.dim() == 2, where, "wq is no [V, pitch] tensor")
+    V = n_max = wq.shape[0]
+    if row_ids is not None:
+        _want(isinstance(row_ids, torch.Tensor) and row_ids.dim() == 2, where, "row_ids is no [B, n_max] tensor")
+        n_max = row_ids.shape[1]
+    _launch(where, _lib.nanospec_mx4_logits_topk, dev, stream, *_mx4(wq, wscale, where, "wq wscale", V, d, dev),
+            None if row_ids is None else _tensor(row_ids, where, "row_ids", _INT32, (B, n_max), dev),
+            None if n_dev is None else _tensor(n_dev, where, "n_dev", _INT32, (B,), dev), n_max, B, V, d,
+            h.data_ptr(), _FLOATS[h.dtype], M, k,
+            None if logits is None else _tensor(logits, where, "logits", _F32, (B, M, n_max), dev),
+            _tensor(topk_ids, where, "topk_ids", _INT32, (B, M, k), dev),
+            _tensor(topk_vals, where, "topk_vals", _F32, (B, M, k), dev),
+            *_workspace(work, where, dev))
+
+
 def nanospec_token_logprobs_workspace_bytes(L: int, V: int, k: int) -> int:
     return _lib.nanospec_token_logprobs_workspace_bytes(L, V, k)
 
@@ -746,6 +833,42 @@ def nanospec_token_logprobs_grad(logits: torch.Tensor, inv_temp: float, tokens: 
             None if g_lse is None else _tensor(g_lse, where, "g_lse", _F32, (L,), dev), dlogits.data_ptr(), ld_d)
 
 
+def nanospec_policy_loss_workspace_bytes(L: int, V: int) -> int:
+    return _lib.nanospec_policy_loss_workspace_bytes(L, V)
+
+
+def nanospec_policy_loss(logits: torch.Tensor, inv_temp: float, tokens: torch.Tensor, old_logprob: torch.Tensor,
+                         ref_logprob: Optional[torch.Tensor], advantage: torch.Tensor, weight: Optional[torch.Tensor],
+                         eps_low: float, eps_high: float, kl_coef: float, ent_coef: float, loss: torch.Tensor,
+                         logprob: torch.Tensor, kl: Optional[torch.Tensor], entropy: Optional[torch.Tensor],
+                         g_loss: Optional[torch.Tensor], dlogits: Optional[torch.Tensor], work: torch.Tensor,
+                         stream=None) -> None:
+    """logits [L, V] (rows contiguous, any row stride), tokens and the other rows' values [L] (ref_logprob, weight, kl,
+    entropy: or None), loss [1], g_loss [1] or None, dlogits [L, V] of the logits' dtype, or None; it may be logits."""
+    where = "nanospec_policy_loss"
+    L, V, ld, code, dev = _matrix(logits, where, "logits")
+    ld_d = 0
+    if dlogits is not None:
+        L_d, V_d, ld_d, code_d, dev_d = _matrix(dlogits, where, "dlogits")
+        if L_d != L or V_d != V or dev_d != dev:
+            _want(False, where, f"dlogits is {(L_d, V_d)} on device {dev_d}, not {(L, V)} on {dev}")
+        if code_d != code:
+            _want(False, where, f"dlogits has dtype {dlogits.dtype}, not {logits.dtype}", NS_EDTYPE)
+    shape = (L,)
+    _launch(where, _lib.nanospec_policy_loss, dev, stream, logits.data_ptr(), ld, L, V, code, inv_temp,
+            _tensor(tokens, where, "tokens", _INT32, shape, dev),
+            _tensor(old_logprob, where, "old_logprob", _F32, shape, dev),
+            None if ref_logprob is None else _tensor(ref_logprob, where, "ref_logprob", _F32, shape, dev),
+            _tensor(advantage, where, "advantage", _F32, shape, dev),
+            None if weight is None else _tensor(weight, where, "weight", _F32, shape, dev),
+            eps_low, eps_high, kl_coef, ent_coef, _tensor(loss, where, "loss", _F32, (1,), dev),
+            _tensor(logprob, where, "logprob", _F32, shape, dev),
+            None if kl is None else _tensor(kl, where, "kl", _F32, shape, dev),
+            None if entropy is None else _tensor(entropy, where, "entropy", _F32, shape, dev),
+            None if g_loss is None else _tensor(g_loss, where, "g_loss", _F32, (1,), dev),
+            None if dlogits is None else dlogits.data_ptr(), ld_d, *_workspace(work, where, dev))
+
+
 def _alloc(nbytes: int, where: str, device) -> torch.Tensor:
     if nbytes == 0:
         raise NanoSpecError(NS_EINVAL, where)
@@ -763,3 +886,13 @@ def alloc_quant_logits_workspace(B: int, n_max: int, M: int, k: int, d: int, dev
 def alloc_token_logprobs_workspace(L: int, V: int, k: int, device="cuda") -> torch.Tensor:
     """A 256-byte-aligned uint8 workspace of nanospec_token_logprobs_workspace_bytes."""
     return _alloc(nanospec_token_logprobs_workspace_bytes(L, V, k), "nanospec_token_logprobs_workspace_bytes", device)
+
+
+def alloc_mx4_logits_workspace(B: int, n_max: int, M: int, k: int, d: int, device="cuda") -> torch.Tensor:
+    """A 256-byte-aligned uint8 workspace of nanospec_mx4_logits_workspace_bytes."""
+    return _alloc(nanospec_mx4_logits_workspace_bytes(B, n_max, M, k, d), "nanospec_mx4_logits_workspace_bytes", device)
+
+
+def alloc_policy_loss_workspace(L: int, V: int, device="cuda") -> torch.Tensor:
+    """A 256-byte-aligned uint8 workspace of nanospec_policy_loss_workspace_bytes."""
+    return _alloc(nanospec_policy_loss_workspace_bytes(L, V), "nanospec_policy_loss_workspace_bytes", device)

@@ -82,7 +82,7 @@ extern "C" {
 #define NS_MAX_BATCH  4096      /* sequences in one batch */
 #define NS_MAX_SLOTS  16384     /* slots of a slot-stable packed buffer */
 #define NS_MAX_TREE_CAND 4096   /* candidates of one nanospec_tree_select */
-#define NS_MAX_ROWS   1048576   /* rows of one quant_rows, quant_matmul or token_logprobs call */
+#define NS_MAX_ROWS   1048576   /* rows of one call over quantised rows or rows of logits */
 #define NS_MIN_INV_TEMP 9.5367431640625e-07f  /* inverse temperatures: 2^-20 .. */
 #define NS_MAX_INV_TEMP 1048576.0f            /* .. 2^20 */
 
@@ -613,6 +613,80 @@ int nanospec_quant_logits_topk(const int8_t* wq, const float* wscale, const int3
                                hipStream_t stream);
 
 /* ======================================================================
+ * 4-bit rows: microscaled floating point, a quarter of the bytes of bf16 rows.
+ * 32 consecutive elements of a row share a power of two (the last block of a
+ * row may be shorter).  With a the block's largest magnitude
+ *     e = floor(log2 a) - 2  (at least -127; -127 for a block of zeros),
+ *     q_i = x_i / 2^e as E2M1: 0, 1/2, 1, 3/2, 2, 3, 4, 6 (codes 0 .. 7) and
+ *           their negatives (codes 8 .. 15), the nearest, halfway cases to the
+ *           even code, magnitudes beyond 6 to 6;
+ * the element stands for q_i 2^e.  The block's scale is the byte e + 127; a block
+ * holding a NaN or an infinity has scale 255 (NaN) and zeros, so that it cannot
+ * pass unseen.
+ * Row r's codes start at q + r * nanospec_mx4_pitch(d), pitch being half of d
+ * rounded up to 256; byte i holds element 2 i in its low half.  Its scales start
+ * at scale + r * pitch / 16.  Codes and scales behind the d-th element are zero,
+ * which the products below rely on (callers who lay out rows of their own clear
+ * them).
+ *   nanospec_mx4_pitch : bytes of one row's codes; 0 if d is outside [1, NS_MAX_D].
+ *   nanospec_mx4_rows  : quantises R rows.
+ *     x     : rows of d elements of `dtype`, ld >= d elements apart, at any
+ *             address their element type may have.
+ *     q     : [R x pitch], 16-byte aligned.  scale : [R x pitch / 16], 8-byte
+ *             aligned.
+ * R = 0 enqueues nothing.  R <= NS_MAX_ROWS.
+ * Errors: NS_EINVAL (nulls, limits, misalignment), NS_EDTYPE, NS_EHIP. */
+int32_t nanospec_mx4_pitch(int32_t d);
+int nanospec_mx4_rows(const void* x, int64_t ld, int32_t R, int32_t d, int32_t dtype, uint8_t* q,
+                      uint8_t* scale, hipStream_t stream);
+
+/* 4-bit rows read back, as nanospec_gather_rows copies others: out[j, :] =
+ * values of row ids[j] for j < n, each rounded once to out_dtype.
+ *   q, scale : rows as above, V of them.
+ *   ids      : [n_max] row ids; ids outside [0, V) leave out[j] untouched.  NULL:
+ *              row j (n_max <= V).
+ *   n_dev    : [1] row count on the device, clamped to [0, n_max]; NULL: n_max.
+ *   out      : rows of d elements of out_dtype, ld_out >= d elements apart; rows
+ *              j >= n and what lies between rows are untouched.
+ * n_max in [0, NS_MAX_ROWS] (0 enqueues nothing).  A block of scale 255 is NaN.
+ * Errors: NS_EINVAL, NS_EDTYPE, NS_EHIP. */
+int nanospec_mx4_gather_rows(const uint8_t* q, const uint8_t* scale, int32_t V, int32_t d,
+                             const int32_t* ids, const int32_t* n_dev, int32_t n_max, void* out,
+                             int64_t ld_out, int32_t out_dtype, hipStream_t stream);
+
+/* The product of M 4-bit token rows and N 4-bit channel rows:
+ *     out[m, n] = sum_i x[m, i] w[n, i]
+ * over the values that the codes stand for, summed in float32 and rounded once
+ * to out_dtype.  Rows whose blocks differ little in scale (by 2^10 at d = 4096)
+ * sum without rounding, so that the result does not depend on how the work was
+ * split; in general the order of the sum is a function of M, N and d.
+ * out[m, n] is NaN where either row has a block of scale 255.
+ *   xq, xs, wq, ws : rows as above.
+ *   out            : [M] rows of N elements of out_dtype, ld_out >= N elements
+ *                    apart; what lies between rows is untouched.
+ * M in [0, NS_MAX_ROWS] (0 enqueues nothing), N in [1, NS_MAX_V].
+ * Errors: NS_EINVAL (nulls, limits, misalignment), NS_EDTYPE, NS_EHIP. */
+int nanospec_mx4_matmul(const uint8_t* xq, const uint8_t* xs, int32_t M, const uint8_t* wq,
+                        const uint8_t* ws, int32_t N, int32_t d, void* out, int64_t ld_out,
+                        int32_t out_dtype, hipStream_t stream);
+
+/* nanospec_draft_logits_topk and its batched form over 4-bit rows of W_head
+ * (NS_INDEXED): for each of B sequences the M hidden rows are quantised as by
+ * nanospec_mx4_rows, multiplied as by nanospec_mx4_matmul with the rows row_ids
+ * names, and the k largest logits of each are written with their ids.  Arguments
+ * as of nanospec_quant_logits_topk, with
+ *   wq, wscale : W_head's 4-bit rows [V x pitch] and scales [V x pitch / 16].
+ * NaN logits are never selected.
+ * Errors: NS_EINVAL, NS_EDTYPE, NS_ECAPACITY (ws too small), NS_EHIP. */
+size_t nanospec_mx4_logits_workspace_bytes(int32_t B, int32_t n_max, int32_t M, int32_t k,
+                                           int32_t d);
+int nanospec_mx4_logits_topk(const uint8_t* wq, const uint8_t* wscale, const int32_t* row_ids,
+                             const int32_t* n_dev, int32_t n_max, int32_t B, int32_t V, int32_t d,
+                             const void* h, int32_t dtype, int32_t M, int32_t k, float* logits,
+                             int32_t* topk_ids, float* topk_vals, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* ======================================================================
  * Log-probabilities of given tokens under full-vocabulary logits, with
  * entropy and top alternatives: the target's side of verification (the
  * children of each tree node), prompt log-probabilities, and, with the
@@ -669,6 +743,55 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
                                  float inv_temp, const int32_t* tokens, int32_t T, const float* lse,
                                  const float* entropy, const float* g_logprob, const float* g_entropy,
                                  const float* g_lse, void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/* ======================================================================
+ * Clipped policy loss with a KL term and an entropy bonus over full-vocabulary
+ * logits, with its gradient: training on tokens that an older policy, or one
+ * with quantised rows, has drawn.  For row i with token a and logp as above:
+ *     r = exp(logp_a - old),  s = min(r A, clip(r, 1 - eps_low, 1 + eps_high) A),
+ *     delta = ref - logp_a,   kl = exp(delta) - delta - 1,
+ *     loss_i = w (-s + kl_coef kl - ent_coef entropy),   loss = sum_i loss_i,
+ *     g = w (-r A [r A <= clip(r) A] + kl_coef (1 - exp(delta))),
+ *     dlogits[i, j] = g_loss inv_temp (g ([j = a] - p_j)
+ *                     + w ent_coef p_j (logp_j + entropy)).
+ *   logits      : L rows of V elements of `dtype`, ld >= V elements apart, at any
+ *                 address their element type may have.
+ *   tokens      : [L] the token of each row.
+ *   old_logprob, advantage : [L] float32.
+ *   ref_logprob : [L] float32, or NULL without a KL term (kl_coef = 0, kl NULL).
+ *   weight      : [L] float32 w, a mask and what the loss is divided by in one;
+ *                 NULL: ones.
+ *   eps_low     : in [0, 1];  eps_high : >= 0, INFINITY allowed;  kl_coef,
+ *                 ent_coef : finite.
+ *   loss        : [1];  logprob : [L];  kl, entropy : [L] or NULL; float32.
+ *   g_loss      : [1] on the device, or NULL (one); only the gradient has it.
+ *   dlogits     : L rows of `dtype`, ld_d >= V elements apart, or NULL for the loss
+ *                 alone; either the logits themselves (ld_d = ld), which it then
+ *                 replaces, or memory apart from them.  What lies between rows is
+ *                 untouched.
+ *   ws          : >= nanospec_policy_loss_workspace_bytes(L, V) bytes, 256-byte
+ *                 aligned, no initialisation needed.  The size never falls as L or
+ *                 V grows.  Calls sharing a workspace must be ordered (two captured
+ *                 graphs among them).
+ * A row of weight 0, or whose token lies outside [0, V) (padding), is not looked
+ * at: logprob, kl, entropy, loss and gradient 0, whatever its logits.
+ * A token of probability 0 (logit -INFINITY, or a logprob below -104, where
+ * float32 has none) cannot have been drawn and teaches nothing: kl, loss and
+ * gradient 0.  A row of logits -INFINITY alone has logprob -INFINITY and entropy
+ * 0.  A row with a NaN or +INFINITY has no distribution: all of its outputs, the
+ * loss and its gradient are NaN.
+ * Statistics are float32, what follows from them once a row float64; values past
+ * float32's range become infinite, probabilities below 2^-126 zero in the gradient.  No atomics, so results repeat bit for bit.
+ * L = 0 gives loss 0.  L <= NS_MAX_ROWS, inv_temp as above.
+ * Errors: NS_EINVAL, NS_EDTYPE, NS_ECAPACITY (ws too small), NS_EHIP. */
+size_t nanospec_policy_loss_workspace_bytes(int32_t L, int32_t V);
+int nanospec_policy_loss(const void* logits, int64_t ld, int32_t L, int32_t V, int32_t dtype,
+                         float inv_temp, const int32_t* tokens, const float* old_logprob,
+                         const float* ref_logprob, const float* advantage, const float* weight,
+                         float eps_low, float eps_high, float kl_coef, float ent_coef, float* loss,
+                         float* logprob, float* kl, float* entropy, const float* g_loss,
+                         void* dlogits, int64_t ld_d, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
 
 #ifdef __cplusplus
 }

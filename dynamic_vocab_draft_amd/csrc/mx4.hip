@@ -12,6 +12,8 @@
 // codes are quarters of integers, and a float32 sum stays exact while its terms'
 // scales lie within some 2^10 of one another (d = 4096), which those of usual
 // rows do; results then do not depend on how the sum was split.
+#include <type_traits>
+
 #include "common.hpp"
 #include "head_top.hpp"
 #include "lds_loads.hpp"
@@ -188,12 +190,12 @@ struct Product {
 };
 
 // 16 x 16 outputs over 128 elements.  Lane (i, g) holds 32 elements of row i of
-// each operand, one block, and byte `STEP` of sa and sb is that block's scale;
+// each operand, one block, and a byte of sa and sb is that block's scale;
 // which elements a place holds is free as long as both operands agree.
-template <int STEP>
+template <int BYTE_A, int BYTE_B>
 __device__ __forceinline__ f32x4 product128(i32x4 a, i32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
   const i32x8 x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, STEP, (int)sa, STEP, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BYTE_A, (int)sa, BYTE_B, (int)sb);
 }
 
 // ---------------------------------------------------------------------------
@@ -235,8 +237,8 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
     for (int u = 0; u < NMT; ++u) {
       const i32x4 b0 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes), b1 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes + 16);
       const uint32_t sb = *(const uint16_t*)(xsr[u] + k * kChunkScales);
-      acc[u] = product128<0>(b0, a0, acc[u], sb, sa);
-      acc[u] = product128<1>(b1, a1, acc[u], sb, sa);
+      acc[u] = product128<0, 0>(b0, a0, acc[u], sb, sa);
+      acc[u] = product128<1, 1>(b1, a1, acc[u], sb, sa);
     }
   }
 #pragma unroll
@@ -258,6 +260,233 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The product for many token rows: compute-bound, tiles in LDS.
+//
+// A block of eight waves owns 256 channel rows and TB * 64 token rows of the
+// output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
+// token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
+// in stages of one chunk a row (128 bytes of codes and 8 scales), two in LDS
+// (72 KB each with TB = 4), three with TB = 1, whose short stages end before a
+// load does, filled by direct global-to-LDS loads.  While one half of a stage (four blocks a
+// row) is multiplied, the next half is read into a second set of registers;
+// once a wave holds a stage's second half and the next stage has landed, one
+// block barrier frees the stage's place for the stage after next.
+//
+// Blocks stay: each takes one tile after the other, and the stages of all its
+// tiles are one stream of loads, so the next tile's first stages arrive while
+// the last ones of this tile are multiplied and its outputs are stored.  Tiles
+// go to the blocks of one XCD from one contiguous run, in groups of four channel
+// tiles by all token tiles, so that its 32 CUs share rows in its L2.
+//
+// Lane i of channel operand t is channel row 8 i + t, so the eight
+// accumulators of a lane are eight consecutive outputs and a store of 16
+// lanes covers 128 of them, without a detour through LDS.  Lane (i, g) takes
+// blocks 2 g and 2 g + 1 of a chunk, whose two scales are one 16-bit read.
+//
+// Place c of row r in LDS holds 16-byte block c ^ (r / 8 % 8) of channel rows and
+// c ^ (r % 8) of token rows, and eight channel rows stand 128 bytes from the next
+// eight, so that lanes i and i + 1 read from different halves of the 64 banks;
+// scales stand in the order in which the lanes read them, so that 16 lanes read
+// 16 consecutive ones: no bank is met twice.
+// ---------------------------------------------------------------------------
+constexpr int kTileN = 256;                        // channel rows of a block
+constexpr int kTileThreads = 512;
+constexpr int tile_stages(int tb) { return tb == 1 ? 3 : 2; }   // in LDS
+constexpr int kEightRows = 9 * kChunkBytes;        // eight channel rows in LDS and 128 bytes between them and the next
+
+template <int OT, int TB>
+__global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int tiles_m, int tiles_n) {
+  constexpr int TM = TB * 64;                      // token rows of a block
+  constexpr int XOFF = kTileN / 8 * kEightRows, SOFF = XOFF + TM * kChunkBytes, STAGE = SOFF + 2 * 256 * kChunkScales;
+  constexpr int LA = kTileN / 64, LB = TM / 64, LW = LA + LB + 2;   // loads of a wave and stage: 8 rows each, and scales
+  constexpr int STORES = TB * 4 * (OT == NS_FP32 ? 2 : 1);   // of a wave and whole tile
+  constexpr int R = tile_stages(TB), AHEAD = (R - 2) * LW;   // loads that may be out when a stage must be here
+  static_assert(AHEAD + STORES < 64, "vmcnt range");
+  __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
+  const int total = tiles_m * tiles_n, per = (total + 7) / 8, slots = (int)(gridDim.x >> 3);
+  const int first = (int)(blockIdx.x & 7) * per, end = first + per < total ? first + per : total;
+  int tile = first + (int)(blockIdx.x >> 3);
+  if (tile >= end) return;
+  const auto origin = [&](int t, int& m0, int& n0) {
+    const int group = t / (tiles_m * 4), rest = t % (tiles_m * 4);
+    const int wide = tiles_n - group * 4 < 4 ? tiles_n - group * 4 : 4;   // channel tiles of this group
+    n0 = (group * 4 + rest % wide) * kTileN;
+    m0 = rest / wide * TM;
+  };
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int S = p.pitch / kChunkBytes, spitch = p.pitch / 16;
+  const uint32_t base = lds_offset(lds);
+
+  // The stream of loads: stage `lk` of tile `lt` comes next.
+  int lt = tile, lk = 0;
+  u32x4 ra, rb, rsa, rsb;
+  int last_a, last_b;                              // rows past the end read the last one and are not stored
+  const auto aim = [&]() {
+    int m0, n0;
+    origin(lt, m0, n0);
+    last_a = p.N - 1 - n0;
+    last_b = p.M - 1 - m0;
+    ra = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(kTileN * p.pitch));
+    rb = buffer_of(p.x + (size_t)m0 * p.pitch, (uint32_t)(TM * p.pitch));
+    rsa = buffer_of(p.ws + (size_t)n0 * spitch, (uint32_t)(kTileN * spitch));
+    rsb = buffer_of(p.xs + (size_t)m0 * spitch, (uint32_t)(TM * spitch));
+  };
+  // Load u of the next stage's LW, into buffer buf.
+  const auto load = [&](int u, int buf) {
+    int l = lane;                                  // opaque: the few values below are computed anew each
+    asm volatile("" : "+v"(l));                    // time instead of being held in registers all along
+    if (u < LA + LB) {
+      const int v = u < LA ? u : u - LA, r = (v * 8 + w) * 8 + (l >> 3), last = u < LA ? last_a : last_b;
+      const int block = (l & 7) ^ (u < LA ? w : l >> 3);
+      load_to_lds(u < LA ? ra : rb, __umul24(r < last ? r : last, p.pitch) + block * 16, lk * kChunkBytes,
+                  base + buf * STAGE + (u < LA ? (v * 8 + w) * kEightRows : XOFF + (v * 8 + w) * 8 * kChunkBytes));
+    } else {
+      // scales of 32 rows; place t * 16 + i of a wave's 128 channel rows holds row 8 i + t
+      const int q = w * 32 + (l >> 1);
+      const int r = u == LA + LB ? (q & 128) + (q & 15) * 8 + (q >> 4 & 7) : q, last = u == LA + LB ? last_a : last_b;
+      load_word_to_lds(u == LA + LB ? rsa : rsb, __umul24(r < last ? r : last, spitch) + (l & 1) * 4, lk * kChunkScales,
+                       base + buf * STAGE + SOFF + (u == LA + LB ? 0 : 256 * kChunkScales) + w * 256);
+    }
+  };
+  // Behind a stage's loads: on to the next stage.
+  const auto advance = [&]() {
+    if (++lk == S) {                               // behind the last tile the stream reads that tile again,
+      lk = 0;                                      // which spares every load a question
+      if (lt + slots < end) {
+        lt += slots;
+        aim();
+      }
+    }
+  };
+
+  const int wr = w >> 2, wc = w & 3;
+  f32x4 acc[8][TB] = {};
+  // The channel operands of the half that is multiplied, 6 and 7 apart: the
+  // next half's replace 0 to 5 as they fall free, and 6 and 7 alternate, so
+  // that no read is still to come behind the half's last products.
+  i32x4 fa[6], fe[2][2], fb[2][TB];
+  // Scales of the stage that is multiplied, two operands' in a register; the next
+  // stage's replace the channels' as they fall free.
+  u16x2 sa[4], sb[(TB + 1) / 2], nb[(TB + 1) / 2];
+  // operand t: channel rows wr * 128 + 8 i + t; operand u: token rows (wc * TB + u) * 16 + i
+  const char* la = lds + (wr * 16 + i) * kEightRows;
+  const char* lb = lds + XOFF + (wc * TB * 16 + i) * kChunkBytes;
+  const char* lsa = lds + SOFF + (wr * 128 + i) * kChunkScales + g * 2;
+  const char* lsb = lds + SOFF + (256 + wc * TB * 16 + i) * kChunkScales + g * 2;
+  const int place0 = ((2 * g) ^ (i & 7)) * 16, place1 = ((2 * g + 1) ^ (i & 7)) * 16;
+  const auto channel_scales = [&](int t, int buf) {
+    sa[t / 2][t & 1] = *(const uint16_t*)(lsa + buf * STAGE + t * 16 * kChunkScales);
+  };
+  const auto token_scales = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < TB; ++u) nb[u / 2][u & 1] = *(const uint16_t*)(lsb + buf * STAGE + u * 16 * kChunkScales);
+  };
+  aim();
+#pragma unroll
+  for (int buf = 0; buf < R; ++buf) {
+#pragma unroll
+    for (int u = 0; u < LW; ++u) load(u, buf);
+    advance();
+  }
+  wait_loads<AHEAD + LW>();
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  token_scales(0);
+#pragma unroll
+  for (int u = 0; u < (TB + 1) / 2; ++u) sb[u] = nb[u];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) channel_scales(t, 0);
+#pragma unroll
+  for (int u = 0; u < TB; ++u) fb[0][u] = *(const i32x4*)(lb + place0 + u * 16 * kChunkBytes);
+#pragma unroll
+  for (int t = 0; t < 6; ++t) fa[t] = *(const i32x4*)(la + place0 + t * kChunkBytes);
+  fe[0][0] = *(const i32x4*)(la + place0 + 6 * kChunkBytes);
+  fe[0][1] = *(const i32x4*)(la + place0 + 7 * kChunkBytes);
+  // Multiplies the half F in registers (fe, fb of F) and reads the next from
+  // `at`.  With F = 1 the next stage's loads go out between the products, one
+  // for each operand, and its scales are read.
+  const auto step = [&](auto half, int at, int buf, int next) {
+    constexpr int F = decltype(half)::value;
+    if (F == 1) token_scales(next);
+#pragma unroll
+    for (int u = 0; u < TB; ++u) fb[1 - F][u] = *(const i32x4*)(lb + at + u * 16 * kChunkBytes);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (F == 1) {
+        load(t, buf);
+        if (t + 8 < LW) load(t + 8, buf);
+      }
+      const i32x4 a = t < 6 ? fa[t % 6] : fe[F][t & 1];
+#pragma unroll
+      for (int u = 0; u < TB; ++u) {
+        const uint32_t x = __builtin_bit_cast(uint32_t, sb[u / 2]), y = __builtin_bit_cast(uint32_t, sa[t / 2]);
+        if (u % 2 == 0 && t % 2 == 0) acc[t][u] = product128<F, F>(fb[F][u], a, acc[t][u], x, y);
+        else if (u % 2 == 0) acc[t][u] = product128<F, 2 + F>(fb[F][u], a, acc[t][u], x, y);
+        else if (t % 2 == 0) acc[t][u] = product128<2 + F, F>(fb[F][u], a, acc[t][u], x, y);
+        else acc[t][u] = product128<2 + F, 2 + F>(fb[F][u], a, acc[t][u], x, y);
+        asm volatile("" : "+v"(acc[t][u]));        // the product stays here, between the loads
+      }
+      if (t < 6) fa[t % 6] = *(const i32x4*)(la + at + t * kChunkBytes);
+      if (t == 3 || t == 4) fe[1 - F][t - 3] = *(const i32x4*)(la + at + (t + 3) * kChunkBytes);
+      if (F == 1 && t % 2 == 1) {
+        channel_scales(t - 1, next);
+        channel_scales(t, next);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int b = 0;
+  bool stored = false;                             // the tile before was whole: STORES stores are behind the loads
+  for (; tile < end; tile += slots) {
+    for (int s = 0; s < S; ++s) {
+      step(std::integral_constant<int, 0>(), b * STAGE + place1, 0, 0);
+      __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0): this wave has read the stage
+      if (s == 0 && stored) wait_loads<AHEAD + STORES>();
+      else wait_loads<AHEAD>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      const int next = b + 1 == R ? 0 : b + 1;
+      step(std::integral_constant<int, 1>(), next * STAGE + place0, b, next);
+#pragma unroll
+      for (int u = 0; u < (TB + 1) / 2; ++u) sb[u] = nb[u];
+      advance();
+      b = next;
+    }
+    int m0, n0, l = lane;
+    asm volatile("" : "+v"(l));                    // as in load
+    const int ni = (l & 15) * 8, mg = (l >> 4) * 4;
+    origin(tile, m0, n0);
+    const int n = n0 + wr * 128 + ni;
+    stored = m0 + TM <= p.M && n0 + kTileN <= p.N;
+#pragma unroll
+    for (int u = 0; u < TB; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int m = m0 + (wc * TB + u) * 16 + mg + r;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[e][u][r];
+        const size_t at = (size_t)m * (size_t)p.sm + n;
+        if (stored) store_eight<OT>(p.out, at, v, 8);
+        else if (m < p.M && n < p.N) store_eight<OT>(p.out, at, v, p.N - n);
+      }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int u = 0; u < TB; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  wait_loads<0>();                                 // the stream's last loads end before their LDS is given back
+}
+
+template <int OT, int TB>
+void launch_tiled(const Product& p, hipStream_t stream) {
+  const int tm = (p.M + TB * 64 - 1) / (TB * 64), tn = (p.N + kTileN - 1) / kTileN;
+  // one block a CU, eight XCDs of 32 CUs
+  const unsigned per = ((unsigned)tm * (unsigned)tn + 7) / 8;
+  hipLaunchKernelGGL((k_mx4_tiled<OT, TB>), dim3((per < 32 ? per : 32) * 8), dim3(kTileThreads), 0, stream, p, tm, tn);
+}
+
 template <int OT, int NMT>
 void launch_few(const Product& p, int B, hipStream_t stream) {
   const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)B, (unsigned)((p.M + NMT * 16 - 1) / (NMT * 16)));
@@ -270,6 +499,24 @@ void launch_few_of(const Product& p, int B, hipStream_t stream) {
   else if (p.M <= 32) launch_few<OT, 2>(p, B, stream);
   else if (p.M <= 48) launch_few<OT, 3>(p, B, stream);
   else launch_few<OT, 4>(p, B, stream);
+}
+
+// Products of many tokens take tiles of 256, 128 or 64 of them: blocks take one
+// tile each a round, and the sum over the rounds decides.
+template <int OT>
+void launch_product(const Product& p, hipStream_t stream) {
+  if (p.M <= 64) {
+    launch_few_of<OT>(p, 1, stream);
+    return;
+  }
+  const auto time = [&](int tb, int round) {
+    const int64_t tiles = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.M + tb * 64 - 1) / (tb * 64));
+    return (tiles + 255) / 256 * round;
+  };
+  const int64_t t4 = time(4, 21), t2 = time(2, 15), t1 = time(1, 11);
+  if (t4 <= t2 && t4 <= t1) launch_tiled<OT, 4>(p, stream);
+  else if (t2 <= t1) launch_tiled<OT, 2>(p, stream);
+  else launch_tiled<OT, 1>(p, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -354,9 +601,9 @@ int nanospec_mx4_matmul(const uint8_t* xq, const uint8_t* xs, int32_t M, const u
   if (!elem_aligned(out, out_dtype)) return NS_EINVAL;
   (void)hipGetLastError();
   const Product p{xq, xs, wq, ws, nullptr, nullptr, M, N, N, pitch_of(d), out, ld_out, 1};
-  if (out_dtype == NS_FP32) launch_few_of<NS_FP32>(p, 1, stream);
-  else if (out_dtype == NS_BF16) launch_few_of<NS_BF16>(p, 1, stream);
-  else launch_few_of<NS_FP16>(p, 1, stream);
+  if (out_dtype == NS_FP32) launch_product<NS_FP32>(p, stream);
+  else if (out_dtype == NS_BF16) launch_product<NS_BF16>(p, stream);
+  else launch_product<NS_FP16>(p, stream);
   return ns_launch_status();
 }
 

@@ -267,7 +267,7 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
 // output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
 // token rows (TB operands), 8 TB accumulator tiles in registers.  The sum runs
 // in stages of one chunk a row (128 bytes of codes and 8 scales), two in LDS
-// (72 KB each with TB = 4), three with TB = 1, whose short stages end before a
+// (68 KB each with TB = 4), three with TB = 1, whose short stages end before a
 // load does, filled by direct global-to-LDS loads.  While one half of a stage (four blocks a
 // row) is multiplied, the next half is read into a second set of registers;
 // once a wave holds a stage's second half and the next stage has landed, one
@@ -284,26 +284,31 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
 // lanes covers 128 of them, without a detour through LDS.  Lane (i, g) takes
 // blocks 2 g and 2 g + 1 of a chunk, whose two scales are one 16-bit read.
 //
-// Place c of row r in LDS holds 16-byte block c ^ (r / 8 % 8) of channel rows and
-// c ^ (r % 8) of token rows, and eight channel rows stand 128 bytes from the next
-// eight, so that lanes i and i + 1 read from different halves of the 64 banks;
-// scales stand in the order in which the lanes read them, so that 16 lanes read
+// The eight 16-byte blocks of a row stand in LDS with the four even ones (those of
+// the first half) first; place c of row r holds the one that is c ^ (r / 8 % 8)
+// in that order in channel rows and c ^ (r % 8) in token rows, and eight channel
+// rows stand 128 bytes from the next eight, so that lanes i and i + 1 read from
+// different halves of the 64 banks; scales stand in the order in which the lanes read them, so that 16 lanes read
 // 16 consecutive ones: no bank is met twice.
 // ---------------------------------------------------------------------------
 constexpr int kTileN = 256;                        // channel rows of a block
 constexpr int kTileThreads = 512;
 constexpr int tile_stages(int tb) { return tb == 1 ? 3 : 2; }   // in LDS
+// The block of a chunk at place c of a row: 0 2 4 6 1 3 5 7.
+__device__ __forceinline__ int block_at(int c) { return (c & 3) * 2 + (c >> 2); }
 constexpr int kEightRows = 9 * kChunkBytes;        // eight channel rows in LDS and 128 bytes between them and the next
 
 template <int OT, int TB>
 __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int tiles_m, int tiles_n) {
   constexpr int TM = TB * 64;                      // token rows of a block
-  constexpr int XOFF = kTileN / 8 * kEightRows, SOFF = XOFF + TM * kChunkBytes, STAGE = SOFF + 2 * 256 * kChunkScales;
-  constexpr int LA = kTileN / 64, LB = TM / 64, LW = LA + LB + 2;   // loads of a wave and stage: 8 rows each, and scales
+  constexpr int XOFF = kTileN / 8 * kEightRows, STAGE = XOFF + TM * kChunkBytes;
+  constexpr int LA = kTileN / 64, LB = TM / 64;    // loads of a wave and stage: 8 rows each
   constexpr int STORES = TB * 4 * (OT == NS_FP32 ? 2 : 1);   // of a wave and whole tile
-  constexpr int R = tile_stages(TB), AHEAD = (R - 2) * LW;   // loads that may be out when a stage must be here
+  constexpr int R = tile_stages(TB), AHEAD = (R - 2) * (LA + LB);   // loads that may be out when a stage must be here
   static_assert(AHEAD + STORES < 64, "vmcnt range");
-  __shared__ __attribute__((aligned(16))) char lds[R * STAGE];
+  // scales of two stages together, R such pairs
+  constexpr int SOFF = R * STAGE, PAIR = (kTileN + TM) * 2 * kChunkScales;
+  __shared__ __attribute__((aligned(16))) char lds[SOFF + R * PAIR];
   const int total = tiles_m * tiles_n, per = (total + 7) / 8, slots = (int)(gridDim.x >> 3);
   const int first = (int)(blockIdx.x & 7) * per, end = first + per < total ? first + per : total;
   int tile = first + (int)(blockIdx.x >> 3);
@@ -319,9 +324,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   const uint32_t base = lds_offset(lds);
 
   // The stream of loads: stage `lk` of tile `lt` comes next.
-  int lt = tile, lk = 0;
-  u32x4 ra, rb, rsa, rsb;
+  int lt = tile, lk = 0, lp = 0;
+  u32x4 ra, rb, rs;
   int last_a, last_b;                              // rows past the end read the last one and are not stored
+  const int tw = (w & 3) % TB;                     // scales: waves 0 to 3 the channels', 4 to 7 the tokens', 64 rows each
   const auto aim = [&]() {
     int m0, n0;
     origin(lt, m0, n0);
@@ -329,28 +335,33 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
     last_b = p.M - 1 - m0;
     ra = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(kTileN * p.pitch));
     rb = buffer_of(p.x + (size_t)m0 * p.pitch, (uint32_t)(TM * p.pitch));
-    rsa = buffer_of(p.ws + (size_t)n0 * spitch, (uint32_t)(kTileN * spitch));
-    rsb = buffer_of(p.xs + (size_t)m0 * spitch, (uint32_t)(TM * spitch));
+    // the range ends with the rows: behind the last one's scales there may be nothing to read
+    rs = w < 4 ? buffer_of(p.ws + (size_t)n0 * spitch, (uint32_t)((last_a < kTileN ? last_a + 1 : kTileN) * spitch))
+               : buffer_of(p.xs + (size_t)m0 * spitch, (uint32_t)((last_b < TM ? last_b + 1 : TM) * spitch));
   };
-  // Load u of the next stage's LW, into buffer buf.
+  // Load u of the next stage's LA + LB, into buffer buf.
   const auto load = [&](int u, int buf) {
     int l = lane;                                  // opaque: the few values below are computed anew each
     asm volatile("" : "+v"(l));                    // time instead of being held in registers all along
-    if (u < LA + LB) {
-      const int v = u < LA ? u : u - LA, r = (v * 8 + w) * 8 + (l >> 3), last = u < LA ? last_a : last_b;
-      const int block = (l & 7) ^ (u < LA ? w : l >> 3);
-      load_to_lds(u < LA ? ra : rb, __umul24(r < last ? r : last, p.pitch) + block * 16, lk * kChunkBytes,
-                  base + buf * STAGE + (u < LA ? (v * 8 + w) * kEightRows : XOFF + (v * 8 + w) * 8 * kChunkBytes));
-    } else {
-      // scales of 32 rows; place t * 16 + i of a wave's 128 channel rows holds row 8 i + t
-      const int q = w * 32 + (l >> 1);
-      const int r = u == LA + LB ? (q & 128) + (q & 15) * 8 + (q >> 4 & 7) : q, last = u == LA + LB ? last_a : last_b;
-      load_word_to_lds(u == LA + LB ? rsa : rsb, __umul24(r < last ? r : last, spitch) + (l & 1) * 4, lk * kChunkScales,
-                       base + buf * STAGE + SOFF + (u == LA + LB ? 0 : 256 * kChunkScales) + w * 256);
-    }
+    const int v = u < LA ? u : u - LA, r = (v * 8 + w) * 8 + (l >> 3), last = u < LA ? last_a : last_b;
+    const int block = block_at((l & 7) ^ (u < LA ? w : l >> 3));
+    load_to_lds(u < LA ? ra : rb, __umul24(r < last ? r : last, p.pitch) + block * 16, lk * kChunkBytes,
+                base + buf * STAGE + (u < LA ? (v * 8 + w) * kEightRows : XOFF + (v * 8 + w) * 8 * kChunkBytes));
   };
-  // Behind a stage's loads: on to the next stage.
+  // Behind an even stage's loads the scales of that stage and the next, a row a
+  // lane (a row's 16 bytes at once: with 4 a lane for each stage the loads, 64
+  // lines of memory each, took 230 of 1240 us), then on to the next stage.
   const auto advance = [&]() {
+    if ((lk & 1) == 0) {
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      // place t * 16 + i of a wave's 128 channel rows holds row 8 i + t
+      const int q = (w & 3) * 64 + l, r = w < 4 ? (q & 128) + (q & 15) * 8 + (q >> 4 & 7) : tw * 64 + l;
+      const int last = w < 4 ? last_a : last_b;
+      load_to_lds(rs, __umul24(r < last ? r : last, spitch), lk * kChunkScales,
+                  base + SOFF + lp * PAIR + (w < 4 ? w : 4 + tw) * 1024);
+      lp = lp + 1 == R ? 0 : lp + 1;
+    }
     if (++lk == S) {                               // behind the last tile the stream reads that tile again,
       lk = 0;                                      // which spares every load a question
       if (lt + slots < end) {
@@ -372,24 +383,25 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   // operand t: channel rows wr * 128 + 8 i + t; operand u: token rows (wc * TB + u) * 16 + i
   const char* la = lds + (wr * 16 + i) * kEightRows;
   const char* lb = lds + XOFF + (wc * TB * 16 + i) * kChunkBytes;
-  const char* lsa = lds + SOFF + (wr * 128 + i) * kChunkScales + g * 2;
-  const char* lsb = lds + SOFF + (256 + wc * TB * 16 + i) * kChunkScales + g * 2;
-  const int place0 = ((2 * g) ^ (i & 7)) * 16, place1 = ((2 * g + 1) ^ (i & 7)) * 16;
-  const auto channel_scales = [&](int t, int buf) {
-    sa[t / 2][t & 1] = *(const uint16_t*)(lsa + buf * STAGE + t * 16 * kChunkScales);
+  const char* lsa = lds + SOFF + (wr * 128 + i) * 2 * kChunkScales + g * 2;
+  const char* lsb = lds + SOFF + (kTileN + wc * TB * 16 + i) * 2 * kChunkScales + g * 2;
+  const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
+  // from byte `at` of the pairs
+  const auto channel_scales = [&](int t, int at) {
+    sa[t / 2][t & 1] = *(const uint16_t*)(lsa + at + t * 32 * kChunkScales);
   };
-  const auto token_scales = [&](int buf) {
+  const auto token_scales = [&](int at) {
 #pragma unroll
-    for (int u = 0; u < TB; ++u) nb[u / 2][u & 1] = *(const uint16_t*)(lsb + buf * STAGE + u * 16 * kChunkScales);
+    for (int u = 0; u < TB; ++u) nb[u / 2][u & 1] = *(const uint16_t*)(lsb + at + u * 32 * kChunkScales);
   };
   aim();
 #pragma unroll
   for (int buf = 0; buf < R; ++buf) {
 #pragma unroll
-    for (int u = 0; u < LW; ++u) load(u, buf);
+    for (int u = 0; u < LA + LB; ++u) load(u, buf);
     advance();
   }
-  wait_loads<AHEAD + LW>();
+  wait_loads<AHEAD + LA + LB>();
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   token_scales(0);
@@ -405,18 +417,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   fe[0][1] = *(const i32x4*)(la + place0 + 7 * kChunkBytes);
   // Multiplies the half F in registers (fe, fb of F) and reads the next from
   // `at`.  With F = 1 the next stage's loads go out between the products, one
-  // for each operand, and its scales are read.
-  const auto step = [&](auto half, int at, int buf, int next) {
+  // for each operand, and the scales at `from` are read.
+  const auto step = [&](auto half, int at, int buf, int from) {
     constexpr int F = decltype(half)::value;
-    if (F == 1) token_scales(next);
+    if (F == 1) token_scales(from);
 #pragma unroll
     for (int u = 0; u < TB; ++u) fb[1 - F][u] = *(const i32x4*)(lb + at + u * 16 * kChunkBytes);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      if (F == 1) {
-        load(t, buf);
-        if (t + 8 < LW) load(t + 8, buf);
-      }
+      if (F == 1 && t < LA + LB) load(t, buf);
       const i32x4 a = t < 6 ? fa[t % 6] : fe[F][t & 1];
 #pragma unroll
       for (int u = 0; u < TB; ++u) {
@@ -430,13 +439,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
       if (t < 6) fa[t % 6] = *(const i32x4*)(la + at + t * kChunkBytes);
       if (t == 3 || t == 4) fe[1 - F][t - 3] = *(const i32x4*)(la + at + (t + 3) * kChunkBytes);
       if (F == 1 && t % 2 == 1) {
-        channel_scales(t - 1, next);
-        channel_scales(t, next);
+        channel_scales(t - 1, from);
+        channel_scales(t, from);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int b = 0;
+  int b = 0, pair = 0;
   bool stored = false;                             // the tile before was whole: STORES stores are behind the loads
   for (; tile < end; tile += slots) {
     for (int s = 0; s < S; ++s) {
@@ -447,7 +456,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       const int next = b + 1 == R ? 0 : b + 1;
-      step(std::integral_constant<int, 1>(), next * STAGE + place0, b, next);
+      const int s1 = s + 1 == S ? 0 : s + 1;       // the next stage's number
+      if ((s1 & 1) == 0) pair = pair + 1 == R ? 0 : pair + 1;
+      step(std::integral_constant<int, 1>(), next * STAGE + place0, b, pair * PAIR + (s1 & 1) * kChunkScales);
 #pragma unroll
       for (int u = 0; u < (TB + 1) / 2; ++u) sb[u] = nb[u];
       advance();

@@ -190,12 +190,20 @@ struct Product {
 };
 
 // 16 x 16 outputs over 128 elements.  Lane (i, g) holds 32 elements of row i of
-// each operand, one block, and a byte of sa and sb is that block's scale;
+// each operand, one block, and byte BYTE of sa and sb is that block's scale;
 // which elements a place holds is free as long as both operands agree.
-template <int BYTE_A, int BYTE_B>
+template <int BYTE>
 __device__ __forceinline__ f32x4 product128(i32x4 a, i32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
   const i32x8 x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BYTE_A, (int)sa, BYTE_B, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BYTE, (int)sa, BYTE, (int)sb);
+}
+
+// Two scales as an operand; its upper half is nobody's.
+__device__ __forceinline__ uint32_t two_scales(uint16_t v) {
+  asm volatile("" : "+v"(v));                      // taken here, not where the register last changed
+  u16x2 r;
+  r.x = v;
+  return __builtin_bit_cast(uint32_t, r);
 }
 
 // ---------------------------------------------------------------------------
@@ -237,8 +245,8 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
     for (int u = 0; u < NMT; ++u) {
       const i32x4 b0 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes), b1 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes + 16);
       const uint32_t sb = *(const uint16_t*)(xsr[u] + k * kChunkScales);
-      acc[u] = product128<0, 0>(b0, a0, acc[u], sb, sa);
-      acc[u] = product128<1, 1>(b1, a1, acc[u], sb, sa);
+      acc[u] = product128<0>(b0, a0, acc[u], sb, sa);
+      acc[u] = product128<1>(b1, a1, acc[u], sb, sa);
     }
   }
 #pragma unroll
@@ -327,6 +335,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   int lt = tile, lk = 0, lp = 0;
   u32x4 ra, rb, rs;
   int last_a, last_b;                              // rows past the end read the last one and are not stored
+  uint32_t at[LA + LB];                            // of the tile's loads
   const int tw = (w & 3) % TB;                     // scales: waves 0 to 3 the channels', 4 to 7 the tokens', 64 rows each
   const auto aim = [&]() {
     int m0, n0;
@@ -335,17 +344,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
     last_b = p.M - 1 - m0;
     ra = buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(kTileN * p.pitch));
     rb = buffer_of(p.x + (size_t)m0 * p.pitch, (uint32_t)(TM * p.pitch));
+#pragma unroll
+    for (int u = 0; u < LA + LB; ++u) {
+      const int v = u < LA ? u : u - LA, r = (v * 8 + w) * 8 + (lane >> 3), last = u < LA ? last_a : last_b;
+      at[u] = __umul24(r < last ? r : last, p.pitch) + block_at((lane & 7) ^ (u < LA ? w : lane >> 3)) * 16;
+    }
     // the range ends with the rows: behind the last one's scales there may be nothing to read
     rs = w < 4 ? buffer_of(p.ws + (size_t)n0 * spitch, (uint32_t)((last_a < kTileN ? last_a + 1 : kTileN) * spitch))
                : buffer_of(p.xs + (size_t)m0 * spitch, (uint32_t)((last_b < TM ? last_b + 1 : TM) * spitch));
   };
   // Load u of the next stage's LA + LB, into buffer buf.
   const auto load = [&](int u, int buf) {
-    int l = lane;                                  // opaque: the few values below are computed anew each
-    asm volatile("" : "+v"(l));                    // time instead of being held in registers all along
-    const int v = u < LA ? u : u - LA, r = (v * 8 + w) * 8 + (l >> 3), last = u < LA ? last_a : last_b;
-    const int block = block_at((l & 7) ^ (u < LA ? w : l >> 3));
-    load_to_lds(u < LA ? ra : rb, __umul24(r < last ? r : last, p.pitch) + block * 16, lk * kChunkBytes,
+    const int v = u < LA ? u : u - LA;
+    load_to_lds(u < LA ? ra : rb, at[u], lk * kChunkBytes,
                 base + buf * STAGE + (u < LA ? (v * 8 + w) * kEightRows : XOFF + (v * 8 + w) * 8 * kChunkBytes));
   };
   // Behind an even stage's loads the scales of that stage and the next, a row a
@@ -377,9 +388,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   // next half's replace 0 to 5 as they fall free, and 6 and 7 alternate, so
   // that no read is still to come behind the half's last products.
   i32x4 fa[6], fe[2][2], fb[2][TB];
-  // Scales of the stage that is multiplied, two operands' in a register; the next
-  // stage's replace the channels' as they fall free.
-  u16x2 sa[4], sb[(TB + 1) / 2], nb[(TB + 1) / 2];
+  // Scales of the stage that is multiplied; the next stage's replace the channels'
+  // as they fall free.
+  uint16_t sa[8], sb[TB], nb[TB];
   // operand t: channel rows wr * 128 + 8 i + t; operand u: token rows (wc * TB + u) * 16 + i
   const char* la = lds + (wr * 16 + i) * kEightRows;
   const char* lb = lds + XOFF + (wc * TB * 16 + i) * kChunkBytes;
@@ -388,11 +399,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
   // from byte `at` of the pairs
   const auto channel_scales = [&](int t, int at) {
-    sa[t / 2][t & 1] = *(const uint16_t*)(lsa + at + t * 32 * kChunkScales);
+    sa[t] = *(const uint16_t*)(lsa + at + t * 32 * kChunkScales);
   };
   const auto token_scales = [&](int at) {
 #pragma unroll
-    for (int u = 0; u < TB; ++u) nb[u / 2][u & 1] = *(const uint16_t*)(lsb + at + u * 32 * kChunkScales);
+    for (int u = 0; u < TB; ++u) nb[u] = *(const uint16_t*)(lsb + at + u * 32 * kChunkScales);
   };
   aim();
 #pragma unroll
@@ -406,7 +417,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
   __builtin_amdgcn_sched_barrier(0);
   token_scales(0);
 #pragma unroll
-  for (int u = 0; u < (TB + 1) / 2; ++u) sb[u] = nb[u];
+  for (int u = 0; u < TB; ++u) sb[u] = nb[u];
 #pragma unroll
   for (int t = 0; t < 8; ++t) channel_scales(t, 0);
 #pragma unroll
@@ -423,25 +434,22 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
     if (F == 1) token_scales(from);
 #pragma unroll
     for (int u = 0; u < TB; ++u) fb[1 - F][u] = *(const i32x4*)(lb + at + u * 16 * kChunkBytes);
+    uint32_t st[TB];
+#pragma unroll
+    for (int u = 0; u < TB; ++u) st[u] = two_scales(sb[u]);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       if (F == 1 && t < LA + LB) load(t, buf);
       const i32x4 a = t < 6 ? fa[t % 6] : fe[F][t & 1];
+      const uint32_t sc = two_scales(sa[t]);
 #pragma unroll
       for (int u = 0; u < TB; ++u) {
-        const uint32_t x = __builtin_bit_cast(uint32_t, sb[u / 2]), y = __builtin_bit_cast(uint32_t, sa[t / 2]);
-        if (u % 2 == 0 && t % 2 == 0) acc[t][u] = product128<F, F>(fb[F][u], a, acc[t][u], x, y);
-        else if (u % 2 == 0) acc[t][u] = product128<F, 2 + F>(fb[F][u], a, acc[t][u], x, y);
-        else if (t % 2 == 0) acc[t][u] = product128<2 + F, F>(fb[F][u], a, acc[t][u], x, y);
-        else acc[t][u] = product128<2 + F, 2 + F>(fb[F][u], a, acc[t][u], x, y);
+        acc[t][u] = product128<F>(fb[F][u], a, acc[t][u], st[u], sc);
         asm volatile("" : "+v"(acc[t][u]));        // the product stays here, between the loads
       }
       if (t < 6) fa[t % 6] = *(const i32x4*)(la + at + t * kChunkBytes);
       if (t == 3 || t == 4) fe[1 - F][t - 3] = *(const i32x4*)(la + at + (t + 3) * kChunkBytes);
-      if (F == 1 && t % 2 == 1) {
-        channel_scales(t - 1, from);
-        channel_scales(t, from);
-      }
+      if (F == 1) channel_scales(t, from);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -460,7 +468,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
       if ((s1 & 1) == 0) pair = pair + 1 == R ? 0 : pair + 1;
       step(std::integral_constant<int, 1>(), next * STAGE + place0, b, pair * PAIR + (s1 & 1) * kChunkScales);
 #pragma unroll
-      for (int u = 0; u < (TB + 1) / 2; ++u) sb[u] = nb[u];
+      for (int u = 0; u < TB; ++u) sb[u] = nb[u];
       advance();
       b = next;
     }

@@ -269,6 +269,212 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
 }
 
 // ---------------------------------------------------------------------------
+// The product for up to 64 token rows: bound by the bytes of the channel rows,
+// each read once.
+//
+// One block of eight waves a CU takes an even share of the channel units of ROWS
+// rows and runs through it in passes of eight units, one a wave (RT operands of 16
+// rows), in stages of one chunk a row.  A ring of stages in LDS is filled by direct
+// global-to-LDS loads, R - 1 stages ahead, across the ends of passes; channel
+// rows and their scales are private to their wave, token rows shared by the
+// block, so one barrier a stage orders the ring; the tokens' scales are in LDS
+// from the start.  Waits count the loads that may still be out; outputs leave by
+// buffer stores, which out-of-range lanes take part in without effect, so the
+// stores behind a pass are as many for every pass and the waits can allow for
+// them.
+//
+// Block b begins every row at chunk 5 b mod S and goes round: blocks that walked
+// along their rows in step would read addresses alike in their low bits, a few
+// memory channels' worth.
+//
+// The token rows are operand A and the channel rows operand B, so 16 lanes
+// hold 16 consecutive outputs of a token.  Blocks of a row stand in LDS as in
+// the tiles below: place c of row r holds block c ^ (r % 8) in that order.
+//
+// With IDS the channel rows are those that ids names (n_dev of them), the
+// block's share of ids waiting in LDS, and blockIdx.y is the sequence.
+// ---------------------------------------------------------------------------
+constexpr int kStreamWaves = 8;
+constexpr int kStreamIds = 4096;                   // ids of a block, at most
+constexpr int kStreamIdsD = 8192;                  // d with ids, at most: the tokens' scales and the ids share what LDS is left
+
+// The 16-byte block of a chunk at place c of a row: 0 2 4 6 1 3 5 7.
+__device__ __forceinline__ int block_at(int c) { return (c & 3) * 2 + (c >> 2); }
+
+template <int OT, int NMT, int ROWS, int R, bool IDS>
+__global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product p) {
+  constexpr int RT = ROWS > 16 ? ROWS / 16 : 1, PROWS = kStreamWaves * ROWS, LR = ROWS / 8;
+  constexpr int XOFF = PROWS * kChunkBytes, SOFF = XOFF + NMT * 16 * kChunkBytes;
+  constexpr int STAGE = SOFF + kStreamWaves * 256;   // channel rows, token rows, channel scales
+  constexpr int XL = NMT % 4 == 0 ? NMT / 4 : NMT, LW = LR + 1 + XL;   // loads of a wave and stage
+  // stores behind a pass that the waits allow for (vmcnt counts to 63)
+  constexpr int STORES = RT * NMT * 4 < 63 - (R - 2) * LW ? RT * NMT * 4 : 63 - (R - 2) * LW;
+  static_assert((R - 2) * LW + STORES < 64, "vmcnt range");
+  constexpr int XS = NMT * 16 * ((IDS ? kStreamIdsD : NS_MAX_D) / 32 + 8);   // the tokens' scales, a row's 8 bytes from the next
+  __shared__ __attribute__((aligned(16))) char lds[R * STAGE + XS];
+  __shared__ int s_id[IDS ? kStreamIds : 1];
+  int live = p.N;
+  if (IDS) {
+    const size_t seq = blockIdx.y;
+    if (p.n_dev) live = p.n_dev[seq] < 0 ? 0 : (p.n_dev[seq] < p.N ? p.n_dev[seq] : p.N);
+    p.x += seq * p.M * p.pitch;
+    p.xs += seq * p.M * (p.pitch / 16);
+    if (p.ids) p.ids += seq * p.N;
+    p.out = (char*)p.out + seq * p.M * (size_t)p.sm * (OT == NS_FP32 ? 4 : 2);
+  }
+  const int units = (live + ROWS - 1) / ROWS, per_block = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
+  const int passes = (u1 - u0 + kStreamWaves - 1) / kStreamWaves;
+  if (passes <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int S = p.pitch / kChunkBytes, spitch = S * kChunkScales;
+  const uint32_t base = lds_offset(lds);
+  const int n0 = u0 * ROWS;                            // the block's first channel row
+  const int last = (u1 * ROWS < live ? u1 * ROWS : live) - 1 - n0;
+  const u32x4 rw = IDS ? buffer_of(p.w, (uint32_t)p.V * p.pitch)
+                       : buffer_of(p.w + (size_t)n0 * p.pitch, (uint32_t)(last + 1) * p.pitch);
+  const u32x4 rs = IDS ? buffer_of(p.ws, (uint32_t)p.V * spitch)
+                       : buffer_of(p.ws + (size_t)n0 * spitch, (uint32_t)(last + 1) * spitch);
+  const u32x4 rx = buffer_of(p.x, (uint32_t)(p.M * p.pitch));
+  char* xs = lds + R * STAGE;
+  for (int q = tid; q < NMT * 16 * S; q += kStreamWaves * NS_WAVE) {   // eight scales each; rows past the end are the last one's
+    const int r = q / S, c = q - r * S;
+    *(u32x2*)(xs + r * (spitch + 8) + c * 8) = *(const u32x2*)(p.xs + (r < p.M ? r : p.M - 1) * spitch + c * 8);
+  }
+  if (IDS) {                                         // a hole reads row 0; nobody reads its output
+    for (int r = tid; r <= last; r += kStreamWaves * NS_WAVE) {
+      const int id = p.ids ? p.ids[n0 + r] : n0 + r;
+      s_id[r] = id < 0 || id >= p.V ? 0 : id;
+    }
+  }
+  __syncthreads();
+  // token rows past the end read the last one and are not stored
+  uint32_t xo[XL];
+  if (NMT % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < XL; ++v) {
+      const int r = (v * 8 + w) * 8 + (lane >> 3);
+      xo[v] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + block_at((lane & 7) ^ (lane >> 3)) * 16);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NMT; ++v) {                  // two rows a load, a word a lane
+      const int r = v * 16 + w * 2 + (lane >> 5), q = lane & 31;
+      xo[v] = (uint32_t)((r < p.M ? r : p.M - 1) * p.pitch + block_at((q >> 2) ^ (r & 7)) * 16 + (q & 3) * 4);
+    }
+  }
+  // The stream of loads: the lk-th stage of pass lp comes next, chunk ks of the rows, into place lb.
+  const int start = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 5u) % S);
+  int lp = 0, lk = 0, lb = 0, ks = start;
+  uint32_t wo[LR], so;                           // of the pass
+  const auto aim = [&]() {
+    const int r0 = (lp * kStreamWaves + w) * ROWS;
+    const auto row = [&](int r) {
+      r = r < last ? r : last;
+      return (uint32_t)(IDS ? s_id[r] : r);
+    };
+#pragma unroll
+    for (int v = 0; v < LR; ++v)
+      wo[v] = __umul24(row(r0 + v * 8 + (lane >> 3)), p.pitch) + block_at((lane & 7) ^ (lane >> 3)) * 16;
+    so = __umul24(row(r0 + (lane >> 1 & (ROWS - 1))), spitch) + (lane & 1) * 4;
+  };
+  const auto issue = [&]() {
+    const uint32_t to = base + lb * STAGE;
+#pragma unroll
+    for (int v = 0; v < LR; ++v) load_to_lds_once(rw, wo[v], ks * kChunkBytes, to + (w * LR + v) * 1024);
+    load_word_to_lds(rs, so, ks * kChunkScales, to + SOFF + w * 256);
+    if (NMT % 4 == 0) {
+#pragma unroll
+      for (int v = 0; v < XL; ++v) load_to_lds(rx, xo[v], ks * kChunkBytes, to + XOFF + (v * 8 + w) * 1024);
+    } else {
+#pragma unroll
+      for (int v = 0; v < NMT; ++v) load_word_to_lds(rx, xo[v], ks * kChunkBytes, to + XOFF + (v * 8 + w) * 256);
+    }
+    lb = lb + 1 == R ? 0 : lb + 1;
+    ks = ks + 1 == S ? 0 : ks + 1;
+    if (++lk == S) {                                 // behind the last pass the stream reads that pass again,
+      lk = 0;                                        // which spares every load a question
+      if (lp + 1 < passes) {
+        ++lp;
+        aim();
+      }
+    }
+  };
+  aim();
+  const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(p.out, 0, 0x7FFFFFFF, 0x00027000);
+  constexpr int ESZ = OT == NS_FP32 ? 4 : 2;
+  f32x4 acc[RT][NMT] = {};
+#pragma unroll
+  for (int v = 0; v < R - 1; ++v) issue();
+  const int place0 = (g ^ (i & 7)) * 16, place1 = ((4 + g) ^ (i & 7)) * 16;
+  const int ir = ROWS < 16 ? i & (ROWS - 1) : i;     // with 8 rows the operand's upper half repeats the lower
+  const char* lw = lds + (w * ROWS + ir) * kChunkBytes;
+  const char* lx = lds + XOFF + i * kChunkBytes;
+  const char* ls = lds + SOFF + w * 256 + ir * kChunkScales + g * 2;
+  const char* lxs = xs + i * (spitch + 8) + g * 2;
+  int b = 0, since = R, kr = start;                  // stages since the last stores; the chunk that is multiplied
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int s = 0; s < S; ++s) {
+      // this stage's loads are done when at most those of the R - 2 stages
+      // behind it, and the stores between them, are out
+      if (since < R - 1) wait_loads<(R - 2) * LW + STORES>();
+      else wait_loads<(R - 2) * LW>();
+      ++since;
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      issue();                                       // into the place of the stage before, which all have read
+      const char* at = lw + b * STAGE;
+      const char* xt = lx + b * STAGE;
+      i32x4 f[RT][2];
+      uint32_t sw[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        sw[t] = *(const uint16_t*)(ls + b * STAGE + t * 16 * kChunkScales);
+        f[t][0] = *(const i32x4*)(at + t * 16 * kChunkBytes + place0);
+        f[t][1] = *(const i32x4*)(at + t * 16 * kChunkBytes + place1);
+      }
+#pragma unroll
+      for (int u = 0; u < NMT; ++u) {
+        const uint32_t sx = *(const uint16_t*)(lxs + u * 16 * (spitch + 8) + kr * kChunkScales);
+        const i32x4 x0 = *(const i32x4*)(xt + u * 16 * kChunkBytes + place0);
+        const i32x4 x1 = *(const i32x4*)(xt + u * 16 * kChunkBytes + place1);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          acc[t][u] = product128<0>(x0, f[t][0], acc[t][u], sx, sw[t]);
+          acc[t][u] = product128<1>(x1, f[t][1], acc[t][u], sx, sw[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int u = 0; u < NMT; ++u) asm volatile("" : "+v"(acc[t][u]));   // the products stay in front of the wait
+      __builtin_amdgcn_sched_barrier(0);             // no read moves behind the wait
+      __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): this wave has read the stage
+      b = b + 1 == R ? 0 : b + 1;
+      kr = kr + 1 == S ? 0 : kr + 1;
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int j = (pass * kStreamWaves + w) * ROWS + t * 16 + i;
+#pragma unroll
+      for (int u = 0; u < NMT; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int m = u * 16 + g * 4 + r;
+          const float v = acc[t][u][r];
+          const uint32_t to =
+              m < p.M && j <= last && (ROWS >= 16 || i < ROWS) ? (uint32_t)(((size_t)m * (size_t)p.sm + (size_t)(n0 + j) * (size_t)p.sn) * ESZ) : 0x80000000u;
+          if (OT == NS_FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, to, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)narrow2<OT>(v, 0.f), ro, to, 0, 0);
+          acc[t][u][r] = 0.f;
+        }
+    }
+    since = 0;
+  }
+  wait_loads<0>();                                   // the stream's last loads end before their LDS is given back
+}
+
+// ---------------------------------------------------------------------------
 // The product for many token rows: compute-bound, tiles in LDS.
 //
 // A block of eight waves owns 256 channel rows and TB * 64 token rows of the
@@ -302,8 +508,6 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
 constexpr int kTileN = 256;                        // channel rows of a block
 constexpr int kTileThreads = 512;
 constexpr int tile_stages(int tb) { return tb == 1 ? 3 : 2; }   // in LDS
-// The block of a chunk at place c of a row: 0 2 4 6 1 3 5 7.
-__device__ __forceinline__ int block_at(int c) { return (c & 3) * 2 + (c >> 2); }
 constexpr int kEightRows = 9 * kChunkBytes;        // eight channel rows in LDS and 128 bytes between them and the next
 
 template <int OT, int TB>
@@ -520,12 +724,37 @@ void launch_few_of(const Product& p, int B, hipStream_t stream) {
   else launch_few<OT, 4>(p, B, stream);
 }
 
-// Products of many tokens take tiles of 256, 128 or 64 of them: blocks take one
-// tile each a round, and the sum over the rounds decides.
+template <int OT, int NMT, int ROWS, int R>
+void launch_stream(const Product& p, hipStream_t stream) {
+  const int units = (p.N + ROWS - 1) / ROWS, per = (units + 255) / 256;
+  hipLaunchKernelGGL((k_mx4_stream<OT, NMT, ROWS, R, false>), dim3((unsigned)((units + per - 1) / per)),
+                     dim3(kStreamWaves * NS_WAVE), 0, stream, p);
+}
+
+// Up to 64 tokens: up to 4096 channels the kernel for few rows, up to 16384 the
+// stream of eight-row units, then taller units.  Products of more tokens take
+// tiles of 256, 128 or 64 of them: blocks take one tile each a round, and the sum
+// over the rounds decides.
 template <int OT>
 void launch_product(const Product& p, hipStream_t stream) {
-  if (p.M <= 64) {
+  const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
+                        (OT == NS_FP32 ? 4 : 2);
+  if (p.M <= 64 && (p.N <= 4096 || span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
     launch_few_of<OT>(p, 1, stream);
+    return;
+  }
+  if (p.M <= 64) {
+    if (p.N <= 16384) {
+      if (p.M <= 16) launch_stream<OT, 1, 8, 7>(p, stream);
+      else if (p.M <= 32) launch_stream<OT, 2, 8, 7>(p, stream);
+      else if (p.M <= 48) launch_stream<OT, 3, 8, 7>(p, stream);
+      else launch_stream<OT, 4, 8, 6>(p, stream);
+    } else {
+      if (p.M <= 16) launch_stream<OT, 1, 16, 7>(p, stream);
+      else if (p.M <= 32) launch_stream<OT, 2, 16, 6>(p, stream);
+      else if (p.M <= 48) launch_stream<OT, 3, 32, 3>(p, stream);
+      else launch_stream<OT, 4, 32, 3>(p, stream);
+    }
     return;
   }
   const auto time = [&](int tb, int round) {
@@ -536,6 +765,38 @@ void launch_product(const Product& p, hipStream_t stream) {
   if (t4 <= t2 && t4 <= t1) launch_tiled<OT, 4>(p, stream);
   else if (t2 <= t1) launch_tiled<OT, 2>(p, stream);
   else launch_tiled<OT, 1>(p, stream);
+}
+
+template <int NMT, int ROWS, int R>
+void launch_head_stream(const Product& p, int B, hipStream_t stream) {
+  // one block a CU over all sequences, none with more ids than it holds
+  const int units = (p.N + ROWS - 1) / ROWS, least = (units * ROWS + kStreamIds - 1) / kStreamIds;
+  int gx = B < 256 ? 256 / B : 1;
+  gx = gx > units ? units : (gx < least ? least : gx);
+  hipLaunchKernelGGL((k_mx4_stream<NS_FP32, NMT, ROWS, R, true>), dim3((unsigned)gx, (unsigned)B),
+                     dim3(kStreamWaves * NS_WAVE), 0, stream, p);
+}
+
+// The head's logits, B sequences.  The stream's 32-bit row addresses reach 4 GB.
+bool few_rows(int B, int n_max, int V, int d) {
+  return (int64_t)B * n_max < 8192 || d > kStreamIdsD || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
+}
+
+void launch_head(const Product& p, int B, int d, hipStream_t stream) {
+  const int64_t rows = (int64_t)B * p.N;
+  if (few_rows(B, p.N, p.V, d)) {
+    launch_few_of<NS_FP32>(p, B, stream);
+  } else if (rows <= 65536) {
+    if (p.M <= 16) launch_head_stream<1, 8, 7>(p, B, stream);
+    else if (p.M <= 32) launch_head_stream<2, 8, 7>(p, B, stream);
+    else if (p.M <= 48) launch_head_stream<3, 8, 7>(p, B, stream);
+    else launch_head_stream<4, 8, 6>(p, B, stream);
+  } else {
+    if (p.M <= 16) launch_head_stream<1, 16, 6>(p, B, stream);
+    else if (p.M <= 32) launch_head_stream<2, 16, 5>(p, B, stream);
+    else if (p.M <= 48) launch_head_stream<3, 32, 3>(p, B, stream);
+    else launch_head_stream<4, 32, 3>(p, B, stream);
+  }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -648,7 +909,7 @@ int nanospec_mx4_logits_topk(const uint8_t* wq, const uint8_t* wscale, const int
   int rc = mx4_rows(h, d, B * M, d, dtype, hq, hs, stream);
   if (rc != NS_OK) return rc;
   const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
-  launch_few_of<NS_FP32>(p, B, stream);
+  launch_head(p, B, d, stream);
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;
   const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};

@@ -10,8 +10,8 @@
 //     g = w (-r A [r A <= clip(r) A] + beta (1 - exp(delta))),
 //     dz_j = g_loss t (g ([j = a] - p_j) + w c_H p_j (logp_j + H)).
 // With y_j = log2(e) z'_j - E, S = sum 2^y_j and W = sum 2^y_j y_j the second
-// line is 2^y_j (A + B y_j) off the token.  What stands once a row (logp_a and
-// all that follows from it) is computed in float64: a ratio is as exact as S.
+// line is 2^y_j (A + B y_j) off the token.  logp_a and its distances from old and
+// ref are taken in float64, so that a ratio is as exact as S.
 #include "common.hpp"
 #include "logits.hpp"
 
@@ -35,9 +35,13 @@ struct Args {
   void* dz;                    // or NULL
   int64_t ld_d;
   double* row_loss;            // [L]
+  int S;                       // parts of a row, a power of two
+  Stat* stat;                  // [L][S], where S > 1
+  float* ztok;                 // [L] the tokens' logits, likewise
 };
 
 constexpr double kUnseen = -104.0;       // a log-probability below this is that of a probability 0 in float32
+constexpr double kLn2d = 0.69314718055994530942;
 
 // What a row's gradient needs: 2^y (A + B y), and G more at the token.
 struct Slope {
@@ -58,50 +62,86 @@ __device__ __forceinline__ void put_nothing(const Args& a, size_t row) {
   a.row_loss[row] = 0.0;
 }
 
+// exp(x) - 1 - x.  Near 0 by its series, whose terms past the tenth are below a
+// step of the first.
+__device__ __forceinline__ float exp_past_line(float x) {
+  if (x > 80.f) return expf(x);                            // what is left out is far below its last digit
+  if (fabsf(x) > 0.5f) return expf(x) - 1.f - x;
+  float r = 1.f / 3628800;
+  r = fmaf(r, x, 1.f / 362880);
+  r = fmaf(r, x, 1.f / 40320);
+  r = fmaf(r, x, 1.f / 5040);
+  r = fmaf(r, x, 1.f / 720);
+  r = fmaf(r, x, 1.f / 120);
+  r = fmaf(r, x, 1.f / 24);
+  r = fmaf(r, x, 1.f / 6);
+  r = fmaf(r, x, 0.5f);
+  return r * x * x;
+}
+
+// What a row needs beside its logits, asked for before they are read.
+struct Given {
+  float old, ref, advantage, w, g_loss;
+  __device__ __forceinline__ Given(const Args& a, size_t row, float weight)
+      : old(a.old[row]), ref(a.ref ? a.ref[row] : 0.f), advantage(a.advantage[row]), w(weight),
+        g_loss(a.g_loss ? *a.g_loss : 1.f) {}
+};
+
 // A row's outputs and slope from its statistics and its token's logit.
-__device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s, float ztok, float w, bool writes) {
-  const double kLn2d = 0.69314718055994530942;
+__device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s, float ztok, const Given& v, bool writes,
+                                        double* row_loss = nullptr) {
   const bool bad = !(s.S < INFINITY) || s.top == INFINITY, none = s.S == 0.f;
+  const float nan = __uint_as_float(0x7FC00000u);
   Slope r{s.ref, s.E, 0.f, 0.f, 0.f};
-  double logp = 0.0, kl = 0.0, loss = 0.0;
-  float H = 0.f;
+  float logp = nan, kl = 0.f, H = nan;
+  double loss = 0.0;
   if (bad) {
-    logp = kl = loss = __longlong_as_double(0x7FF8000000000000ll);
-    H = r.A = r.B = r.G = (float)logp;
+    r.A = r.B = r.G = kl = nan;
+    loss = nan;
+  } else if (none) {
+    logp = -INFINITY;
+    H = 0.f;
   } else {
-    // c (1 + eps) is what c stands for; the sum's large terms have c z close to E
-    const double l = none ? 0.0 : log2((double)s.S) + (double)a.eps * s.E;
+    // log2 of S by its mantissa's, in [1/sqrt 2, sqrt 2], which is near 0 where S is
+    // near a power of two.  c (1 + eps) is what c stands for; the sum's large terms
+    // have c z close to E.
+    int e;
+    float m = frexpf(s.S, &e);
+    if (m < 0.70710678f) m *= 2.f, --e;
+    const double l0 = (double)e + (double)log2f(m), l = l0 + (double)a.eps * s.E;
     const double y = ((double)ztok - s.ref) * ((double)a.c * (1.0 + (double)a.eps)) - s.E;
-    logp = none ? -INFINITY : kLn2d * (y - l);
-    H = none ? 0.f : fmaxf((float)(kLn2d * (log2((double)s.S) - (double)s.W / s.S)), 0.f);
-    if (logp > kUnseen) {
-      const double adv = a.advantage[row], ratio = exp(logp - (double)a.old[row]);
-      const double lo = 1.0 - (double)a.eps_low, hi = 1.0 + (double)a.eps_high;
-      const double held = ratio < lo ? lo : (ratio > hi ? hi : ratio), gain = ratio * adv, most = held * adv;
+    const double lp = kLn2d * (y - l);
+    logp = (float)lp;
+    H = fmaxf((float)(kLn2d * (l0 - (double)(s.W / s.S))), 0.f);
+    if (lp > kUnseen) {
+      const float ratio = expf((float)(lp - (double)v.old));
+      const float lo = 1.f - a.eps_low, hi = 1.f + a.eps_high;
+      const float held = ratio < lo ? lo : (ratio > hi ? hi : ratio), gain = ratio * v.advantage, most = held * v.advantage;
       const bool clipped = gain > most;                    // not where one of them is NaN
-      double g = clipped ? 0.0 : -gain;
+      float g = clipped ? 0.f : -gain;
       loss = clipped ? -most : -gain;
       if (a.ref) {
-        const double delta = (double)a.ref[row] - logp, e = expm1(delta);
-        kl = e - delta;
+        const float delta = (float)((double)v.ref - lp);
+        kl = exp_past_line(delta);
         if (a.beta != 0.f) {
           loss += (double)a.beta * kl;
-          g -= (double)a.beta * e;
+          g -= a.beta * (kl + delta);
         }
       }
-      loss = (double)w * (loss - (double)a.c_ent * H);
-      const double up = (a.g_loss ? (double)*a.g_loss : 1.0) * (double)a.t, over = up / s.S * (double)w, ent = a.c_ent;
-      r.G = (float)(up * (double)w * g);
-      r.A = (float)(over * (ent * ((double)H - kLn2d * l) - g));
-      r.B = (float)(over * ent * kLn2d);
+      loss = (double)v.w * (loss - (double)a.c_ent * H);
+      const float up = v.g_loss * a.t, over = up * v.w / s.S;
+      r.G = up * v.w * g;
+      r.A = over * (a.c_ent * (H - (float)(kLn2d * l)) - g);
+      r.B = over * a.c_ent * (float)kLn2d;
     }
   }
   if (writes) {
-    a.logprob[row] = (float)logp;
-    if (a.kl) a.kl[row] = (float)kl;
+    a.logprob[row] = logp;
+    if (a.kl) a.kl[row] = kl;
     if (a.entropy) a.entropy[row] = H;
-    a.row_loss[row] = loss;
+    if (!row_loss) a.row_loss[row] = loss;
   }
+  if (row_loss) *row_loss = loss;
   return r;
 }
 
@@ -138,14 +178,13 @@ __device__ __forceinline__ Stat stat_of_lanes(float v, float c) {
   return s;
 }
 
-constexpr int kRowThreads = 512;
-
-// A block takes a row: its statistics, its outputs, and, where there is a
-// gradient, the row again.
-template <int ET>
-__global__ __launch_bounds__(kRowThreads) void k_policy_row(Args a) {
-  constexpr int EPV = per_vec(ET), STEP = NS_WAVE * kUnroll, NW = kRowThreads / NS_WAVE;
+// A block of T threads takes a row and holds it in registers (U vectors a thread;
+// what is longer is read again) between its statistics and its gradient.
+template <int ET, int T, int U>
+__global__ __launch_bounds__(T) void k_policy_row(Args a) {
+  constexpr int EPV = per_vec(ET), NW = T / NS_WAVE, HELD = T * U;
   __shared__ Stat sh[NW];
+  __shared__ Slope sh_slope;
   const size_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1), wv = tid / NS_WAVE;
   const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
@@ -155,75 +194,323 @@ __global__ __launch_bounds__(kRowThreads) void k_policy_row(Args a) {
   float w;
   if (!taken(a, row, tok, w)) {                            // uniform
     if (tid == 0) put_nothing(a, row);
-    if (a.dz) {
-      for (int q = tid; q < nvec; q += kRowThreads) *(u32x4_any*)(drow + (size_t)q * 16) = u32x4{0, 0, 0, 0};
-      if (tail < a.V) put_elem<ET>(drow, tail, 0.f);
-    }
+    for (int q = tid; q < nvec; q += T) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, (u32x4_any*)(drow + (size_t)q * 16));
+    if (tail < a.V) put_elem<ET>(drow, tail, 0.f);
     return;
   }
-  const float ztok = one_elem<ET>(zrow, tok);
-  Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
-  for (int base = wv * STEP; base < nvec; base += NW * STEP) {
-    u32x4 x[kUnroll];
+  const auto load = [&](int q) {
+    return __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)(q < nvec ? q : 0) * 16));
+  };
+  u32x4 x[U];
+  if (nvec > 0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int q = base + u * NS_WAVE + lane;
-      x[u] = *(const u32x4_any*)(zrow + (size_t)(q < nvec ? q : nvec - 1) * 16);
-      if (q >= nvec) x[u] = minus_inf<ET>();
-    }
+    for (int u = 0; u < U; ++u) x[u] = load(u * T + tid);
+  }
+  const Given given(a, row, w);
+  const float ztok = one_elem<ET>(zrow, tok);
+  float ztail = -INFINITY;
+  if (tail < a.V) ztail = one_elem<ET>(zrow, tail);
+  NS_ISSUE_FENCE();
+  Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
+  const auto add = [&](const u32x4(&v)[kUnroll], int q) {  // q: the lane's first vector
+    u32x4 y[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) y[u] = q + u * T < nvec ? v[u] : minus_inf<ET>();
     float mx[kUnroll], lane_max;
-    add_batch<ET>(x, a.c, st, mx, lane_max);
+    add_batch<ET>(y, a.c, st, mx, lane_max);
+  };
+#pragma unroll
+  for (int u = 0; u < U; u += kUnroll) {
+    if (u * T >= nvec) break;                              // uniform
+    const u32x4 v[kUnroll] = {x[u], x[u + 1], x[u + 2], x[u + 3]};
+    add(v, u * T + tid);
+  }
+  for (int q = HELD + tid; q - tid < nvec; q += T * kUnroll) {
+    u32x4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = *(const u32x4_any*)(zrow + (size_t)(q + u * T < nvec ? q + u * T : 0) * 16);
+    NS_ISSUE_FENCE();
+    add(v, q);
   }
   st.S = ns::wave_sum_f32(st.S);
   st.W = ns::wave_sum_f32(st.W);
-  if (wv == 0 && nvec * EPV < a.V)
-    st = join(st, stat_of_lanes(tail < a.V ? one_elem<ET>(zrow, tail) : -INFINITY, a.c), a.c);
-  if (lane == 0) sh[wv] = st;
-  __syncthreads();
-  st = sh[0];
-#pragma unroll
-  for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
-  const Slope s = finish(a, row, st, ztok, w, tid == 0);
-  if (!a.dz) return;
-  for (int q = tid; q < nvec; q += kRowThreads) {
-    float v[EPV];
-    widen<ET>(*(const u32x4_any*)(zrow + (size_t)q * 16), v);
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) v[e] = slope_at(s, a.c, v[e]) + (q * EPV + e == tok ? s.G : 0.f);
-    *(u32x4_any*)(drow + (size_t)q * 16) = narrow<ET>(v);
+  if (wv == 0 && nvec * EPV < a.V) st = join(st, stat_of_lanes(ztail, a.c), a.c);
+  if (NW > 1) {
+    if (lane == 0) sh[wv] = st;
+    __syncthreads();
   }
-  if (tail < a.V) put_elem<ET>(drow, tail, slope_at(s, a.c, one_elem<ET>(zrow, tail)) + (tail == tok ? s.G : 0.f));
+  Slope s;
+  if (wv == 0) {
+#pragma unroll
+    for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
+    s = finish(a, row, st, ztok, given, tid == 0);
+    if (NW > 1 && tid == 0) sh_slope = s;
+  }
+  if (NW > 1) {
+    __syncthreads();
+    s = sh_slope;
+  }
+  const auto put = [&](u32x4 z, int q) {
+    float v[EPV];
+    widen<ET>(z, v);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) v[e] = slope_at(s, a.c, v[e]);
+    __builtin_nontemporal_store(narrow<ET>(v), (u32x4_any*)(drow + (size_t)q * 16));
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u * T + tid < nvec) put(x[u], u * T + tid);
+  for (int q = HELD + tid; q < nvec; q += T) put(*(const u32x4_any*)(zrow + (size_t)q * 16), q);
+  if (tail < a.V) put_elem<ET>(drow, tail, slope_at(s, a.c, ztail));
+  // the thread that wrote the token's element writes it once more
+  const int owner = tok < nvec * EPV ? tok / EPV % T : tok - nvec * EPV;
+  if (tid == owner) put_elem<ET>(drow, tok, slope_at(s, a.c, ztok) + s.G);
 }
 
-// The sum of the rows' losses, in the same order each time.
-constexpr int kTotalThreads = 1024;
+// Parts of rows: a wave streams part `part` of S of one row.  With S = 1 it ends
+// the row, else it leaves the part's statistics.
+constexpr int kPartWaves = 4;
 
-__global__ __launch_bounds__(kTotalThreads) void k_policy_total(const double* __restrict__ row_loss, int L,
-                                                                float* __restrict__ loss) {
-  __shared__ double sh[kTotalThreads / NS_WAVE];
+template <int ET>
+__global__ __launch_bounds__(kPartWaves* NS_WAVE) void k_policy_parts(Args a) {
+  constexpr int EPV = per_vec(ET), STEP = NS_WAVE * kUnroll;
+  const int lane = threadIdx.x & (NS_WAVE - 1);
+  const int64_t item = (int64_t)blockIdx.x * kPartWaves + threadIdx.x / NS_WAVE;
+  const size_t row = (size_t)(item / a.S);
+  const int part = (int)(item % a.S);
+  if (row >= (size_t)a.L) return;                          // wave-uniform; no block barrier below
+  int tok;
+  float w;
+  if (!taken(a, row, tok, w)) {
+    if (a.S == 1 && lane == 0) put_nothing(a, row);
+    return;
+  }
+  const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
+  const int nvec = a.V / EPV;
+  const int q0 = (int)((int64_t)nvec * part / a.S), q1 = (int)((int64_t)nvec * (part + 1) / a.S);
+  Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
+  // loads under no condition, so that a batch stays in flight behind the one that is summed
+  const auto load = [&](int base, u32x4(&x)[kUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int q = base + u * NS_WAVE + lane;
+      const u32x4_any* from = (const u32x4_any*)(zrow + (size_t)(q < q1 ? q : q1 - 1) * 16);
+      x[u] = a.dz ? *from : __builtin_nontemporal_load(from);   // the gradient reads them again
+    }
+  };
+  u32x4 x0[kUnroll], x1[kUnroll];
+  if (q0 < q1) load(q0, x0);
+#pragma unroll 1
+  for (int base = q0; base < q1; base += STEP) {
+    load(base + STEP, x1);
+    NS_ISSUE_FENCE();
+    if (base + STEP > q1) {                                // uniform
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (base + u * NS_WAVE + lane >= q1) x0[u] = minus_inf<ET>();
+    }
+    float mx[kUnroll], lane_max;
+    add_batch<ET>(x0, a.c, st, mx, lane_max);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x0[u] = x1[u];
+  }
+  st.S = ns::wave_sum_f32(st.S);
+  st.W = ns::wave_sum_f32(st.W);
+  if (part + 1 == a.S && a.V % EPV != 0) {                 // the last elements, fewer than a vector
+    const int e = nvec * EPV + lane;
+    st = join(st, stat_of_lanes(e < a.V ? one_elem<ET>(zrow, e) : -INFINITY, a.c), a.c);
+  }
+  if (a.S == 1) {
+    finish(a, row, st, one_elem<ET>(zrow, tok), Given(a, row, w), lane == 0);
+  } else if (lane == 0) {
+    a.stat[item] = st;
+    if (part == 0) a.ztok[row] = one_elem<ET>(zrow, tok);
+  }
+}
+
+// The parts of a row joined, one in each of S lanes and the whole in all of them.
+__device__ __forceinline__ Stat join_parts(const Args& a, Stat st, int lane) {
+  for (int m = 1; m < a.S; m <<= 1) {
+    Stat o;
+    o.top = __shfl_xor(st.top, m, NS_WAVE);
+    o.ref = __shfl_xor(st.ref, m, NS_WAVE);
+    o.E = __shfl_xor(st.E, m, NS_WAVE);
+    o.S = __shfl_xor(st.S, m, NS_WAVE);
+    o.W = __shfl_xor(st.W, m, NS_WAVE);
+    st = lane & m ? join(o, st, a.c) : join(st, o, a.c);   // the lower part first in both lanes
+  }
+  return st;
+}
+
+// The sum of a block's values, in the same order each time.
+template <int T>
+__device__ __forceinline__ void put_sum(double s, float* loss) {
+  __shared__ double sh[T / NS_WAVE];
   const int tid = threadIdx.x;
-  double s = 0.0;
-  for (int i = tid; i < L; i += kTotalThreads) s += row_loss[i];
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m, NS_WAVE);
   if ((tid & (NS_WAVE - 1)) == 0) sh[tid / NS_WAVE] = s;
   __syncthreads();
   if (tid != 0) return;
-  s = 0.0;
-  for (int i = 0; i < kTotalThreads / NS_WAVE; ++i) s += sh[i];
+  s = sh[0];
+  for (int i = 1; i < T / NS_WAVE; ++i) s += sh[i];
   *loss = (float)s;
 }
 
+// Rows whose parts are known: the outputs of every row, S lanes each, and the loss.
+constexpr int kTotalThreads = 1024;
+
+__device__ __forceinline__ void end_rows(const Args& a, float* loss) {
+  const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1), part = tid & (a.S - 1);
+  double total = 0.0;
+  for (int row = tid / a.S; row < a.L; row += kTotalThreads / a.S) {
+    int tok;
+    float w;
+    const bool in = taken(a, row, tok, w);
+    const Given given(a, row, w);
+    const float ztok = a.ztok[row];                        // of a row that is not taken: anything
+    const Stat st = join_parts(a, a.stat[(size_t)row * a.S + part], lane);
+    if (in) {
+      double mine = 0.0;
+      finish(a, row, st, ztok, given, part == 0, &mine);
+      if (part == 0) total += mine;
+    } else if (part == 0) {
+      put_nothing(a, row);
+    }
+  }
+  put_sum<kTotalThreads>(total, loss);
+}
+
+__global__ __launch_bounds__(kTotalThreads) void k_policy_end(Args a, float* loss) { end_rows(a, loss); }
+
+// The same beside the gradient: the last block ends the rows, each of the others
+// takes a part of one row and joins that row's parts for itself.  dlogits may be
+// logits: a block reads its part before it writes it, and the token's logit is in
+// the workspace.
+constexpr int kSlopeThreads = kTotalThreads;
+
 template <int ET>
-void launch_policy(const Args& a, hipStream_t stream) {
-  hipLaunchKernelGGL(k_policy_row<ET>, dim3((unsigned)a.L), dim3(kRowThreads), 0, stream, a);
+__global__ __launch_bounds__(kSlopeThreads) void k_policy_slope(Args a, float* loss, int chunks) {
+  constexpr int EPV = per_vec(ET), U = 2;
+  if (blockIdx.x + 1 == gridDim.x) {
+    end_rows(a, loss);
+    return;
+  }
+  __shared__ Slope sh;
+  const size_t row = blockIdx.x / (unsigned)chunks;
+  const int chunk = (int)(blockIdx.x % (unsigned)chunks);
+  const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1);
+  const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
+  char* drow = (char*)a.dz + row * (size_t)a.ld_d * elem_bytes(ET);
+  const int nvec = a.V / EPV, tail = nvec * EPV + tid;
+  const int step = chunks * kSlopeThreads * U, q0 = chunk * kSlopeThreads * U + tid;
+  int tok;
+  float w;
+  const bool in = taken(a, row, tok, w);                   // uniform
+  if (in && tid < NS_WAVE) {
+    const Given given(a, row, w);
+    const Slope s = finish(a, row, join_parts(a, a.stat[row * a.S + (lane & (a.S - 1))], lane), a.ztok[row], given, false);
+    if (tid == 0) sh = s;
+  }
+  u32x4 x[U];
+  const auto load = [&](int q) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = q + u * kSlopeThreads;
+      x[u] = __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)(at < nvec ? at : 0) * 16));
+    }
+  };
+  if (in && q0 - tid < nvec) load(q0);
+  __syncthreads();
+  Slope s{0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in) s = sh;
+  for (int q = q0; q - tid < nvec; q += step) {
+    if (in && q != q0) load(q);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = q + u * kSlopeThreads;
+      if (at >= nvec) continue;
+      float v[EPV];
+      widen<ET>(x[u], v);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) v[e] = in ? slope_at(s, a.c, v[e]) : 0.f;
+      __builtin_nontemporal_store(narrow<ET>(v), (u32x4_any*)(drow + (size_t)at * 16));
+      // the token's element once more
+      if (in && at == tok / EPV) put_elem<ET>(drow, tok, slope_at(s, a.c, a.ztok[row]) + s.G);
+    }
+  }
+  if (chunk == 0 && tail < a.V) {
+    const float z = one_elem<ET>(zrow, tail);
+    put_elem<ET>(drow, tail, in ? slope_at(s, a.c, z) + (tail == tok ? s.G : 0.f) : 0.f);
+  }
+}
+
+// The sum of the rows' losses.
+__global__ __launch_bounds__(kTotalThreads) void k_policy_total(const double* __restrict__ row_loss, int L,
+                                                                float* __restrict__ loss) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < L; i += kTotalThreads) s += row_loss[i];
+  put_sum<kTotalThreads>(s, loss);
+}
+
+// Parts of a row: doubled until about 2048 waves run, each with a batch at least.
+constexpr int kMaxParts = 64;
+constexpr int kWavesWanted = 2048;
+
+int parts_of(int L, int V, int dtype) {
+  const int batch = NS_WAVE * kUnroll * per_vec(dtype);
+  const int most = (V + batch - 1) / batch;
+  int s = 1;
+  while ((int64_t)s * L * 4 < kWavesWanted * 3 && s * 2 <= most && s < kMaxParts) s *= 2;
+  return s;
+}
+
+// From this many rows on a block takes one and reads it once.
+constexpr int kWholeRows = 256;
+
+template <int ET, int T, int U>
+void launch_row(const Args& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_policy_row<ET, T, U>), dim3((unsigned)a.L), dim3(T), 0, stream, a);
+}
+
+template <int ET>
+int launch_policy(Args a, float* loss, hipStream_t stream) {
+  const int nvec = a.V / per_vec(ET);
+  if (a.dz && a.L >= kWholeRows) {
+    if (nvec <= 64 * 4) launch_row<ET, 64, 4>(a, stream);
+    else if (nvec <= 256 * 4) launch_row<ET, 256, 4>(a, stream);
+    else if (nvec <= 256 * 8) launch_row<ET, 256, 8>(a, stream);
+    else if (nvec <= 256 * 16) launch_row<ET, 256, 16>(a, stream);
+    else if (nvec <= 512 * 16) launch_row<ET, 512, 16>(a, stream);
+    else launch_row<ET, 1024, 16>(a, stream);
+    a.S = 1;
+  } else {
+    if (a.dz && a.S == 1) a.S = 2;                         // the gradient's blocks take statistics from the workspace
+    const dim3 grid((unsigned)(((int64_t)a.L * a.S + kPartWaves - 1) / kPartWaves)), block(kPartWaves * NS_WAVE);
+    hipLaunchKernelGGL(k_policy_parts<ET>, grid, block, 0, stream, a);
+  }
+  const int rc = ns_launch_status();
+  if (rc != NS_OK) return rc;
+  if (a.S == 1) {
+    hipLaunchKernelGGL(k_policy_total, dim3(1), dim3(kTotalThreads), 0, stream, (const double*)a.row_loss, a.L, loss);
+  } else if (!a.dz) {
+    hipLaunchKernelGGL(k_policy_end, dim3(1), dim3(kTotalThreads), 0, stream, a, loss);
+  } else {
+    const int chunks = nvec > 0 ? (nvec + 2 * kSlopeThreads - 1) / (2 * kSlopeThreads) : 1;
+    hipLaunchKernelGGL(k_policy_slope<ET>, dim3((unsigned)(chunks * a.L + 1)), dim3(kSlopeThreads), 0, stream, a, loss, chunks);
+  }
+  return ns_launch_status();
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Room for the parts of L rows or any fewer: a row has at most the parts of a
+// single one (of float32, which has the smallest batches), two where there is a
+// gradient, and rows in more come to less than 3/2 kWavesWanted of them together.
 size_t policy_ws(int L, int V) {
-  (void)V;
-  return align256((size_t)(L > 0 ? L : 1) * 8);
+  const size_t l = (size_t)(L > 0 ? L : 1), one = (size_t)parts_of(1, V, NS_FP32);
+  const size_t most = l * (one < 2 ? 2 : one), few = l * 2 > kWavesWanted * 3 / 2 ? l * 2 : kWavesWanted * 3 / 2;
+  return align256(l * 8) + align256((most < few ? most : few) * sizeof(Stat)) + align256(l * 4);
 }
 
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
@@ -259,18 +546,21 @@ int nanospec_policy_loss(const void* logits, int64_t ld, int32_t L, int32_t V, i
   if (ws_bytes < policy_ws(L, V)) return NS_ECAPACITY;
   (void)hipGetLastError();
   const float c = (float)((double)inv_temp * 1.4426950408889634);
-  const Args a{logits, ld, L, V, inv_temp, c, (float)((double)inv_temp * 1.4426950408889634 / c - 1.0), tokens,
-               old_logprob, ref_logprob, advantage, weight, eps_low, eps_high, kl_coef, ent_coef, logprob, kl, entropy,
-               g_loss, dlogits, ld_d, (double*)ws};
-  if (L > 0) {
-    if (dtype == NS_BF16) launch_policy<NS_BF16>(a, stream);
-    else if (dtype == NS_FP16) launch_policy<NS_FP16>(a, stream);
-    else launch_policy<NS_FP32>(a, stream);
-    const int rc = ns_launch_status();
-    if (rc != NS_OK) return rc;
+  char* base = (char*)ws;
+  const int S = parts_of(L, V, dtype);
+  Args a{logits, ld, L, V, inv_temp, c, (float)((double)inv_temp * 1.4426950408889634 / c - 1.0), tokens,
+         old_logprob, ref_logprob, advantage, weight, eps_low, eps_high, kl_coef, ent_coef, logprob, kl, entropy,
+         g_loss, dlogits, ld_d, (double*)base, S, nullptr, nullptr};
+  const size_t rows = align256((size_t)(L > 0 ? L : 1) * 8);
+  a.ztok = (float*)(base + rows);
+  a.stat = (Stat*)(base + rows + align256((size_t)(L > 0 ? L : 1) * 4));
+  if (L == 0) {
+    hipLaunchKernelGGL(k_policy_total, dim3(1), dim3(kTotalThreads), 0, stream, (const double*)a.row_loss, 0, loss);
+    return ns_launch_status();
   }
-  hipLaunchKernelGGL(k_policy_total, dim3(1), dim3(kTotalThreads), 0, stream, (const double*)a.row_loss, L, loss);
-  return ns_launch_status();
+  if (dtype == NS_BF16) return launch_policy<NS_BF16>(a, loss, stream);
+  if (dtype == NS_FP16) return launch_policy<NS_FP16>(a, loss, stream);
+  return launch_policy<NS_FP32>(a, loss, stream);
 }
 
 }  // extern "C"

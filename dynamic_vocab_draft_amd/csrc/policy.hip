@@ -178,93 +178,191 @@ __device__ __forceinline__ Stat stat_of_lanes(float v, float c) {
   return s;
 }
 
+// A row as a buffer: its whole vectors, at any address that its elements may have.
+// Vectors past the last are read as zeros and not written, without a question.
+struct Row {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Row(const void* p, size_t row, int64_t ld, int esz, int nvec)
+      : r(__builtin_amdgcn_make_buffer_rsrc((char*)p + row * (size_t)ld * esz, 0, nvec * 16, 0x00027000)) {}
+  __device__ __forceinline__ u32x4 get(uint32_t at) const {   // read once
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 2));
+  }
+  __device__ __forceinline__ void put(uint32_t at, u32x4 v) const { __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 2); }
+};
+
 // A block of T threads takes a row and holds it in registers (U vectors a thread;
-// what is longer is read again) between its statistics and its gradient.
+// what is longer is read again) between its statistics and its gradient, then
+// the row gridDim.x on, whose vectors are asked for as this one's fall free: the
+// memory works on both while either is computed.
 template <int ET, int T, int U>
 __global__ __launch_bounds__(T) void k_policy_row(Args a) {
-  constexpr int EPV = per_vec(ET), NW = T / NS_WAVE, HELD = T * U;
+  constexpr int EPV = per_vec(ET), NW = T / NS_WAVE, HELD = T * U, ESZ = elem_bytes(ET);
   __shared__ Stat sh[NW];
   __shared__ Slope sh_slope;
+  const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1), wv = __builtin_amdgcn_readfirstlane(tid / NS_WAVE);
+  const int nvec = a.V / EPV, tail = nvec * EPV + tid;
+  int tok;
+  float w;
+  // The first row from `row` on that is taken; the others' outputs are zeros.
+  const auto next_row = [&](int row) {
+    for (; row < a.L; row += gridDim.x) {
+      if (taken(a, (size_t)row, tok, w)) break;            // uniform
+      const Row d(a.dz, (size_t)row, a.ld_d, ESZ, nvec);
+      if (tid == 0) put_nothing(a, (size_t)row);
+      for (int q = tid; q < nvec; q += T) d.put((uint32_t)q * 16, u32x4{0, 0, 0, 0});
+      if (tail < a.V) put_elem<ET>(a.dz, (size_t)row * (size_t)a.ld_d + tail, 0.f);
+    }
+    return row;
+  };
+  int row = next_row((int)blockIdx.x);
+  if (row >= a.L) return;
+  u32x4 x[U];
+  {
+    const Row z(a.z, (size_t)row, a.ld, ESZ, nvec);
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = z.get((uint32_t)(u * T + tid) * 16);
+  }
+  while (true) {
+    const size_t at = (size_t)row * (size_t)a.ld;
+    const Given given(a, (size_t)row, w);
+    const float ztok = one_elem<ET>(a.z, at + tok);
+    float ztail = -INFINITY;
+    if (tail < a.V) ztail = one_elem<ET>(a.z, at + tail);
+    NS_ISSUE_FENCE();
+    Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
+    const auto add = [&](u32x4(&v)[kUnroll], int q, int first) {   // q: the lane's first vector, `first` the block's
+      if (first + kUnroll * T > nvec) {                    // uniform
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (q + u * T >= nvec) v[u] = minus_inf<ET>();
+      }
+      float mx[kUnroll], lane_max;
+      add_batch<ET>(v, a.c, st, mx, lane_max);
+    };
+#pragma unroll
+    for (int u = 0; u < U; u += kUnroll) {
+      if (u * T >= nvec) break;                            // uniform
+      u32x4 v[kUnroll] = {x[u], x[u + 1], x[u + 2], x[u + 3]};
+      add(v, u * T + tid, u * T);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (HELD < nvec) {
+      const Row z(a.z, (size_t)row, a.ld, ESZ, nvec);
+      for (int q = HELD; q < nvec; q += T * kUnroll) {
+        u32x4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = z.get((uint32_t)(q + u * T + tid) * 16);
+        NS_ISSUE_FENCE();
+        add(v, q + tid, q);
+      }
+    }
+    st.S = ns::wave_sum_f32(st.S);
+    st.W = ns::wave_sum_f32(st.W);
+    if (wv == 0 && nvec * EPV < a.V) st = join(st, stat_of_lanes(ztail, a.c), a.c);
+    if (NW > 1) {
+      if (lane == 0) sh[wv] = st;
+      __syncthreads();
+    }
+    Slope s;
+    if (wv == 0) {
+#pragma unroll
+      for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
+      s = finish(a, (size_t)row, st, ztok, given, tid == 0);
+      if (NW > 1 && tid == 0) sh_slope = s;
+    }
+    if (NW > 1) {
+      __syncthreads();
+      s = sh_slope;
+    }
+    const int this_row = row, this_tok = tok;
+    row = next_row(row + (int)gridDim.x);
+    const bool more = row < a.L;
+    const Row zn(a.z, (size_t)(more ? row : this_row), a.ld, ESZ, more ? nvec : 0);
+    const Row d(a.dz, (size_t)this_row, a.ld_d, ESZ, nvec);
+    const auto slope = [&](u32x4 z) {
+      float v[EPV];
+      widen<ET>(z, v);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) v[e] = slope_at(s, a.c, v[e]);
+      return narrow<ET>(v);
+    };
+    uint32_t place = (uint32_t)tid * 16;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      asm volatile("" : "+v"(place));                      // added up as it goes, not kept for every u
+      if (u * T < nvec) d.put(place, slope(x[u]));         // uniform
+      x[u] = zn.get(place);                                // zeros behind the last row
+      place += T * 16;
+    }
+    if (HELD < nvec) {
+      const Row z(a.z, (size_t)this_row, a.ld, ESZ, nvec);
+      for (int q = HELD + tid; q < nvec; q += T) d.put((uint32_t)q * 16, slope(z.get((uint32_t)q * 16)));
+    }
+    const size_t to = (size_t)this_row * (size_t)a.ld_d;
+    if (tail < a.V) put_elem<ET>(a.dz, to + tail, slope_at(s, a.c, ztail));
+    // the thread that wrote the token's element writes it once more
+    const int owner = this_tok < nvec * EPV ? this_tok / EPV % T : this_tok - nvec * EPV;
+    if (tid == owner) put_elem<ET>(a.dz, to + this_tok, slope_at(s, a.c, ztok) + s.G);
+    if (!more) return;
+  }
+}
+
+// Many rows without a gradient: a block of four waves streams a row, two batches
+// a wave in flight.
+constexpr int kStreamThreads = 256;
+
+template <int ET>
+__global__ __launch_bounds__(kStreamThreads) void k_policy_stream(Args a) {
+  constexpr int EPV = per_vec(ET), NW = kStreamThreads / NS_WAVE, STEP = NS_WAVE * kUnroll;
+  __shared__ Stat sh[NW];
   const size_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1), wv = tid / NS_WAVE;
-  const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
-  char* drow = (char*)a.dz + row * (size_t)a.ld_d * elem_bytes(ET);
-  const int nvec = a.V / EPV, tail = nvec * EPV + tid;
   int tok;
   float w;
   if (!taken(a, row, tok, w)) {                            // uniform
     if (tid == 0) put_nothing(a, row);
-    for (int q = tid; q < nvec; q += T) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, (u32x4_any*)(drow + (size_t)q * 16));
-    if (tail < a.V) put_elem<ET>(drow, tail, 0.f);
     return;
   }
-  const auto load = [&](int q) {
-    return __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)(q < nvec ? q : 0) * 16));
-  };
-  u32x4 x[U];
-  if (nvec > 0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = load(u * T + tid);
-  }
-  const Given given(a, row, w);
+  const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
+  const int nvec = a.V / EPV;
   const float ztok = one_elem<ET>(zrow, tok);
-  float ztail = -INFINITY;
-  if (tail < a.V) ztail = one_elem<ET>(zrow, tail);
-  NS_ISSUE_FENCE();
+  const Given given(a, row, w);
   Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
-  const auto add = [&](const u32x4(&v)[kUnroll], int q) {  // q: the lane's first vector
-    u32x4 y[kUnroll];
+  const auto load = [&](int base, u32x4(&x)[kUnroll]) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) y[u] = q + u * T < nvec ? v[u] : minus_inf<ET>();
-    float mx[kUnroll], lane_max;
-    add_batch<ET>(y, a.c, st, mx, lane_max);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int q = base + u * NS_WAVE + lane;
+      x[u] = __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)(q < nvec ? q : nvec - 1) * 16));
+    }
   };
-#pragma unroll
-  for (int u = 0; u < U; u += kUnroll) {
-    if (u * T >= nvec) break;                              // uniform
-    const u32x4 v[kUnroll] = {x[u], x[u + 1], x[u + 2], x[u + 3]};
-    add(v, u * T + tid);
-  }
-  for (int q = HELD + tid; q - tid < nvec; q += T * kUnroll) {
-    u32x4 v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = *(const u32x4_any*)(zrow + (size_t)(q + u * T < nvec ? q + u * T : 0) * 16);
+  u32x4 x0[kUnroll], x1[kUnroll];
+  if (wv * STEP < nvec) load(wv * STEP, x0);
+#pragma unroll 1
+  for (int base = wv * STEP; base < nvec; base += NW * STEP) {
+    load(base + NW * STEP, x1);
     NS_ISSUE_FENCE();
-    add(v, q);
+    if (base + STEP > nvec) {                              // uniform
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (base + u * NS_WAVE + lane >= nvec) x0[u] = minus_inf<ET>();
+    }
+    float mx[kUnroll], lane_max;
+    add_batch<ET>(x0, a.c, st, mx, lane_max);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x0[u] = x1[u];
   }
   st.S = ns::wave_sum_f32(st.S);
   st.W = ns::wave_sum_f32(st.W);
-  if (wv == 0 && nvec * EPV < a.V) st = join(st, stat_of_lanes(ztail, a.c), a.c);
-  if (NW > 1) {
-    if (lane == 0) sh[wv] = st;
-    __syncthreads();
+  if (wv == 0 && a.V % EPV != 0) {                         // the last elements, fewer than a vector
+    const int e = nvec * EPV + lane;
+    st = join(st, stat_of_lanes(e < a.V ? one_elem<ET>(zrow, e) : -INFINITY, a.c), a.c);
   }
-  Slope s;
-  if (wv == 0) {
+  if (lane == 0) sh[wv] = st;
+  __syncthreads();
+  if (wv != 0) return;
 #pragma unroll
-    for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
-    s = finish(a, row, st, ztok, given, tid == 0);
-    if (NW > 1 && tid == 0) sh_slope = s;
-  }
-  if (NW > 1) {
-    __syncthreads();
-    s = sh_slope;
-  }
-  const auto put = [&](u32x4 z, int q) {
-    float v[EPV];
-    widen<ET>(z, v);
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) v[e] = slope_at(s, a.c, v[e]);
-    __builtin_nontemporal_store(narrow<ET>(v), (u32x4_any*)(drow + (size_t)q * 16));
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (u * T + tid < nvec) put(x[u], u * T + tid);
-  for (int q = HELD + tid; q < nvec; q += T) put(*(const u32x4_any*)(zrow + (size_t)q * 16), q);
-  if (tail < a.V) put_elem<ET>(drow, tail, slope_at(s, a.c, ztail));
-  // the thread that wrote the token's element writes it once more
-  const int owner = tok < nvec * EPV ? tok / EPV % T : tok - nvec * EPV;
-  if (tid == owner) put_elem<ET>(drow, tok, slope_at(s, a.c, ztok) + s.G);
+  for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
+  finish(a, row, st, ztok, given, lane == 0);
 }
 
 // Parts of rows: a wave streams part `part` of S of one row.  With S = 1 it ends
@@ -470,13 +568,18 @@ constexpr int kWholeRows = 256;
 
 template <int ET, int T, int U>
 void launch_row(const Args& a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_policy_row<ET, T, U>), dim3((unsigned)a.L), dim3(T), 0, stream, a);
+  // one block of 1024 threads a CU; smaller ones overlap each other
+  const unsigned blocks = T == 1024 && a.L > 256 ? 256u : (unsigned)a.L;
+  hipLaunchKernelGGL((k_policy_row<ET, T, U>), dim3(blocks), dim3(T), 0, stream, a);
 }
 
 template <int ET>
 int launch_policy(Args a, float* loss, hipStream_t stream) {
   const int nvec = a.V / per_vec(ET);
-  if (a.dz && a.L >= kWholeRows) {
+  if (a.L >= kWholeRows && !a.dz) {
+    hipLaunchKernelGGL(k_policy_stream<ET>, dim3((unsigned)a.L), dim3(kStreamThreads), 0, stream, a);
+    a.S = 1;
+  } else if (a.L >= kWholeRows) {
     if (nvec <= 64 * 4) launch_row<ET, 64, 4>(a, stream);
     else if (nvec <= 256 * 4) launch_row<ET, 256, 4>(a, stream);
     else if (nvec <= 256 * 8) launch_row<ET, 256, 8>(a, stream);

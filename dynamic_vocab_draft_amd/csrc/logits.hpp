@@ -74,25 +74,8 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
   return r;
 }
 
-// Adds a batch of a wave's vectors to its statistics; mx, lane_max and the
-// result are the maxima of each vector, of the lane's and of the wave's.
-template <int ET>
-__device__ __forceinline__ float add_batch(const u32x4 (&x)[kUnroll], float c, Stat& st, float (&mx)[kUnroll],
-                                           float& lane_max) {
-  constexpr int EPV = per_vec(ET);
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    float v[EPV];
-    widen<ET>(x[u], v);
-    float m = v[0];
-#pragma unroll
-    for (int e = 1; e < EPV; ++e) m = fmaxf(m, v[e]);
-    mx[u] = m;
-  }
-  lane_max = mx[0];
-#pragma unroll
-  for (int u = 1; u < kUnroll; ++u) lane_max = fmaxf(lane_max, mx[u]);
-  const float top = ns::wave_max_f32(lane_max);
+// Takes a maximum into a wave's statistics, which are scaled anew where they have to be.
+__device__ __forceinline__ void raise(Stat& st, float top, float c) {
   if (top > st.top) {                                      // uniform
     const bool had = st.top != -INFINITY;
     st.top = top;
@@ -115,6 +98,28 @@ __device__ __forceinline__ float add_batch(const u32x4 (&x)[kUnroll], float c, S
       st.E = 0.f;
     }
   }
+}
+
+// Adds a batch of a wave's vectors to its statistics; mx, lane_max and the
+// result are the maxima of each vector, of the lane's and of the wave's.
+template <int ET>
+__device__ __forceinline__ float add_batch(const u32x4 (&x)[kUnroll], float c, Stat& st, float (&mx)[kUnroll],
+                                           float& lane_max) {
+  constexpr int EPV = per_vec(ET);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float v[EPV];
+    widen<ET>(x[u], v);
+    float m = v[0];
+#pragma unroll
+    for (int e = 1; e < EPV; ++e) m = fmaxf(m, v[e]);
+    mx[u] = m;
+  }
+  lane_max = mx[0];
+#pragma unroll
+  for (int u = 1; u < kUnroll; ++u) lane_max = fmaxf(lane_max, mx[u]);
+  const float top = ns::wave_max_f32(lane_max);
+  raise(st, top, c);
   // A batch is summed by itself first: shorter chains of roundings.
   float S = 0.f, W = 0.f;
   const float E = st.E, ref = st.ref;

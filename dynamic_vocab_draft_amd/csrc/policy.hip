@@ -160,6 +160,25 @@ __device__ __forceinline__ u32x4 narrow(const float (&v)[per_vec(ET)]) {
   }
 }
 
+// The gradient of a vector.  B is 0 where there is no entropy term: a usual row
+// does without a third of the instructions, at a uniform branch a vector.
+template <int ET>
+__device__ __forceinline__ u32x4 slope_of(const Slope& s, float c, bool usual, u32x4 z) {
+  float v[per_vec(ET)];
+  widen<ET>(z, v);
+  if (usual) {
+#pragma unroll
+    for (int e = 0; e < per_vec(ET); ++e) v[e] = exp2_fast(fmaf(v[e], c, -s.E)) * s.A;
+  } else {
+#pragma unroll
+    for (int e = 0; e < per_vec(ET); ++e) v[e] = slope_at(s, c, v[e]);
+  }
+  return narrow<ET>(v);
+}
+__device__ __forceinline__ bool is_usual(const Slope& s) {
+  return __builtin_amdgcn_readfirstlane((int)(s.ref == 0.f && s.B == 0.f)) != 0;
+}
+
 // Statistics of fewer elements than a vector's, one a lane.
 __device__ __forceinline__ Stat stat_of_lanes(float v, float c) {
   Stat s{-INFINITY, 0.f, 0.f, 0.f, 0.f};
@@ -188,6 +207,62 @@ struct Row {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 2));
   }
   __device__ __forceinline__ void put(uint32_t at, u32x4 v) const { __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 2); }
+};
+
+// Adds a vector to a wave's sums.
+template <int ET>
+__device__ __forceinline__ void add_vector(u32x4 x, float c, Stat& st) {
+  constexpr int EPV = per_vec(ET);
+  float v[EPV], S = 0.f, W = 0.f;
+  widen<ET>(x, v);
+  if (st.ref == 0.f) {                                     // uniform
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) {
+      const float y = fmaf(v[e], c, -st.E), p = exp2_fast(y);
+      S += p;
+      W = fmaf(p, fmaxf(y, -200.f), W);                    // 2^y is 0 for masked logits: no 0 * inf
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) {
+      const float y = (v[e] - st.ref) * c, p = exp2_fast(y);
+      S += p;
+      W = fmaf(p, fmaxf(y, -200.f), W);
+    }
+  }
+  st.S += S;
+  st.W += W;
+}
+
+// The largest element of many vectors, two 16-bit elements an instruction.
+// bfloat16 compares as signed integers do where some element is positive; where
+// all are negative the order is reversed.  NaN is found by the sums.
+template <int ET>
+struct Top {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  typedef short i16x2 __attribute__((ext_vector_type(2)));
+  float f = -INFINITY;
+  f16x2 h = {(_Float16)-INFINITY, (_Float16)-INFINITY};
+  i16x2 hi = {(short)0x8000, (short)0x8000}, lo = {0x7FFF, 0x7FFF};
+  __device__ __forceinline__ void add(u32x4 x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (ET == NS_FP32) {
+        f = fmaxf(f, __uint_as_float(x[i]));
+      } else if constexpr (ET == NS_FP16) {
+        h = __builtin_elementwise_max(h, __builtin_bit_cast(f16x2, x[i]));
+      } else {
+        hi = __builtin_elementwise_max(hi, __builtin_bit_cast(i16x2, x[i]));
+        lo = __builtin_elementwise_min(lo, __builtin_bit_cast(i16x2, x[i]));
+      }
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    if constexpr (ET == NS_FP32) return f;
+    if constexpr (ET == NS_FP16) return fmaxf((float)h.x, (float)h.y);
+    const short a = hi.x > hi.y ? hi.x : hi.y, b = lo.x < lo.y ? lo.x : lo.y;
+    return ns::bf16_lo((uint32_t)(uint16_t)(a >= 0 ? a : b));
+  }
 };
 
 // A block of T threads takes a row and holds it in registers (U vectors a thread;
@@ -229,31 +304,42 @@ __global__ __launch_bounds__(T) void k_policy_row(Args a) {
     float ztail = -INFINITY;
     if (tail < a.V) ztail = one_elem<ET>(a.z, at + tail);
     NS_ISSUE_FENCE();
+    // each wave's vectors by themselves: their maximum, then their sums
+    Top<ET> most;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if ((u + 1) * T > nvec && u * T + tid >= nvec) x[u] = minus_inf<ET>();
+      most.add(x[u]);
+    }
     Stat st{-INFINITY, 0.f, 0.f, 0.f, 0.f};
-    const auto add = [&](u32x4(&v)[kUnroll], int q, int first) {   // q: the lane's first vector, `first` the block's
-      if (first + kUnroll * T > nvec) {                    // uniform
+    raise(st, ns::wave_max_f32(most.value()), a.c);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if (q + u * T >= nvec) v[u] = minus_inf<ET>();
-      }
-      float mx[kUnroll], lane_max;
-      add_batch<ET>(v, a.c, st, mx, lane_max);
-    };
-#pragma unroll
-    for (int u = 0; u < U; u += kUnroll) {
-      if (u * T >= nvec) break;                            // uniform
-      u32x4 v[kUnroll] = {x[u], x[u + 1], x[u + 2], x[u + 3]};
-      add(v, u * T + tid, u * T);
+    for (int u = 0; u < U; ++u) {
+      if (u * T < nvec) add_vector<ET>(x[u], a.c, st);     // uniform
+      asm volatile("" : "+v"(x[u]));                       // widened anew below: twice the registers otherwise
       __builtin_amdgcn_sched_barrier(0);
     }
     if (HELD < nvec) {
       const Row z(a.z, (size_t)row, a.ld, ESZ, nvec);
-      for (int q = HELD; q < nvec; q += T * kUnroll) {
-        u32x4 v[kUnroll];
+      constexpr int AT_ONCE = 4;
+#pragma unroll 1
+      for (int q = HELD; q < nvec; q += T * AT_ONCE) {
+        u32x4 v[AT_ONCE];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = z.get((uint32_t)(q + u * T + tid) * 16);
-        NS_ISSUE_FENCE();
-        add(v, q + tid, q);
+        for (int u = 0; u < AT_ONCE; ++u) v[u] = z.get((uint32_t)(q + u * T + tid) * 16);
+        Top<ET> more;
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          if (q + (u + 1) * T > nvec && q + u * T + tid >= nvec) v[u] = minus_inf<ET>();
+          more.add(v[u]);
+        }
+        const float top = more.value();
+        if (__ballot(top > st.top)) raise(st, ns::wave_max_f32(top), a.c);
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          add_vector<ET>(v[u], a.c, st);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     st.S = ns::wave_sum_f32(st.S);
@@ -279,24 +365,19 @@ __global__ __launch_bounds__(T) void k_policy_row(Args a) {
     const bool more = row < a.L;
     const Row zn(a.z, (size_t)(more ? row : this_row), a.ld, ESZ, more ? nvec : 0);
     const Row d(a.dz, (size_t)this_row, a.ld_d, ESZ, nvec);
-    const auto slope = [&](u32x4 z) {
-      float v[EPV];
-      widen<ET>(z, v);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) v[e] = slope_at(s, a.c, v[e]);
-      return narrow<ET>(v);
-    };
+    const bool usual = is_usual(s);
     uint32_t place = (uint32_t)tid * 16;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       asm volatile("" : "+v"(place));                      // added up as it goes, not kept for every u
-      if (u * T < nvec) d.put(place, slope(x[u]));         // uniform
+      if (u * T < nvec) d.put(place, slope_of<ET>(s, a.c, usual, x[u]));   // uniform
       x[u] = zn.get(place);                                // zeros behind the last row
+      __builtin_amdgcn_sched_barrier(0);
       place += T * 16;
     }
     if (HELD < nvec) {
       const Row z(a.z, (size_t)this_row, a.ld, ESZ, nvec);
-      for (int q = HELD + tid; q < nvec; q += T) d.put((uint32_t)q * 16, slope(z.get((uint32_t)q * 16)));
+      for (int q = HELD + tid; q < nvec; q += T) d.put((uint32_t)q * 16, slope_of<ET>(s, a.c, usual, z.get((uint32_t)q * 16)));
     }
     const size_t to = (size_t)this_row * (size_t)a.ld_d;
     if (tail < a.V) put_elem<ET>(a.dz, to + tail, slope_at(s, a.c, ztail));
@@ -501,7 +582,7 @@ __global__ __launch_bounds__(kSlopeThreads) void k_policy_slope(Args a, float* l
   const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
   char* drow = (char*)a.dz + row * (size_t)a.ld_d * elem_bytes(ET);
   const int nvec = a.V / EPV, tail = nvec * EPV + tid;
-  const int step = chunks * kSlopeThreads * U, q0 = chunk * kSlopeThreads * U + tid;
+  const int q0 = chunk * kSlopeThreads * U + tid;
   int tok;
   float w;
   const bool in = taken(a, row, tok, w);                   // uniform
@@ -511,31 +592,25 @@ __global__ __launch_bounds__(kSlopeThreads) void k_policy_slope(Args a, float* l
     if (tid == 0) sh = s;
   }
   u32x4 x[U];
-  const auto load = [&](int q) {
+  if (in && q0 - tid < nvec) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = q + u * kSlopeThreads;
+      const int at = q0 + u * kSlopeThreads;
       x[u] = __builtin_nontemporal_load((const u32x4_any*)(zrow + (size_t)(at < nvec ? at : 0) * 16));
     }
-  };
-  if (in && q0 - tid < nvec) load(q0);
+  }
   __syncthreads();
   Slope s{0.f, 0.f, 0.f, 0.f, 0.f};
   if (in) s = sh;
-  for (int q = q0; q - tid < nvec; q += step) {
-    if (in && q != q0) load(q);
+  const bool usual = is_usual(s);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = q + u * kSlopeThreads;
-      if (at >= nvec) continue;
-      float v[EPV];
-      widen<ET>(x[u], v);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) v[e] = in ? slope_at(s, a.c, v[e]) : 0.f;
-      __builtin_nontemporal_store(narrow<ET>(v), (u32x4_any*)(drow + (size_t)at * 16));
-      // the token's element once more
-      if (in && at == tok / EPV) put_elem<ET>(drow, tok, slope_at(s, a.c, a.ztok[row]) + s.G);
-    }
+  for (int u = 0; u < U; ++u) {
+    const int at = q0 + u * kSlopeThreads;
+    if (at >= nvec) continue;
+    const u32x4 y = in ? slope_of<ET>(s, a.c, usual, x[u]) : u32x4{0, 0, 0, 0};
+    __builtin_nontemporal_store(y, (u32x4_any*)(drow + (size_t)at * 16));
+    // the token's element once more
+    if (in && at == tok / EPV) put_elem<ET>(drow, tok, slope_at(s, a.c, a.ztok[row]) + s.G);
   }
   if (chunk == 0 && tail < a.V) {
     const float z = one_elem<ET>(zrow, tail);

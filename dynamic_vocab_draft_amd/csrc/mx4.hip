@@ -73,17 +73,13 @@ __device__ __forceinline__ uint32_t quant_eight(const Eight<ET>& x, uint32_t byt
   return byte == 255 ? 0u : r;
 }
 
-// The block's largest magnitude, as float32 bits, from what a lane holds of it.
+// The largest magnitude of eight elements, as float32 bits, which order like it.
 template <int ET>
-__device__ __forceinline__ uint32_t block_top(const Eight<ET>& x) {
+__device__ __forceinline__ uint32_t top_bits(const Eight<ET>& x) {
   const uint32_t m = x.top(0);
-  float top;
-  if (ET == NS_FP32) top = __uint_as_float(m);
-  else {
-    const uint32_t lo = m & 0xFFFFu, hi = m >> 16, b = lo > hi ? lo : hi;
-    top = ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b);
-  }
-  return quad_max_u32(__float_as_uint(top));       // float32 bits order the same way
+  if (ET == NS_FP32) return m;
+  const uint32_t lo = m & 0xFFFFu, hi = m >> 16, b = lo > hi ? lo : hi;
+  return __float_as_uint(ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b));
 }
 
 template <int ET>
@@ -106,7 +102,7 @@ __global__ __launch_bounds__(kRowThreads) void k_mx4_rows(const void* __restrict
   for (int u = 0; u < kRowUnits; ++u) {
     const int c = c0 + u * (kRowThreads / 32);
     if (c >= total) continue;                      // whole half waves
-    const uint32_t byte = scale_byte(block_top<ET>(v[u]));
+    const uint32_t byte = scale_byte(quad_max_u32(top_bits<ET>(v[u])));
     *(uint32_t*)(q + (size_t)c * kChunkBytes + l * 4) = quant_eight<ET>(v[u], byte);
     if ((l & 3) == 0) scale[(size_t)c * kChunkScales + (l >> 2)] = (uint8_t)byte;
   }
@@ -207,52 +203,41 @@ __device__ __forceinline__ uint32_t two_scales(uint16_t v) {
 }
 
 // ---------------------------------------------------------------------------
-// A block of eight waves owns 16 channel rows and up to 64 token rows
-// (blockIdx.z of them); each wave takes an eighth of the row's chunks and the
-// eight sums are joined in LDS.  Lane (i, g) reads 32 bytes of a chunk, blocks
-// 2 g and 2 g + 1.
+// The product for few channel rows: bound by latency.  A block of eight waves
+// owns 16 channel rows and up to 64 token rows (blockIdx.z of them); each wave
+// takes an eighth of the row's chunks, asks for BATCH of them at once and
+// multiplies; the eight sums are joined in LDS.  Lane (i, g) reads 32 bytes of a
+// chunk, blocks 2 g and 2 g + 1.
 // ---------------------------------------------------------------------------
+// A block's 16 channel rows of one sequence, and a wave's share of their chunks.
+struct Channels {
+  int j0, n, k0, k1;
+  const uint8_t* w;         // of the lane's row and blocks
+  const uint8_t* ws;
+  __device__ __forceinline__ Channels(const Product& p, int w, int i, int g) {
+    const size_t seq = blockIdx.y;
+    j0 = (int)blockIdx.x * 16;
+    const int j = j0 + i < p.N ? j0 + i : p.N - 1;
+    n = p.n_dev ? p.n_dev[seq] : p.N;
+    int id = p.ids ? p.ids[seq * p.N + j] : j;
+    n = n < p.N ? n : p.N;
+    id = id < 0 || id >= p.V ? 0 : id;               // a hole reads row 0; nobody reads its output
+    const int chunks = p.pitch / kChunkBytes, per = (chunks + 7) / 8;
+    k0 = w * per;
+    k1 = k0 + per < chunks ? k0 + per : chunks;
+    this->w = p.w + (size_t)id * p.pitch + g * 32;
+    ws = p.ws + (size_t)id * (p.pitch / 16) + g * 2;
+  }
+};
+
+// The eight waves' sums of token operand u joined by wave u.  Lane (i, g) holds
+// tokens 4 g .. 4 g + 3 of channel i.
 template <int OT, int NMT>
-__global__ __launch_bounds__(512) void k_mx4_few(Product p) {
-  __shared__ f32x4 sh[8][NMT][NS_WAVE];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
-  const int m0 = (int)blockIdx.z * NMT * 16;         // tokens in groups
-  const size_t seq = blockIdx.y;
-  const int M = p.M - m0, spitch = p.pitch / 16;     // tokens from here on
-  const int j0 = (int)blockIdx.x * 16, j = j0 + i < p.N ? j0 + i : p.N - 1;
-  int n = p.n_dev ? p.n_dev[seq] : p.N;
-  int id = p.ids ? p.ids[seq * p.N + j] : j;
-  n = n < p.N ? n : p.N;
-  if (j0 >= n) return;
-  id = id < 0 || id >= p.V ? 0 : id;                 // a hole reads row 0; nobody reads its output
-  const int chunks = p.pitch / kChunkBytes, per = (chunks + 7) / 8;
-  const int k0 = w * per, k1 = k0 + per < chunks ? k0 + per : chunks;
-  const uint8_t* wr = p.w + (size_t)id * p.pitch + g * 32;
-  const uint8_t* wsr = p.ws + (size_t)id * spitch + g * 2;
-  const uint8_t* xr[NMT];
-  const uint8_t* xsr[NMT];
-#pragma unroll
-  for (int u = 0; u < NMT; ++u) {
-    const size_t m = seq * p.M + m0 + (u * 16 + i < M ? u * 16 + i : M - 1);
-    xr[u] = p.x + m * p.pitch + g * 32;
-    xsr[u] = p.xs + m * spitch + g * 2;
-  }
-  f32x4 acc[NMT] = {};
-  for (int k = k0; k < k1; ++k) {
-    const i32x4 a0 = *(const i32x4*)(wr + (size_t)k * kChunkBytes), a1 = *(const i32x4*)(wr + (size_t)k * kChunkBytes + 16);
-    const uint32_t sa = *(const uint16_t*)(wsr + k * kChunkScales);
-#pragma unroll
-    for (int u = 0; u < NMT; ++u) {
-      const i32x4 b0 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes), b1 = *(const i32x4*)(xr[u] + (size_t)k * kChunkBytes + 16);
-      const uint32_t sb = *(const uint16_t*)(xsr[u] + k * kChunkScales);
-      acc[u] = product128<0>(b0, a0, acc[u], sb, sa);
-      acc[u] = product128<1>(b1, a1, acc[u], sb, sa);
-    }
-  }
+__device__ __forceinline__ void join_waves(const Product& p, f32x4 (&sh)[8][NMT][NS_WAVE], const f32x4 (&acc)[NMT], int w, int lane,
+                                           const Channels& c, size_t row0, int M) {
 #pragma unroll
   for (int u = 0; u < NMT; ++u) sh[w][u][lane] = acc[u];
   __syncthreads();
-  // wave u joins token operand u; lane (i, g) holds tokens 4 g .. 4 g + 3 of channel i
 #pragma unroll
   for (int u = 0; u < NMT; ++u) {
     if (u != w) continue;
@@ -261,11 +246,116 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
     for (int q = 1; q < 8; ++q) s += sh[q][u][lane];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int m = u * 16 + g * 4 + r;
-      if (m < M && j0 + i < n)
-        store_out<OT>(p.out, (seq * p.M + m0 + m) * (size_t)p.sm + (size_t)(j0 + i) * (size_t)p.sn, s[r]);
+      const int m = u * 16 + (lane >> 4) * 4 + r, j = c.j0 + (lane & 15);
+      if (m < M && j < c.n) store_out<OT>(p.out, (row0 + m) * (size_t)p.sm + (size_t)j * (size_t)p.sn, s[r]);
     }
   }
+}
+
+template <int OT, int NMT>
+__global__ __launch_bounds__(512) void k_mx4_few(Product p) {
+  constexpr int BATCH = NMT <= 2 ? 4 : 2;            // chunks of a row in flight
+  __shared__ f32x4 sh[8][NMT][NS_WAVE];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int m0 = (int)blockIdx.z * NMT * 16, M = p.M - m0, spitch = p.pitch / 16;   // tokens in groups; from here on
+  const size_t row0 = (size_t)blockIdx.y * p.M + m0;
+  const Channels c(p, w, i, g);
+  if (c.j0 >= c.n) return;
+  const uint8_t* xr[NMT];
+  const uint8_t* xsr[NMT];
+#pragma unroll
+  for (int u = 0; u < NMT; ++u) {
+    const size_t m = row0 + (u * 16 + i < M ? u * 16 + i : M - 1);
+    xr[u] = p.x + m * p.pitch + g * 32;
+    xsr[u] = p.xs + m * spitch + g * 2;
+  }
+  f32x4 acc[NMT] = {};
+  for (int k = c.k0; k < c.k1; k += BATCH) {
+    i32x4 a[BATCH][2], b[BATCH][NMT][2];
+    uint32_t sa[BATCH], sb[BATCH][NMT];
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q) {
+      const int at = k + q < c.k1 ? k + q : c.k0;
+      a[q][0] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes);
+      a[q][1] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes + 16);
+      sa[q] = *(const uint16_t*)(c.ws + at * kChunkScales);
+#pragma unroll
+      for (int u = 0; u < NMT; ++u) {
+        b[q][u][0] = *(const i32x4*)(xr[u] + (size_t)at * kChunkBytes);
+        b[q][u][1] = *(const i32x4*)(xr[u] + (size_t)at * kChunkBytes + 16);
+        sb[q][u] = *(const uint16_t*)(xsr[u] + at * kChunkScales);
+      }
+    }
+    NS_ISSUE_FENCE();
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q)
+      if (k + q < c.k1) {                            // uniform over the wave
+#pragma unroll
+        for (int u = 0; u < NMT; ++u) {
+          acc[u] = product128<0>(b[q][u][0], a[q][0], acc[u], sb[q][u], sa[q]);
+          acc[u] = product128<1>(b[q][u][1], a[q][1], acc[u], sb[q][u], sa[q]);
+        }
+      }
+  }
+  join_waves<OT>(p, sh, acc, w, lane, c, row0, M);
+}
+
+// ---------------------------------------------------------------------------
+// The head over few rows with the quantisation of its hidden rows in the same
+// launch, for up to 16 of them: a lane's 64 elements of a chunk are two whole
+// blocks, so each wave quantises what it multiplies, without a word to another.
+// ---------------------------------------------------------------------------
+// 32 consecutive elements, a block, in four eights: their codes, and the scale byte.
+template <int ET>
+__device__ __forceinline__ uint32_t quant_block(const Eight<ET> (&v)[4], i32x4& codes) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t t = top_bits<ET>(v[e]);
+    top = t > top ? t : top;
+  }
+  const uint32_t byte = scale_byte(top);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) codes[e] = (int)quant_eight<ET>(v[e], byte);
+  return byte;
+}
+
+template <int ET>
+__global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __restrict__ h, int d) {
+  constexpr int BATCH = ET == NS_FP32 ? 1 : 2;
+  __shared__ f32x4 sh[8][1][NS_WAVE];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const size_t row0 = (size_t)blockIdx.y * p.M;
+  const char* hr = (const char*)h + (row0 + (i < p.M ? i : p.M - 1)) * (size_t)d * (ET == NS_FP32 ? 4 : 2);
+  const int tail = d & ~(ET == NS_FP32 ? 3 : 7);
+  const u32x4 rest = Eight<ET>::rest_of(hr, tail, d);
+  const Channels c(p, w, i, g);
+  if (c.j0 >= c.n) return;
+  f32x4 acc[1] = {};
+  for (int k = c.k0; k < c.k1; k += BATCH) {
+    i32x4 a[BATCH][2];
+    uint32_t sa[BATCH];
+    Eight<ET> v[BATCH][2][4];
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q) {
+      const int at = k + q < c.k1 ? k + q : c.k0;
+      a[q][0] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes);
+      a[q][1] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes + 16);
+      sa[q] = *(const uint16_t*)(c.ws + at * kChunkScales);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[q][e >> 2][e & 3].load(hr, at * kChunk + g * 64 + e * 8, 4, tail, rest);
+    }
+    NS_ISSUE_FENCE();
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q)
+      if (k + q < c.k1) {                            // uniform over the wave
+        i32x4 b0, b1;
+        const uint32_t s0 = quant_block<ET>(v[q][0], b0), s1 = quant_block<ET>(v[q][1], b1);
+        acc[0] = product128<0>(b0, a[q][0], acc[0], s0, sa[q]);
+        acc[0] = product128<1>(b1, a[q][1], acc[0], s1 << 8, sa[q]);
+      }
+  }
+  join_waves<NS_FP32>(p, sh, acc, w, lane, c, row0, p.M);
 }
 
 // ---------------------------------------------------------------------------
@@ -748,7 +838,7 @@ void launch_product(const Product& p, hipStream_t stream) {
       if (p.M <= 16) launch_stream<OT, 1, 8, 7>(p, stream);
       else if (p.M <= 32) launch_stream<OT, 2, 8, 7>(p, stream);
       else if (p.M <= 48) launch_stream<OT, 3, 8, 7>(p, stream);
-      else launch_stream<OT, 4, 8, 6>(p, stream);
+      else launch_stream<OT, 4, 8, 7>(p, stream);
     } else {
       if (p.M <= 16) launch_stream<OT, 1, 16, 7>(p, stream);
       else if (p.M <= 32) launch_stream<OT, 2, 16, 6>(p, stream);
@@ -790,7 +880,7 @@ void launch_head(const Product& p, int B, int d, hipStream_t stream) {
     if (p.M <= 16) launch_head_stream<1, 8, 7>(p, B, stream);
     else if (p.M <= 32) launch_head_stream<2, 8, 7>(p, B, stream);
     else if (p.M <= 48) launch_head_stream<3, 8, 7>(p, B, stream);
-    else launch_head_stream<4, 8, 6>(p, B, stream);
+    else launch_head_stream<4, 8, 7>(p, B, stream);
   } else {
     if (p.M <= 16) launch_head_stream<1, 16, 6>(p, B, stream);
     else if (p.M <= 32) launch_head_stream<2, 16, 5>(p, B, stream);
@@ -906,10 +996,18 @@ int nanospec_mx4_logits_topk(const uint8_t* wq, const uint8_t* wscale, const int
   uint8_t* hq = (uint8_t*)(base + l.q);
   uint8_t* hs = (uint8_t*)(base + l.scale);
   float* z = (float*)(base + l.z);
-  int rc = mx4_rows(h, d, B * M, d, dtype, hq, hs, stream);
-  if (rc != NS_OK) return rc;
   const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
-  launch_head(p, B, d, stream);
+  int rc;
+  if (M <= 16 && few_rows(B, n_max, V, d)) {
+    const dim3 grid((unsigned)((n_max + 15) / 16), (unsigned)B), block(512);
+    if (dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_head_few<NS_BF16>, grid, block, 0, stream, p, h, d);
+    else if (dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_head_few<NS_FP16>, grid, block, 0, stream, p, h, d);
+    else hipLaunchKernelGGL(k_mx4_head_few<NS_FP32>, grid, block, 0, stream, p, h, d);
+  } else {
+    rc = mx4_rows(h, d, B * M, d, dtype, hq, hs, stream);
+    if (rc != NS_OK) return rc;
+    launch_head(p, B, d, stream);
+  }
   rc = ns_launch_status();
   if (rc != NS_OK) return rc;
   const Top t{z, l.ld, row_ids, n_dev, n_max, V, M, k, logits, topk_ids, topk_vals, (uint64_t*)(base + l.cand)};

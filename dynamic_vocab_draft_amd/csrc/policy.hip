@@ -291,6 +291,10 @@ __global__ __launch_bounds__(T) void k_policy_row(Args a) {
   };
   int row = next_row((int)blockIdx.x);
   if (row >= a.L) return;
+  // Blocks that run for long start up to 10 us apart: in step they would all ask
+  // for memory at once and all compute at once (4096 x 128256 bf16 440 -> 422 us).
+  if ((int)gridDim.x * 8 <= a.L)
+    for (int i = (int)(blockIdx.x >> 3 & 7); i > 0; --i) __builtin_amdgcn_s_sleep(48);
   u32x4 x[U];
   {
     const Row z(a.z, (size_t)row, a.ld, ESZ, nvec);
@@ -638,8 +642,11 @@ int parts_of(int L, int V, int dtype) {
   return s;
 }
 
-// From this many rows on a block takes one and reads it once.
-constexpr int kWholeRows = 256;
+// From this many rows on a block takes one and reads it once; fewer are split over
+// the chip (with gradient, in parts and whole: 32 x 128256 bf16 16.8 and 25.3 us, 64 x
+// 50257 float32 17.0 and 19.2, 129 x 50257 23.4 and 20.9, 256 x 128256 bf16 41.7 and
+// 33.1; the loss alone, 129 x 128256 bf16, 19.1 and 17.1).
+constexpr int kWholeRows = 96;
 
 template <int ET, int T, int U>
 void launch_row(const Args& a, hipStream_t stream) {

@@ -705,12 +705,21 @@ def nanospec_mx4_pitch(d: int) -> int:
     return _lib.nanospec_mx4_pitch(d)
 
 
-def _mx4(q, scale, where: str, names: str, rows: int, d: int, dev: int):
+_pitches = {}                                             # of the row lengths seen, a call into the library each
+
+
+def _mx4(q, scale, where: str, rows: int, d: int, dev: int, q_name: str = "q", scale_name: str = "scale"):
     """The addresses of 4-bit rows and their scales."""
-    pitch = _lib.nanospec_mx4_pitch(d)
-    name = names.split()
-    return (_tensor(q, where, name[0], _UINT8, (rows, pitch), dev),
-            _tensor(scale, where, name[1], _UINT8, (rows, pitch // 16), dev))
+    pitch = _pitches.get(d)
+    if pitch is None:
+        pitch = _pitches[d] = _lib.nanospec_mx4_pitch(d)
+    if not (isinstance(q, torch.Tensor) and q.get_device() == dev >= 0 and q.dtype is _UINT8
+            and q.shape == (rows, pitch) and q.is_contiguous()):
+        _misfit(q, where, q_name, (_UINT8,), (rows, pitch), dev)
+    if not (isinstance(scale, torch.Tensor) and scale.get_device() == dev and scale.dtype is _UINT8
+            and scale.shape == (rows, pitch >> 4) and scale.is_contiguous()):
+        _misfit(scale, where, scale_name, (_UINT8,), (rows, pitch >> 4), dev)
+    return q.data_ptr(), scale.data_ptr()
 
 
 def nanospec_mx4_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
@@ -718,7 +727,7 @@ def nanospec_mx4_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, str
     where = "nanospec_mx4_rows"
     R, d, ld, code, dev = _matrix(x, where, "x")
     _launch(where, _lib.nanospec_mx4_rows, dev, stream, x.data_ptr(), ld, R, d, code,
-            *_mx4(q, scale, where, "q scale", R, d, dev))
+            *_mx4(q, scale, where, R, d, dev))
 
 
 def nanospec_mx4_gather_rows(q: torch.Tensor, scale: torch.Tensor, ids: Optional[torch.Tensor],
@@ -729,7 +738,7 @@ def nanospec_mx4_gather_rows(q: torch.Tensor, scale: torch.Tensor, ids: Optional
     n, d, ld, code, dev = _matrix(out, where, "out")
     _want(isinstance(q, torch.Tensor) and q.dim() == 2, where, "q is no [V, pitch] tensor")
     V = q.shape[0]
-    _launch(where, _lib.nanospec_mx4_gather_rows, dev, stream, *_mx4(q, scale, where, "q scale", V, d, dev), V, d,
+    _launch(where, _lib.nanospec_mx4_gather_rows, dev, stream, *_mx4(q, scale, where, V, d, dev), V, d,
             None if ids is None else _tensor(ids, where, "ids", _INT32, (n,), dev),
             None if n_dev is None else _tensor(n_dev, where, "n_dev", _INT32, (1,), dev), n, out.data_ptr(), ld, code)
 
@@ -740,8 +749,9 @@ def nanospec_mx4_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws
     row stride)."""
     where = "nanospec_mx4_matmul"
     M, N, ld, code, dev = _matrix(out, where, "out")
-    x, w = _mx4(xq, xs, where, "xq xs", M, d, dev), _mx4(wq, ws, where, "wq ws", N, d, dev)
-    _launch(where, _lib.nanospec_mx4_matmul, dev, stream, *x, M, *w, N, d, out.data_ptr(), ld, code)
+    x, x_scale = _mx4(xq, xs, where, M, d, dev, "xq", "xs")
+    w, w_scale = _mx4(wq, ws, where, N, d, dev, "wq", "ws")
+    _launch(where, _lib.nanospec_mx4_matmul, dev, stream, x, x_scale, M, w, w_scale, N, d, out.data_ptr(), ld, code)
 
 
 def nanospec_mx4_logits_workspace_bytes(B: int, n_max: int, M: int, k: int, d: int) -> int:
@@ -765,7 +775,7 @@ def nanospec_mx4_logits_topk(wq: torch.Tensor, wscale: torch.Tensor, row_ids: Op
     if row_ids is not None:
         _want(isinstance(row_ids, torch.Tensor) and row_ids.dim() == 2, where, "row_ids is no [B, n_max] tensor")
         n_max = row_ids.shape[1]
-    _launch(where, _lib.nanospec_mx4_logits_topk, dev, stream, *_mx4(wq, wscale, where, "wq wscale", V, d, dev),
+    _launch(where, _lib.nanospec_mx4_logits_topk, dev, stream, *_mx4(wq, wscale, where, V, d, dev, "wq", "wscale"),
             None if row_ids is None else _tensor(row_ids, where, "row_ids", _INT32, (B, n_max), dev),
             None if n_dev is None else _tensor(n_dev, where, "n_dev", _INT32, (B,), dev), n_max, B, V, d,
             h.data_ptr(), _FLOATS[h.dtype], M, k,
@@ -855,16 +865,23 @@ def nanospec_policy_loss(logits: torch.Tensor, inv_temp: float, tokens: torch.Te
         if code_d != code:
             _want(False, where, f"dlogits has dtype {dlogits.dtype}, not {logits.dtype}", NS_EDTYPE)
     shape = (L,)
+    if not (isinstance(tokens, torch.Tensor) and tokens.get_device() == dev and tokens.dtype is _INT32
+            and tokens.shape == shape and tokens.is_contiguous()):
+        _misfit(tokens, where, "tokens", (_INT32,), shape, dev)
+    at = []                                               # a loop: a call a tensor would take twice as long
+    for t in (old_logprob, ref_logprob, advantage, weight, logprob, kl, entropy):
+        if t is None:
+            at.append(None)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is _F32 and t.shape == shape
+                and t.is_contiguous()):
+            names = ("old_logprob", "ref_logprob", "advantage", "weight", "logprob", "kl", "entropy")
+            _misfit(t, where, names[len(at)], (_F32,), shape, dev)
+        at.append(t.data_ptr())
+    old, ref, adv, wgt, lp, kl_at, ent = at
     _launch(where, _lib.nanospec_policy_loss, dev, stream, logits.data_ptr(), ld, L, V, code, inv_temp,
-            _tensor(tokens, where, "tokens", _INT32, shape, dev),
-            _tensor(old_logprob, where, "old_logprob", _F32, shape, dev),
-            None if ref_logprob is None else _tensor(ref_logprob, where, "ref_logprob", _F32, shape, dev),
-            _tensor(advantage, where, "advantage", _F32, shape, dev),
-            None if weight is None else _tensor(weight, where, "weight", _F32, shape, dev),
-            eps_low, eps_high, kl_coef, ent_coef, _tensor(loss, where, "loss", _F32, (1,), dev),
-            _tensor(logprob, where, "logprob", _F32, shape, dev),
-            None if kl is None else _tensor(kl, where, "kl", _F32, shape, dev),
-            None if entropy is None else _tensor(entropy, where, "entropy", _F32, shape, dev),
+            tokens.data_ptr(), old, ref, adv, wgt, eps_low, eps_high, kl_coef, ent_coef,
+            _tensor(loss, where, "loss", _F32, (1,), dev), lp, kl_at, ent,
             None if g_loss is None else _tensor(g_loss, where, "g_loss", _F32, (1,), dev),
             None if dlogits is None else dlogits.data_ptr(), ld_d, *_workspace(work, where, dev))
 

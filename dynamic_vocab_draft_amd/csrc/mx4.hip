@@ -31,11 +31,15 @@ __host__ __device__ constexpr int chunks_of(int d) { return (d + kChunk - 1) / k
 __host__ __device__ constexpr int pitch_of(int d) { return chunks_of(d) * kChunkBytes; }
 
 // ---------------------------------------------------------------------------
-// Quantisation: one pass.  A lane takes eight elements, four lanes a block, so
-// a row's 256-element chunk is half a wave's.
+// Quantisation: one pass, bound by its bytes (128256 x 4096 bf16 219 us, 6.0 TB/s
+// read and written).  A lane takes eight elements, four lanes a block, so a row's
+// 256-element chunk is half a wave's.  Of float32 a lane takes four in each half
+// of the chunk, so that a load of all lanes is one run of the row.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
-constexpr int kRowUnits = 4;                       // chunks of a half wave
+// Chunks of a half wave: many where there are enough to fill the chip, else one,
+// whose blocks are more and end sooner.
+constexpr int kManyUnits = 8, kManyChunks = 1 << 17;
 
 // c / d for c < 2^26 and d <= 64, from 2^32 / d rounded up: the product is over
 // by less than c d / 2^32 < 1 / d.  0 stands for 2^32.
@@ -47,6 +51,13 @@ __device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
   uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);    // quad_perm 1 0 3 2
   v = o > v ? o : v;
   o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);             // quad_perm 2 3 0 1
+  return o > v ? o : v;
+}
+
+// The largest value of eight lanes.
+__device__ __forceinline__ uint32_t oct_max_u32(uint32_t v) {
+  v = quad_max_u32(v);
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);   // row_half_mirror
   return o > v ? o : v;
 }
 
@@ -82,40 +93,65 @@ __device__ __forceinline__ uint32_t top_bits(const Eight<ET>& x) {
   return __float_as_uint(ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b));
 }
 
-template <int ET>
+template <int ET, int UNITS>
 __global__ __launch_bounds__(kRowThreads) void k_mx4_rows(const void* __restrict__ x, int64_t ld, int R, int d,
                                                           uint32_t rcp, uint8_t* __restrict__ q,
                                                           uint8_t* __restrict__ scale) {
   const int per_row = chunks_of(d), total = R * per_row;   // below 2^26
-  const int l = threadIdx.x & 31, c0 = (int)blockIdx.x * (kRowThreads / 32 * kRowUnits) + (threadIdx.x >> 5);
+  const int l = threadIdx.x & 31, c0 = (int)blockIdx.x * (kRowThreads / 32 * UNITS) + (threadIdx.x >> 5);
   const int tail = d & ~(ET == NS_FP32 ? 3 : 7);
-  Eight<ET> v[kRowUnits];
+  Eight<ET> v[UNITS];
 #pragma unroll
-  for (int u = 0; u < kRowUnits; ++u) {
+  for (int u = 0; u < UNITS; ++u) {
     const int c = c0 + u * (kRowThreads / 32), cc = c < total ? c : total - 1;
     const int r = (int)divided((uint32_t)cc, rcp);
     const char* row = (const char*)x + (size_t)r * (size_t)ld * (ET == NS_FP32 ? 4 : 2);
-    v[u].load(row, (cc - r * per_row) * kChunk + l * 8, 4, tail, Eight<ET>::rest_of(row, tail, d));
+    v[u].load(row, (cc - r * per_row) * kChunk + l * (ET == NS_FP32 ? 4 : 8), kChunk / 2, tail, Eight<ET>::rest_of(row, tail, d));
   }
   NS_ISSUE_FENCE();
 #pragma unroll
-  for (int u = 0; u < kRowUnits; ++u) {
+  for (int u = 0; u < UNITS; ++u) {
     const int c = c0 + u * (kRowThreads / 32);
     if (c >= total) continue;                      // whole half waves
-    const uint32_t byte = scale_byte(quad_max_u32(top_bits<ET>(v[u])));
-    *(uint32_t*)(q + (size_t)c * kChunkBytes + l * 4) = quant_eight<ET>(v[u], byte);
-    if ((l & 3) == 0) scale[(size_t)c * kChunkScales + (l >> 2)] = (uint8_t)byte;
+    uint8_t* to = q + (size_t)c * kChunkBytes;
+    if constexpr (ET == NS_FP32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t t = v[u].v[h][e] & 0x7FFFFFFFu;
+          top = t > top ? t : top;
+        }
+        const uint32_t byte = scale_byte(oct_max_u32(top));
+        const float f = scale_value(byte);
+        uint32_t r = 0;
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[u].get(4 * h), v[u].get(4 * h + 1), f, 0);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[u].get(4 * h + 2), v[u].get(4 * h + 3), f, 1);
+        *(uint16_t*)(to + h * (kChunkBytes / 2) + l * 2) = byte == 255 ? (uint16_t)0 : (uint16_t)r;
+        if ((l & 7) == 0) scale[(size_t)c * kChunkScales + h * (kChunkScales / 2) + (l >> 3)] = (uint8_t)byte;
+      }
+    } else {
+      const uint32_t byte = scale_byte(quad_max_u32(top_bits<ET>(v[u])));
+      *(uint32_t*)(to + l * 4) = quant_eight<ET>(v[u], byte);
+      if ((l & 3) == 0) scale[(size_t)c * kChunkScales + (l >> 2)] = (uint8_t)byte;
+    }
   }
 }
 
-int mx4_rows(const void* x, int64_t ld, int R, int d, int dtype, uint8_t* q, uint8_t* scale, hipStream_t stream) {
-  constexpr int per_block = kRowThreads / 32 * kRowUnits;
-  const int total = R * chunks_of(d);
+template <int ET>
+void launch_rows(const void* x, int64_t ld, int R, int d, uint8_t* q, uint8_t* scale, hipStream_t stream) {
+  const int total = R * chunks_of(d), groups = kRowThreads / 32;
   const uint32_t rcp = reciprocal_of((uint32_t)chunks_of(d));
-  const dim3 grid((unsigned)((total + per_block - 1) / per_block)), block(kRowThreads);
-  if (dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_rows<NS_BF16>, grid, block, 0, stream, x, ld, R, d, rcp, q, scale);
-  else if (dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_rows<NS_FP16>, grid, block, 0, stream, x, ld, R, d, rcp, q, scale);
-  else hipLaunchKernelGGL(k_mx4_rows<NS_FP32>, grid, block, 0, stream, x, ld, R, d, rcp, q, scale);
+  const auto blocks = [&](int units) { return dim3((unsigned)((total + groups * units - 1) / (groups * units))); };
+  if (total >= kManyChunks) hipLaunchKernelGGL((k_mx4_rows<ET, kManyUnits>), blocks(kManyUnits), dim3(kRowThreads), 0, stream, x, ld, R, d, rcp, q, scale);
+  else hipLaunchKernelGGL((k_mx4_rows<ET, 1>), blocks(1), dim3(kRowThreads), 0, stream, x, ld, R, d, rcp, q, scale);
+}
+
+int mx4_rows(const void* x, int64_t ld, int R, int d, int dtype, uint8_t* q, uint8_t* scale, hipStream_t stream) {
+  if (dtype == NS_BF16) launch_rows<NS_BF16>(x, ld, R, d, q, scale, stream);
+  else if (dtype == NS_FP16) launch_rows<NS_FP16>(x, ld, R, d, q, scale, stream);
+  else launch_rows<NS_FP32>(x, ld, R, d, q, scale, stream);
   return ns_launch_status();
 }
 
@@ -135,39 +171,87 @@ __device__ __forceinline__ void values_of(uint32_t codes, uint32_t byte, float (
   }
 }
 
-template <int OT>
+// A lane takes eight elements, of float32 four in each half of the chunk, so that
+// a store of all lanes is one run of the row.  Nobody reads the outputs soon:
+// stores past the caches (128256 x 4096 bf16 294 -> 217 us, 6.1 TB/s).
+template <int OT, int UNITS>
 __global__ __launch_bounds__(kRowThreads) void k_mx4_gather(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                             int V, int d, uint32_t rcp, const int32_t* __restrict__ ids,
                                                             const int32_t* __restrict__ n_dev, int n_max,
                                                             void* __restrict__ out, int64_t ld) {
+  constexpr bool F32 = OT == NS_FP32;
   const int per_row = chunks_of(d);
   int n = n_dev ? *n_dev : n_max;
   n = n < 0 ? 0 : (n > n_max ? n_max : n);
   const int total = n * per_row;                   // below 2^26
-  const int l = threadIdx.x & 31, c0 = (int)blockIdx.x * (kRowThreads / 32 * kRowUnits) + (threadIdx.x >> 5);
-  uint32_t codes[kRowUnits], byte[kRowUnits];
-  int row[kRowUnits], at[kRowUnits];
+  const int l = threadIdx.x & 31, c0 = (int)blockIdx.x * (kRowThreads / 32 * UNITS) + (threadIdx.x >> 5);
+  uint32_t codes[UNITS], byte[UNITS];              // of float32 two halves in each
+  int row[UNITS], at[UNITS];
 #pragma unroll
-  for (int u = 0; u < kRowUnits; ++u) {
+  for (int u = 0; u < UNITS; ++u) {
     const int c = c0 + u * (kRowThreads / 32);
     row[u] = -1;
     if (c >= total) continue;
     const int j = (int)divided((uint32_t)c, rcp), id = ids ? ids[j] : j;
-    at[u] = c - j * per_row;
+    at[u] = (c - j * per_row) * kChunk;
     if (id < 0 || id >= V) continue;
-    const size_t from = (size_t)id * per_row + at[u];
-    codes[u] = *(const uint32_t*)(q + from * kChunkBytes + l * 4);
-    byte[u] = scale[from * kChunkScales + (l >> 2)];
-    at[u] = at[u] * kChunk + l * 8;
+    const size_t from = (size_t)id * per_row + (c - j * per_row);
+    const uint8_t *f = q + from * kChunkBytes, *b = scale + from * kChunkScales;
+    if (F32) {
+      codes[u] = (uint32_t)__builtin_nontemporal_load((const uint16_t*)(f + l * 2)) |
+                 (uint32_t)__builtin_nontemporal_load((const uint16_t*)(f + kChunkBytes / 2 + l * 2)) << 16;
+      byte[u] = (uint32_t)b[l >> 3] | (uint32_t)b[kChunkScales / 2 + (l >> 3)] << 8;
+    } else {
+      codes[u] = __builtin_nontemporal_load((const uint32_t*)(f + l * 4));
+      byte[u] = b[l >> 2];
+    }
     row[u] = j;
   }
+  NS_ISSUE_FENCE();
 #pragma unroll
-  for (int u = 0; u < kRowUnits; ++u) {
-    if (row[u] < 0 || at[u] >= d) continue;
+  for (int u = 0; u < UNITS; ++u) {
+    if (row[u] < 0) continue;
+    const size_t base = (size_t)row[u] * (size_t)ld;
     float v[8];
-    values_of(codes[u], byte[u], v);
-    store_eight<OT>(out, (size_t)row[u] * (size_t)ld + at[u], v, d - at[u]);
+    if constexpr (F32) {
+      float w[8];
+      values_of(codes[u], byte[u] & 255, v);       // the lower half's four
+      values_of(codes[u], byte[u] >> 8, w);        // and, behind four of no use, the upper's
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = at[u] + h * (kChunk / 2) + l * 4;
+        const float* x = h == 0 ? v : w + 4;
+        float* to = (float*)out + base + i;
+        if (d - i >= 4) {
+          __builtin_nontemporal_store(u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}, (u32x4_any*)to);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < d - i) to[e] = x[e];
+        }
+      }
+    } else {
+      const int i = at[u] + l * 8;
+      if (i >= d) continue;
+      values_of(codes[u], byte[u], v);
+      if (d - i >= 8) {
+        __builtin_nontemporal_store(u32x4{narrow2<OT>(v[0], v[1]), narrow2<OT>(v[2], v[3]), narrow2<OT>(v[4], v[5]), narrow2<OT>(v[6], v[7])},
+                                    (u32x4_any*)((uint16_t*)out + base + i));
+      } else {
+        store_eight<OT>(out, base + i, v, d - i);
+      }
+    }
   }
+}
+
+template <int OT>
+void launch_gather(const uint8_t* q, const uint8_t* scale, int V, int d, const int32_t* ids, const int32_t* n_dev, int n_max, void* out,
+                   int64_t ld, hipStream_t stream) {
+  const int total = n_max * chunks_of(d), groups = kRowThreads / 32;
+  const uint32_t rcp = reciprocal_of((uint32_t)chunks_of(d));
+  const auto blocks = [&](int units) { return dim3((unsigned)((total + groups * units - 1) / (groups * units))); };
+  if (total >= kManyChunks) hipLaunchKernelGGL((k_mx4_gather<OT, kManyUnits>), blocks(kManyUnits), dim3(kRowThreads), 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld);
+  else hipLaunchKernelGGL((k_mx4_gather<OT, 1>), blocks(1), dim3(kRowThreads), 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld);
 }
 
 // ---------------------------------------------------------------------------
@@ -403,21 +487,26 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product
   constexpr int XS = NMT * 16 * ((IDS ? kStreamIdsD : NS_MAX_D) / 32 + 8);   // the tokens' scales, a row's 8 bytes from the next
   __shared__ __attribute__((aligned(16))) char lds[R * STAGE + XS];
   __shared__ int s_id[IDS ? kStreamIds : 1];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int S = p.pitch / kChunkBytes, spitch = S * kChunkScales;
   int live = p.N;
   if (IDS) {
     const size_t seq = blockIdx.y;
-    if (p.n_dev) live = p.n_dev[seq] < 0 ? 0 : (p.n_dev[seq] < p.N ? p.n_dev[seq] : p.N);
+    if (p.n_dev) live = p.n_dev[seq];                  // its latency passes under the scales'
     p.x += seq * p.M * p.pitch;
-    p.xs += seq * p.M * (p.pitch / 16);
+    p.xs += seq * p.M * spitch;
     if (p.ids) p.ids += seq * p.N;
     p.out = (char*)p.out + seq * p.M * (size_t)p.sm * (OT == NS_FP32 ? 4 : 2);
   }
+  char* xs = lds + R * STAGE;
+  for (int r = tid >> 5; r < NMT * 16; r += kStreamWaves * 2)   // eight scales a lane; rows past the end are the last one's
+    for (int c = tid & 31; c < S; c += 32)
+      *(u32x2*)(xs + r * (spitch + 8) + c * 8) = *(const u32x2*)(p.xs + (r < p.M ? r : p.M - 1) * spitch + c * 8);
+  live = live < 0 ? 0 : (live < p.N ? live : p.N);
   const int units = (live + ROWS - 1) / ROWS, per_block = (units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int u0 = (int)blockIdx.x * per_block, u1 = u0 + per_block < units ? u0 + per_block : units;
   const int passes = (u1 - u0 + kStreamWaves - 1) / kStreamWaves;
   if (passes <= 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
-  const int S = p.pitch / kChunkBytes, spitch = S * kChunkScales;
   const uint32_t base = lds_offset(lds);
   const int n0 = u0 * ROWS;                            // the block's first channel row
   const int last = (u1 * ROWS < live ? u1 * ROWS : live) - 1 - n0;
@@ -426,11 +515,6 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product
   const u32x4 rs = IDS ? buffer_of(p.ws, (uint32_t)p.V * spitch)
                        : buffer_of(p.ws + (size_t)n0 * spitch, (uint32_t)(last + 1) * spitch);
   const u32x4 rx = buffer_of(p.x, (uint32_t)(p.M * p.pitch));
-  char* xs = lds + R * STAGE;
-  for (int q = tid; q < NMT * 16 * S; q += kStreamWaves * NS_WAVE) {   // eight scales each; rows past the end are the last one's
-    const int r = q / S, c = q - r * S;
-    *(u32x2*)(xs + r * (spitch + 8) + c * 8) = *(const u32x2*)(p.xs + (r < p.M ? r : p.M - 1) * spitch + c * 8);
-  }
   if (IDS) {                                         // a hole reads row 0; nobody reads its output
     for (int r = tid; r <= last; r += kStreamWaves * NS_WAVE) {
       const int id = p.ids ? p.ids[n0 + r] : n0 + r;
@@ -951,12 +1035,9 @@ int nanospec_mx4_gather_rows(const uint8_t* q, const uint8_t* scale, int32_t V, 
   if (n_max == 0) return NS_OK;
   if (!q || !scale || !out || !rows_aligned(q, scale) || !elem_aligned(out, out_dtype)) return NS_EINVAL;
   (void)hipGetLastError();
-  constexpr int per_block = kRowThreads / 32 * kRowUnits;
-  const uint32_t rcp = reciprocal_of((uint32_t)chunks_of(d));
-  const dim3 grid((unsigned)((n_max * chunks_of(d) + per_block - 1) / per_block)), block(kRowThreads);
-  if (out_dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_gather<NS_BF16>, grid, block, 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld_out);
-  else if (out_dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_gather<NS_FP16>, grid, block, 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld_out);
-  else hipLaunchKernelGGL(k_mx4_gather<NS_FP32>, grid, block, 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld_out);
+  if (out_dtype == NS_BF16) launch_gather<NS_BF16>(q, scale, V, d, ids, n_dev, n_max, out, ld_out, stream);
+  else if (out_dtype == NS_FP16) launch_gather<NS_FP16>(q, scale, V, d, ids, n_dev, n_max, out, ld_out, stream);
+  else launch_gather<NS_FP32>(q, scale, V, d, ids, n_dev, n_max, out, ld_out, stream);
   return ns_launch_status();
 }
 

@@ -470,7 +470,7 @@ __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __r
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8;
 constexpr int kStreamIds = 4096;                   // ids of a block, at most
-constexpr int kStreamIdsD = 8192;                  // d with ids, at most: the tokens' scales and the ids share what LDS is left
+constexpr int kStreamIdsD = 8192;                  // d with ids and over 32 tokens, at most: their scales and the ids share what LDS is left
 
 // The 16-byte block of a chunk at place c of a row: 0 2 4 6 1 3 5 7.
 __device__ __forceinline__ int block_at(int c) { return (c & 3) * 2 + (c >> 2); }
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product
   // stores behind a pass that the waits allow for (vmcnt counts to 63)
   constexpr int STORES = RT * NMT * 4 < 63 - (R - 2) * LW ? RT * NMT * 4 : 63 - (R - 2) * LW;
   static_assert((R - 2) * LW + STORES < 64, "vmcnt range");
-  constexpr int XS = NMT * 16 * ((IDS ? kStreamIdsD : NS_MAX_D) / 32 + 8);   // the tokens' scales, a row's 8 bytes from the next
+  constexpr int XS = NMT * 16 * ((IDS && NMT > 2 ? kStreamIdsD : NS_MAX_D) / 32 + 8);   // the tokens' scales, a row's 8 bytes from the next
   __shared__ __attribute__((aligned(16))) char lds[R * STAGE + XS];
   __shared__ int s_id[IDS ? kStreamIds : 1];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
@@ -905,40 +905,50 @@ void launch_stream(const Product& p, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-// Up to 64 tokens: up to 4096 channels the kernel for few rows, up to 16384 the
-// stream of eight-row units, then taller units.  Products of more tokens take
-// tiles of 256, 128 or 64 of them: blocks take one tile each a round, and the sum
-// over the rounds decides.
+// Up to 64 tokens: up to 4096 channels the kernel for few rows (d = 4096, M = 8:
+// 4096 channels 8.0 us against 8.7 streamed, 6000 11.0 against 8.8; M = 64: 4096 9.4
+// against 11.8, 8000 16.9 against 12.5), then the stream, of eight-row units up
+// to 16384 channels (M = 64, 16000 13.5 against 16.1 with taller units; 60 x 30000 x
+// 3584 20.7 against 18.7) and for up to 16 tokens (M = 8, 30000 15.0 against 17.0,
+// 128256 57.4 against 58.6).
+// More than 64 tokens over few channels go to the kernel for few rows, 64 at a
+// time, up to a block a CU (100 x 2000 x 16384, 250 blocks, 29.8 us against 44.4 in
+// tiles of 64 tokens; 4096 x 64 x 4096, 256 blocks, 10.0 against 14.5; 4096 x 100 x
+// 4096, 448 blocks, 17.8 against 14.9).
+// The rest takes tiles of 256, 128 or 64 tokens.  Blocks take one tile each a
+// round, and a round takes about 28, 21 and 17 us at d = 4096 (256 x 16384, one
+// round each: 27.2, 20.9, 18.3); the sum over the rounds decides (1000 x 8000 x
+// 4096, rounds 1, 1 and 2: 30.1, 25.2, 31.9; 128 x 128256 x 4096, rounds 2, 2 and 4:
+// 75.5, 67.0, 78.6).
 template <int OT>
 void launch_product(const Product& p, hipStream_t stream) {
   const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
                         (OT == NS_FP32 ? 4 : 2);
-  if (p.M <= 64 && (p.N <= 4096 || span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
+  const int64_t few = (int64_t)((p.N + 15) / 16) * ((p.M + 63) / 64);   // blocks of the kernel for few rows
+  if (few <= 256 || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
     launch_few_of<OT>(p, 1, stream);
-    return;
-  }
-  if (p.M <= 64) {
-    if (p.N <= 16384) {
-      if (p.M <= 16) launch_stream<OT, 1, 8, 7>(p, stream);
-      else if (p.M <= 32) launch_stream<OT, 2, 8, 7>(p, stream);
+  } else if (p.M <= 64) {
+    if (p.M <= 16) {
+      launch_stream<OT, 1, 8, 7>(p, stream);
+    } else if (p.N <= 16384) {
+      if (p.M <= 32) launch_stream<OT, 2, 8, 7>(p, stream);
       else if (p.M <= 48) launch_stream<OT, 3, 8, 7>(p, stream);
       else launch_stream<OT, 4, 8, 7>(p, stream);
     } else {
-      if (p.M <= 16) launch_stream<OT, 1, 16, 7>(p, stream);
-      else if (p.M <= 32) launch_stream<OT, 2, 16, 6>(p, stream);
+      if (p.M <= 32) launch_stream<OT, 2, 16, 6>(p, stream);
       else if (p.M <= 48) launch_stream<OT, 3, 32, 3>(p, stream);
       else launch_stream<OT, 4, 32, 3>(p, stream);
     }
-    return;
+  } else {
+    const auto time = [&](int tb, int round) {
+      const int64_t tiles = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.M + tb * 64 - 1) / (tb * 64));
+      return (tiles + 255) / 256 * round;
+    };
+    const int64_t t4 = time(4, 28), t2 = time(2, 21), t1 = time(1, 17);
+    if (t4 <= t2 && t4 <= t1) launch_tiled<OT, 4>(p, stream);
+    else if (t2 <= t1) launch_tiled<OT, 2>(p, stream);
+    else launch_tiled<OT, 1>(p, stream);
   }
-  const auto time = [&](int tb, int round) {
-    const int64_t tiles = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.M + tb * 64 - 1) / (tb * 64));
-    return (tiles + 255) / 256 * round;
-  };
-  const int64_t t4 = time(4, 21), t2 = time(2, 15), t1 = time(1, 11);
-  if (t4 <= t2 && t4 <= t1) launch_tiled<OT, 4>(p, stream);
-  else if (t2 <= t1) launch_tiled<OT, 2>(p, stream);
-  else launch_tiled<OT, 1>(p, stream);
 }
 
 template <int NMT, int ROWS, int R>
@@ -951,23 +961,33 @@ void launch_head_stream(const Product& p, int B, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-// The head's logits, B sequences.  The stream's 32-bit row addresses reach 4 GB.
-bool few_rows(int B, int n_max, int V, int d) {
-  return (int64_t)B * n_max < 8192 || d > kStreamIdsD || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
+// The head's logits, B sequences.  Whole calls (d = 4096), the kernel for few rows
+// against the stream: M = 8, 4000 rows 16.8 against 17.1 us, 8000 20.2 against 18.8;
+// M = 64, 4000 rows 16.8 against 20.2, 8000 26.6 against 23.0; 64 sequences of 100
+// rows, M = 8, 21.2 against 19.4.  Eight-row units against taller ones: M = 64,
+// 15500 rows 24.6 against 27.5, 100000 81.1 against 68.8; M = 8, 100000 59.5 against
+// 60.7.  The stream's 32-bit row addresses reach 4 GB.
+bool few_rows(int B, int n_max, int V, int M, int d) {
+  return (int64_t)B * n_max <= 4096 || (M > 32 && d > kStreamIdsD) || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
 }
 
+// Whether the kernel for few rows also quantises (M = 8, 1000 rows 13.6 us against
+// 16.9, 4000 13.8 against 16.8; M = 16, 1000 14.1 against 16.5).  A block's waves
+// quantise the same rows as the next block's, which pays up to a block a CU and for
+// rows of up to 4096 elements (M = 16, 4 x 1000 rows of 8192: 28.0 against 16.0).
+bool fuses_rows(int B, int n_max, int M, int d) { return M <= 16 && (int64_t)B * n_max <= 4096 && d <= 4096; }
+
 void launch_head(const Product& p, int B, int d, hipStream_t stream) {
-  const int64_t rows = (int64_t)B * p.N;
-  if (few_rows(B, p.N, p.V, d)) {
+  if (few_rows(B, p.N, p.V, p.M, d)) {
     launch_few_of<NS_FP32>(p, B, stream);
-  } else if (rows <= 65536) {
-    if (p.M <= 16) launch_head_stream<1, 8, 7>(p, B, stream);
-    else if (p.M <= 32) launch_head_stream<2, 8, 7>(p, B, stream);
+  } else if (p.M <= 16) {
+    launch_head_stream<1, 8, 7>(p, B, stream);
+  } else if ((int64_t)B * p.N <= 16384) {
+    if (p.M <= 32) launch_head_stream<2, 8, 7>(p, B, stream);
     else if (p.M <= 48) launch_head_stream<3, 8, 7>(p, B, stream);
     else launch_head_stream<4, 8, 7>(p, B, stream);
   } else {
-    if (p.M <= 16) launch_head_stream<1, 16, 6>(p, B, stream);
-    else if (p.M <= 32) launch_head_stream<2, 16, 5>(p, B, stream);
+    if (p.M <= 32) launch_head_stream<2, 16, 5>(p, B, stream);
     else if (p.M <= 48) launch_head_stream<3, 32, 3>(p, B, stream);
     else launch_head_stream<4, 32, 3>(p, B, stream);
   }
@@ -1079,7 +1099,7 @@ int nanospec_mx4_logits_topk(const uint8_t* wq, const uint8_t* wscale, const int
   float* z = (float*)(base + l.z);
   const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
   int rc;
-  if (M <= 16 && few_rows(B, n_max, V, d)) {
+  if (fuses_rows(B, n_max, M, d)) {
     const dim3 grid((unsigned)((n_max + 15) / 16), (unsigned)B), block(512);
     if (dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_head_few<NS_BF16>, grid, block, 0, stream, p, h, d);
     else if (dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_head_few<NS_FP16>, grid, block, 0, stream, p, h, d);

@@ -193,6 +193,11 @@ def exact_in_float32(a, b, total):
         v = blocks(v)
         return np.min(np.where(v == 0, np.inf, np.ldexp(1.0, np.frexp(v)[1] - 2)), axis=2)
     ua, ub = units(a), units(b)
+    with np.errstate(all="ignore"):
+        unit = ua.min(1)[:, None] * ub.min(1)
+        sure = (total == 0) | (total < 2.0 ** 24 * unit)
+    if sure.all():
+        return sure
     unit = np.full(total.shape, np.inf)
     for k in range(ua.shape[1]):
         np.minimum(unit, ua[:, k, None] * ub[:, k], out=unit)
@@ -319,11 +324,15 @@ def check_head(ns, B, M, k, n_max, V, d, dtype, live=None, holes=0, all_rows=Fal
         ok = np.flatnonzero((ids[b, :nb] >= 0) & (ids[b, :nb] < V))
         rows = w[ids[b, ok]]
         want, total = x @ rows.T, np.abs(x) @ np.abs(rows).T
-        if len(ok):
-            assert exact_in_float32(x, rows, total).all()
+        sure = exact_in_float32(x, rows, total) if len(ok) else np.ones(want.shape, bool)
+        assert logits or sure.all()
         if logits:
             got = z[b].cpu().numpy()
-            assert np.array_equal(got[:, ok], want.astype(np.float32)), b
+            assert np.array_equal(got[:, ok][sure], want.astype(np.float32)[sure]), b
+            assert sure.size == 0 or sure.mean() > 0.9
+            bound = (2 * -(-d // 256) + 8) * 2.0 ** -22 * total + 2.0 ** -24 * np.abs(want)
+            assert (np.abs(got[:, ok] - want) <= bound).all()
+            want = np.where(sure, want, got[:, ok])        # the selection is held to the logits as they are
             rest = np.setdiff1d(np.arange(n_max), ok)
             assert (got[:, rest] == 77).all(), "columns that are no rows"
         ri, rv = best_of(want.astype(np.float32), ids[b, ok], k)

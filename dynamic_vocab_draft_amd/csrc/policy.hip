@@ -392,13 +392,14 @@ __global__ __launch_bounds__(T) void k_policy_row(Args a) {
   }
 }
 
-// Many rows without a gradient: a block of four waves streams a row, two batches
-// a wave in flight.
-constexpr int kStreamThreads = 256;
-
-template <int ET>
-__global__ __launch_bounds__(kStreamThreads) void k_policy_stream(Args a) {
-  constexpr int EPV = per_vec(ET), NW = kStreamThreads / NS_WAVE, STEP = NS_WAVE * kUnroll;
+// Many rows without a gradient: a block streams a row, two batches a wave in flight.
+// Eight waves for long rows, so that blocks end early and rows that are left out
+// leave no CU behind (2048 x 151936 fp16, half of them left out, 71 us with four
+// waves, 64 with eight, 82 with 16), one for short ones (20000 x 2000 bf16 37 us
+// with four, 67 with eight).
+template <int ET, int T>
+__global__ __launch_bounds__(T) void k_policy_stream(Args a) {
+  constexpr int EPV = per_vec(ET), NW = T / NS_WAVE, STEP = NS_WAVE * kUnroll;
   __shared__ Stat sh[NW];
   const size_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1), wv = tid / NS_WAVE;
@@ -442,11 +443,13 @@ __global__ __launch_bounds__(kStreamThreads) void k_policy_stream(Args a) {
     const int e = nvec * EPV + lane;
     st = join(st, stat_of_lanes(e < a.V ? one_elem<ET>(zrow, e) : -INFINITY, a.c), a.c);
   }
-  if (lane == 0) sh[wv] = st;
-  __syncthreads();
-  if (wv != 0) return;
+  if (NW > 1) {
+    if (lane == 0) sh[wv] = st;
+    __syncthreads();
+    if (wv != 0) return;
 #pragma unroll
-  for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
+    for (int i = 1; i < NW; ++i) st = join(st, sh[i], a.c);
+  }
   finish(a, row, st, ztok, given, lane == 0);
 }
 
@@ -659,7 +662,10 @@ template <int ET>
 int launch_policy(Args a, float* loss, hipStream_t stream) {
   const int nvec = a.V / per_vec(ET);
   if (a.L >= kWholeRows && !a.dz) {
-    hipLaunchKernelGGL(k_policy_stream<ET>, dim3((unsigned)a.L), dim3(kStreamThreads), 0, stream, a);
+    const dim3 grid((unsigned)a.L);
+    if (nvec <= 512) hipLaunchKernelGGL((k_policy_stream<ET, 64>), grid, dim3(64), 0, stream, a);
+    else if (nvec <= 4096) hipLaunchKernelGGL((k_policy_stream<ET, 256>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_policy_stream<ET, 512>), grid, dim3(512), 0, stream, a);
     a.S = 1;
   } else if (a.L >= kWholeRows) {
     if (nvec <= 64 * 4) launch_row<ET, 64, 4>(a, stream);

@@ -333,3 +333,24 @@ def test_agrees_with_token_logprobs(ns):
     ns.nanospec_token_logprobs_grad(z, 1.0, tok[:, None].contiguous(), lse, H, -torch.ones((L, 1), device="cuda"), None, None, dz2)
     assert abs(loss.item() + L) < 1e-4 and torch.allclose(lp2, lp[:, 0], rtol=0, atol=2e-6) and torch.allclose(H, H2, rtol=0, atol=2e-5)
     assert torch.allclose(dz, dz2, rtol=2e-5, atol=2e-6)
+
+
+# forms taken by size: rows in parts or whole, blocks of one, four and eight waves, a row a block or many, rows longer than
+# a block's registers, every third row left out
+@pytest.mark.parametrize("c", [(95, 3000, "bf16"), (96, 3000, "bf16"), (120, 2000, "fp32"), (130, 9000, "fp16"), (100, 20000, "fp32"), (97, 40000, "fp32"),
+                               (100, 66000, "bf16"), (260, 70001, "fp32"), (2100, 66001, "bf16"), (270, 131073, "bf16"), (3000, 300, "fp32"), (700, 4099, "fp16")],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_forms_by_size(ns, c):
+    case = Case(*c)
+    case.weight[::3] = 0
+    case.weight[-1] = 0
+    check(ns, case)
+    check(ns, case, grad=False)
+
+
+def test_no_row_taken(ns):
+    for L, V in ((5, 1000), (300, 70000), (2100, 600)):
+        case = Case(L, V, "bf16")
+        case.weight[:] = 0
+        check(ns, case)
+        check(ns, case, grad=False)

@@ -173,13 +173,16 @@ __device__ __forceinline__ void values_of(uint32_t codes, uint32_t byte, float (
 
 // A lane takes eight elements, of float32 four in each half of the chunk, so that
 // a store of all lanes is one run of the row.  Nobody reads the outputs soon:
-// stores past the caches (128256 x 4096 bf16 294 -> 217 us, 6.1 TB/s).
+// stores past the caches (128256 x 4096 bf16 294 -> 217 us, 6.1 TB/s), but for float32
+// rows that share lines (60000 x 1001, quantised and read back, 132 us past them, 106
+// through them; 4095 bf16 elements 345 and 373).
 template <int OT, int UNITS>
 __global__ __launch_bounds__(kRowThreads) void k_mx4_gather(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                             int V, int d, uint32_t rcp, const int32_t* __restrict__ ids,
                                                             const int32_t* __restrict__ n_dev, int n_max,
                                                             void* __restrict__ out, int64_t ld) {
   constexpr bool F32 = OT == NS_FP32;
+  const bool lines = ((uint64_t)out | (uint64_t)ld * 4) % 128 == 0;
   const int per_row = chunks_of(d);
   int n = n_dev ? *n_dev : n_max;
   n = n < 0 ? 0 : (n > n_max ? n_max : n);
@@ -223,7 +226,9 @@ __global__ __launch_bounds__(kRowThreads) void k_mx4_gather(const uint8_t* __res
         const float* x = h == 0 ? v : w + 4;
         float* to = (float*)out + base + i;
         if (d - i >= 4) {
-          __builtin_nontemporal_store(u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}, (u32x4_any*)to);
+          const u32x4 y = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+          if (lines) __builtin_nontemporal_store(y, (u32x4_any*)to);
+          else *(u32x4_any*)to = y;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -684,6 +689,13 @@ constexpr int kTileThreads = 512;
 constexpr int tile_stages(int tb) { return tb == 1 ? 3 : 2; }   // in LDS
 constexpr int kEightRows = 9 * kChunkBytes;        // eight channel rows in LDS and 128 bytes between them and the next
 
+// Eight consecutive 16-bit outputs, aligned, that nobody reads soon.
+template <int OT>
+__device__ __forceinline__ void store_once(void* out, size_t i, const float (&v)[8]) {
+  __builtin_nontemporal_store(u32x4{narrow2<OT>(v[0], v[1]), narrow2<OT>(v[2], v[3]), narrow2<OT>(v[4], v[5]), narrow2<OT>(v[6], v[7])},
+                              (u32x4*)((uint16_t*)out + i));
+}
+
 template <int OT, int TB>
 __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int tiles_m, int tiles_n) {
   constexpr int TM = TB * 64;                      // token rows of a block
@@ -856,6 +868,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
     origin(tile, m0, n0);
     const int n = n0 + wr * 128 + ni;
     stored = m0 + TM <= p.M && n0 + kTileN <= p.N;
+    // Whole lines past the caches (4096 x 128256 x 4096 1022 -> 996 us); parts of
+    // lines would be written one by one (4096 x 30001 x 512 68 -> 143).
+    const bool lines = OT != NS_FP32 && stored && ((uint64_t)p.out | (uint64_t)p.sm * 2) % 128 == 0;
 #pragma unroll
     for (int u = 0; u < TB; ++u)
 #pragma unroll
@@ -865,7 +880,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mx4_tiled(Product p, int ti
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = acc[e][u][r];
         const size_t at = (size_t)m * (size_t)p.sm + n;
-        if (stored) store_eight<OT>(p.out, at, v, 8);
+        if (lines) store_once<OT>(p.out, at, v);
         else if (m < p.M && n < p.N) store_eight<OT>(p.out, at, v, p.N - n);
       }
 #pragma unroll

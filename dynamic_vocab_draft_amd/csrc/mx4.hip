@@ -176,13 +176,12 @@ __device__ __forceinline__ void values_of(uint32_t codes, uint32_t byte, float (
 // stores past the caches (128256 x 4096 bf16 294 -> 217 us, 6.1 TB/s), but for float32
 // rows that share lines (60000 x 1001, quantised and read back, 132 us past them, 106
 // through them; 4095 bf16 elements 345 and 373).
-template <int OT, int UNITS>
+template <int OT, int UNITS, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void k_mx4_gather(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                             int V, int d, uint32_t rcp, const int32_t* __restrict__ ids,
                                                             const int32_t* __restrict__ n_dev, int n_max,
                                                             void* __restrict__ out, int64_t ld) {
   constexpr bool F32 = OT == NS_FP32;
-  const bool lines = ((uint64_t)out | (uint64_t)ld * 4) % 128 == 0;
   const int per_row = chunks_of(d);
   int n = n_dev ? *n_dev : n_max;
   n = n < 0 ? 0 : (n > n_max ? n_max : n);
@@ -227,7 +226,7 @@ __global__ __launch_bounds__(kRowThreads) void k_mx4_gather(const uint8_t* __res
         float* to = (float*)out + base + i;
         if (d - i >= 4) {
           const u32x4 y = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
-          if (lines) __builtin_nontemporal_store(y, (u32x4_any*)to);
+          if (ONCE) __builtin_nontemporal_store(y, (u32x4_any*)to);
           else *(u32x4_any*)to = y;
         } else {
 #pragma unroll
@@ -255,8 +254,14 @@ void launch_gather(const uint8_t* q, const uint8_t* scale, int V, int d, const i
   const int total = n_max * chunks_of(d), groups = kRowThreads / 32;
   const uint32_t rcp = reciprocal_of((uint32_t)chunks_of(d));
   const auto blocks = [&](int units) { return dim3((unsigned)((total + groups * units - 1) / (groups * units))); };
-  if (total >= kManyChunks) hipLaunchKernelGGL((k_mx4_gather<OT, kManyUnits>), blocks(kManyUnits), dim3(kRowThreads), 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld);
-  else hipLaunchKernelGGL((k_mx4_gather<OT, 1>), blocks(1), dim3(kRowThreads), 0, stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld);
+  const auto go = [&](auto units, auto once) {
+    hipLaunchKernelGGL((k_mx4_gather<OT, decltype(units)::value, decltype(once)::value>), blocks(decltype(units)::value), dim3(kRowThreads), 0,
+                       stream, q, scale, V, d, rcp, ids, n_dev, n_max, out, ld);
+  };
+  const bool once = OT != NS_FP32 || ((uint64_t)(uintptr_t)out | (uint64_t)ld * 4) % 128 == 0;
+  if (total < kManyChunks) go(std::integral_constant<int, 1>(), std::true_type());
+  else if (once) go(std::integral_constant<int, kManyUnits>(), std::true_type());
+  else go(std::integral_constant<int, kManyUnits>(), std::integral_constant<bool, OT != NS_FP32>());
 }
 
 // ---------------------------------------------------------------------------

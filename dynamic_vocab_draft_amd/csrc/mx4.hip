@@ -297,7 +297,8 @@ __device__ __forceinline__ uint32_t two_scales(uint16_t v) {
 }
 
 // ---------------------------------------------------------------------------
-// The product for few channel rows: bound by latency.  A block of eight waves
+// The product for few channel rows: bound by latency (4 x 2048 x 256 3.0 us, one
+// trip to memory and the joining of the sums).  A block of eight waves
 // owns 16 channel rows and up to 64 token rows (blockIdx.z of them); each wave
 // takes an eighth of the row's chunks, asks for BATCH of them at once and
 // multiplies; the eight sums are joined in LDS.  Lane (i, g) reads 32 bytes of a
@@ -398,6 +399,8 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
 // The head over few rows with the quantisation of its hidden rows in the same
 // launch, for up to 16 of them: a lane's 64 elements of a chunk are two whole
 // blocks, so each wave quantises what it multiplies, without a word to another.
+// Bound by latency: the ids, then the rows they name (8 hidden rows of 4096, 1000
+// channel rows: 8.2 us).
 // ---------------------------------------------------------------------------
 // 32 consecutive elements, a block, in four eights: their codes, and the scale byte.
 template <int ET>
@@ -454,7 +457,8 @@ __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __r
 
 // ---------------------------------------------------------------------------
 // The product for up to 64 token rows: bound by the bytes of the channel rows,
-// each read once.
+// each read once (8 x 128256 x 4096 54 us, 5.2 TB/s; 60 x 151936 x 3584 67 us, 4.6
+// TB/s with the outputs; the head's 15500 rows of 4096 for 64 hidden rows 15 us).
 //
 // One block of eight waves a CU takes an even share of the channel units of ROWS
 // rows and runs through it in passes of eight units, one a wave (RT operands of 16
@@ -659,7 +663,15 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product
 }
 
 // ---------------------------------------------------------------------------
-// The product for many token rows: compute-bound, tiles in LDS.
+// The product for many token rows: compute-bound, tiles in LDS.  4096 x 128256 x
+// 4096 takes 1010 to 1050 us (4.1 to 4.25 PFLOP/s), 4096 x 16384 x 16384 450 (4.9).
+// The matrix instructions alone reach 7.0 to 7.4 with such data: the power limit
+// holds the clock near 1.85 GHz, and they are busy for 59 % of its cycles.  In
+// between, a stage's 68 KB come in by direct loads at some 57 bytes a cycle, and
+// what the waves read from LDS takes as long as the products.  Stages of half a
+// chunk in a deeper ring, loads in other places or in pairs, raised wave priority
+// and rows fetched into L2 ahead changed nothing or were slower; reading no scales
+// at all would save 3 %.
 //
 // A block of eight waves owns 256 channel rows and TB * 64 token rows of the
 // output; a wave owns 128 channel rows (eight operands of 16) and TB * 16
@@ -686,8 +698,9 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product
 // the first half) first; place c of row r holds the one that is c ^ (r / 8 % 8)
 // in that order in channel rows and c ^ (r % 8) in token rows, and eight channel
 // rows stand 128 bytes from the next eight, so that lanes i and i + 1 read from
-// different halves of the 64 banks; scales stand in the order in which the lanes read them, so that 16 lanes read
-// 16 consecutive ones: no bank is met twice.
+// different halves of the 64 banks: no bank is met twice.  Scales stand in the
+// order in which the lanes read them, 16 bytes a row for two stages; a bank is met
+// twice there (reads without that took the same time, 1030 and 1031 us).
 // ---------------------------------------------------------------------------
 constexpr int kTileN = 256;                        // channel rows of a block
 constexpr int kTileThreads = 512;

@@ -268,7 +268,9 @@ struct Top {
 // A block of T threads takes a row and holds it in registers (U vectors a thread;
 // what is longer is read again) between its statistics and its gradient, then
 // the row gridDim.x on, whose vectors are asked for as this one's fall free: the
-// memory works on both while either is computed.
+// memory works on both while either is computed.  Bound by memory: 4096 x 128256
+// bf16 422 us, 5.0 TB/s read and written; 129 x 50257 float32, a row a block, 19 us,
+// most of it the row's way in and out.
 template <int ET, int T, int U>
 __global__ __launch_bounds__(T) void k_policy_row(Args a) {
   constexpr int EPV = per_vec(ET), NW = T / NS_WAVE, HELD = T * U, ESZ = elem_bytes(ET);
@@ -393,6 +395,8 @@ __global__ __launch_bounds__(T) void k_policy_row(Args a) {
 }
 
 // Many rows without a gradient: a block streams a row, two batches a wave in flight.
+// Bound by memory (2048 x 151936 fp16, half left out, 59 to 64 us, 5 TB/s; 4096 x
+// 128256 bf16 165, 6.4).
 // Eight waves for long rows, so that blocks end early and rows that are left out
 // leave no CU behind (2048 x 151936 fp16, half of them left out, 71 us with four
 // waves, 64 with eight, 82 with 16), one for short ones (20000 x 2000 bf16 37 us
@@ -454,7 +458,8 @@ __global__ __launch_bounds__(T) void k_policy_stream(Args a) {
 }
 
 // Parts of rows: a wave streams part `part` of S of one row.  With S = 1 it ends
-// the row, else it leaves the part's statistics.
+// the row, else it leaves the part's statistics.  Bound by latency (8 x 128256
+// float32 4.4 us, and 4.7 for k_policy_end behind it).
 constexpr int kPartWaves = 4;
 
 template <int ET>

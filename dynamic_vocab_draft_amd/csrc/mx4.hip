@@ -93,6 +93,33 @@ __device__ __forceinline__ uint32_t top_bits(const Eight<ET>& x) {
   return __float_as_uint(ET == NS_BF16 ? ns::bf16_lo(b) : ns::fp16_lo(b));
 }
 
+// A chunk of a row by half a wave, lane l of it: its codes and scales.
+template <int ET>
+__device__ __forceinline__ void put_chunk(const Eight<ET>& v, int l, uint8_t* to, uint8_t* scale) {
+  if constexpr (ET == NS_FP32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t t = v.v[h][e] & 0x7FFFFFFFu;
+        top = t > top ? t : top;
+      }
+      const uint32_t byte = scale_byte(oct_max_u32(top));
+      const float f = scale_value(byte);
+      uint32_t r = 0;
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v.get(4 * h), v.get(4 * h + 1), f, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v.get(4 * h + 2), v.get(4 * h + 3), f, 1);
+      *(uint16_t*)(to + h * (kChunkBytes / 2) + l * 2) = byte == 255 ? (uint16_t)0 : (uint16_t)r;
+      if ((l & 7) == 0) scale[h * (kChunkScales / 2) + (l >> 3)] = (uint8_t)byte;
+    }
+  } else {
+    const uint32_t byte = scale_byte(quad_max_u32(top_bits<ET>(v)));
+    *(uint32_t*)(to + l * 4) = quant_eight<ET>(v, byte);
+    if ((l & 3) == 0) scale[l >> 2] = (uint8_t)byte;
+  }
+}
+
 template <int ET, int UNITS>
 __global__ __launch_bounds__(kRowThreads) void k_mx4_rows(const void* __restrict__ x, int64_t ld, int R, int d,
                                                           uint32_t rcp, uint8_t* __restrict__ q,
@@ -113,29 +140,7 @@ __global__ __launch_bounds__(kRowThreads) void k_mx4_rows(const void* __restrict
   for (int u = 0; u < UNITS; ++u) {
     const int c = c0 + u * (kRowThreads / 32);
     if (c >= total) continue;                      // whole half waves
-    uint8_t* to = q + (size_t)c * kChunkBytes;
-    if constexpr (ET == NS_FP32) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t t = v[u].v[h][e] & 0x7FFFFFFFu;
-          top = t > top ? t : top;
-        }
-        const uint32_t byte = scale_byte(oct_max_u32(top));
-        const float f = scale_value(byte);
-        uint32_t r = 0;
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[u].get(4 * h), v[u].get(4 * h + 1), f, 0);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[u].get(4 * h + 2), v[u].get(4 * h + 3), f, 1);
-        *(uint16_t*)(to + h * (kChunkBytes / 2) + l * 2) = byte == 255 ? (uint16_t)0 : (uint16_t)r;
-        if ((l & 7) == 0) scale[(size_t)c * kChunkScales + h * (kChunkScales / 2) + (l >> 3)] = (uint8_t)byte;
-      }
-    } else {
-      const uint32_t byte = scale_byte(quad_max_u32(top_bits<ET>(v[u])));
-      *(uint32_t*)(to + l * 4) = quant_eight<ET>(v[u], byte);
-      if ((l & 3) == 0) scale[(size_t)c * kChunkScales + (l >> 2)] = (uint8_t)byte;
-    }
+    put_chunk<ET>(v[u], l, q + (size_t)c * kChunkBytes, scale + (size_t)c * kChunkScales);
   }
 }
 
@@ -365,12 +370,14 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
     xsr[u] = p.xs + m * spitch + g * 2;
   }
   f32x4 acc[NMT] = {};
-  for (int k = c.k0; k < c.k1; k += BATCH) {
-    i32x4 a[BATCH][2], b[BATCH][NMT][2];
-    uint32_t sa[BATCH], sb[BATCH][NMT];
+  // `count` chunks at once; those behind the wave's last are its first again, unused
+  const auto step = [&](auto count, int k) {
+    constexpr int C = decltype(count)::value;
+    i32x4 a[C][2], b[C][NMT][2];
+    uint32_t sa[C], sb[C][NMT];
 #pragma unroll
-    for (int q = 0; q < BATCH; ++q) {
-      const int at = k + q < c.k1 ? k + q : c.k0;
+    for (int q = 0; q < C; ++q) {
+      const int at = q == 0 || k + q < c.k1 ? k + q : c.k0;
       a[q][0] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes);
       a[q][1] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes + 16);
       sa[q] = *(const uint16_t*)(c.ws + at * kChunkScales);
@@ -383,74 +390,85 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
     }
     NS_ISSUE_FENCE();
 #pragma unroll
-    for (int q = 0; q < BATCH; ++q)
-      if (k + q < c.k1) {                            // uniform over the wave
+    for (int q = 0; q < C; ++q)
+      if (q == 0 || k + q < c.k1) {                  // uniform over the wave
 #pragma unroll
         for (int u = 0; u < NMT; ++u) {
           acc[u] = product128<0>(b[q][u][0], a[q][0], acc[u], sb[q][u], sa[q]);
           acc[u] = product128<1>(b[q][u][1], a[q][1], acc[u], sb[q][u], sa[q]);
         }
       }
+  };
+  // two or one where no more are left: their loads are not asked for several times
+  for (int k = c.k0; k < c.k1; k += BATCH) {
+    if (c.k1 - k == 1) step(std::integral_constant<int, 1>(), k);
+    else if (BATCH > 2 && c.k1 - k == 2) step(std::integral_constant<int, 2>(), k);
+    else step(std::integral_constant<int, BATCH>(), k);
   }
   join_waves<OT>(p, sh, acc, w, lane, c, row0, M);
 }
 
 // ---------------------------------------------------------------------------
 // The head over few rows with the quantisation of its hidden rows in the same
-// launch, for up to 16 of them: a lane's 64 elements of a chunk are two whole
-// blocks, so each wave quantises what it multiplies, without a word to another.
-// Bound by latency: the ids, then the rows they name (8 hidden rows of 4096, 1000
-// channel rows: 8.2 us).
+// launch: each wave quantises the chunks that it multiplies, without a word to
+// another.  Half a wave takes a chunk of a row, so that loads are whole lines, and
+// the codes pass through LDS to the lanes that multiply them (lanes that read and
+// quantised what they multiply asked for 64 lines a load: 8 hidden rows of 4096,
+// 1000 channel rows, 8.2 us).
 // ---------------------------------------------------------------------------
-// 32 consecutive elements, a block, in four eights: their codes, and the scale byte.
-template <int ET>
-__device__ __forceinline__ uint32_t quant_block(const Eight<ET> (&v)[4], i32x4& codes) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t t = top_bits<ET>(v[e]);
-    top = t > top ? t : top;
-  }
-  const uint32_t byte = scale_byte(top);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) codes[e] = (int)quant_eight<ET>(v[e], byte);
-  return byte;
-}
+constexpr int kHeadRow = kChunkBytes + 16;           // of a row in LDS: 16 rows meet no bank twice
 
-template <int ET>
+template <int ET, int NMT>
 __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __restrict__ h, int d) {
-  constexpr int BATCH = ET == NS_FP32 ? 1 : 2;
-  __shared__ f32x4 sh[8][1][NS_WAVE];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  constexpr int ROWS = 8;                            // hidden rows at once, two a load
+  __shared__ f32x4 sh[8][NMT][NS_WAVE];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[8][NMT * 16 * kHeadRow];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[8][NMT * 16 * kChunkScales];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
   const size_t row0 = (size_t)blockIdx.y * p.M;
-  const char* hr = (const char*)h + (row0 + (i < p.M ? i : p.M - 1)) * (size_t)d * (ET == NS_FP32 ? 4 : 2);
-  const int tail = d & ~(ET == NS_FP32 ? 3 : 7);
-  const u32x4 rest = Eight<ET>::rest_of(hr, tail, d);
+  const int tail = d & ~(ET == NS_FP32 ? 3 : 7), chunks = p.pitch / kChunkBytes;
+  const int l = lane & 31, half = lane >> 5;
+  Eight<ET> v[ROWS / 2], next[ROWS / 2];
+  // rows m .. m + 7 of chunk k; rows past the last are the last one again
+  const auto load = [&](int k, int m, Eight<ET>(&to)[ROWS / 2]) {
+#pragma unroll
+    for (int t = 0; t < ROWS / 2; ++t) {
+      const int r = m + t * 2 + half;
+      const char* row = (const char*)h + (row0 + (r < p.M ? r : p.M - 1)) * (size_t)d * (ET == NS_FP32 ? 4 : 2);
+      u32x4 rest = {0, 0, 0, 0};
+      if (k + 1 == chunks) rest = Eight<ET>::rest_of(row, tail, d);
+      to[t].load(row, k * kChunk + l * (ET == NS_FP32 ? 4 : 8), kChunk / 2, tail, rest);
+    }
+  };
   const Channels c(p, w, i, g);
+  if (c.k0 < c.k1) load(c.k0, 0, v);
   if (c.j0 >= c.n) return;
-  f32x4 acc[1] = {};
-  for (int k = c.k0; k < c.k1; k += BATCH) {
-    i32x4 a[BATCH][2];
-    uint32_t sa[BATCH];
-    Eight<ET> v[BATCH][2][4];
+  f32x4 acc[NMT] = {};
+  for (int k = c.k0; k < c.k1; ++k) {
+    const i32x4 a0 = *(const i32x4*)(c.w + (size_t)k * kChunkBytes), a1 = *(const i32x4*)(c.w + (size_t)k * kChunkBytes + 16);
+    const uint32_t sa = *(const uint16_t*)(c.ws + k * kChunkScales);
+    for (int m = 0; m < p.M; m += ROWS) {
+      const bool same = m + ROWS < p.M;
+      load(same || k + 1 == c.k1 ? k : k + 1, same ? m + ROWS : 0, next);   // behind the last rows any
+      NS_ISSUE_FENCE();
 #pragma unroll
-    for (int q = 0; q < BATCH; ++q) {
-      const int at = k + q < c.k1 ? k + q : c.k0;
-      a[q][0] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes);
-      a[q][1] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes + 16);
-      sa[q] = *(const uint16_t*)(c.ws + at * kChunkScales);
+      for (int t = 0; t < ROWS / 2; ++t) {
+        const int r = m + t * 2 + half;
+        put_chunk<ET>(v[t], l, &codes[w][r * kHeadRow], &scales[w][r * kChunkScales]);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[q][e >> 2][e & 3].load(hr, at * kChunk + g * 64 + e * 8, 4, tail, rest);
+      for (int t = 0; t < ROWS / 2; ++t) v[t] = next[t];
+    }
+    NS_ISSUE_FENCE();                                // a wave's LDS accesses are in order
+#pragma unroll
+    for (int u = 0; u < NMT; ++u) {
+      const int r = u * 16 + i;
+      const i32x4 b0 = *(const i32x4*)&codes[w][r * kHeadRow + g * 32], b1 = *(const i32x4*)&codes[w][r * kHeadRow + g * 32 + 16];
+      const uint32_t sb = *(const uint16_t*)&scales[w][r * kChunkScales + g * 2];
+      acc[u] = product128<0>(b0, a0, acc[u], sb, sa);
+      acc[u] = product128<1>(b1, a1, acc[u], sb, sa);
     }
     NS_ISSUE_FENCE();
-#pragma unroll
-    for (int q = 0; q < BATCH; ++q)
-      if (k + q < c.k1) {                            // uniform over the wave
-        i32x4 b0, b1;
-        const uint32_t s0 = quant_block<ET>(v[q][0], b0), s1 = quant_block<ET>(v[q][1], b1);
-        acc[0] = product128<0>(b0, a[q][0], acc[0], s0, sa[q]);
-        acc[0] = product128<1>(b1, a[q][1], acc[0], s1 << 8, sa[q]);
-      }
   }
   join_waves<NS_FP32>(p, sh, acc, w, lane, c, row0, p.M);
 }
@@ -938,12 +956,13 @@ void launch_stream(const Product& p, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-// Up to 64 tokens: up to 4096 channels the kernel for few rows (d = 4096, M = 8:
-// 4096 channels 8.0 us against 8.7 streamed, 6000 11.0 against 8.8; M = 64: 4096 9.4
-// against 11.8, 8000 16.9 against 12.5), then the stream, of eight-row units up
-// to 16384 channels (M = 64, 16000 13.5 against 16.1 with taller units; 60 x 30000 x
-// 3584 20.7 against 18.7) and for up to 16 tokens (M = 8, 30000 15.0 against 17.0,
-// 128256 57.4 against 58.6).
+// Up to 64 tokens: the kernel for few rows, whose loads of 16 rows are many lines
+// each, up to 8192 channels for 16 tokens (d = 4096, M = 8: 8000 channels 7.2 us
+// against 9.0 streamed, 12000 9.8 against 9.1) and up to 4096 for more (M = 64: 4096
+// 9.6 against 11.8, 5000 16.7 against 12.2; M = 17: 8000 9.5 against 10.5), then the
+// stream, of eight-row units up to 16384 channels (M = 64, 16000 13.5 against 16.1
+// with taller units; 60 x 30000 x 3584 20.7 against 18.7) and for up to 16 tokens
+// (M = 8, 30000 15.0 against 17.0, 128256 57.4 against 58.6).
 // More than 64 tokens over few channels go to the kernel for few rows, 64 at a
 // time, up to a block a CU (100 x 2000 x 16384, 250 blocks, 29.8 us against 44.4 in
 // tiles of 64 tokens; 4096 x 64 x 4096, 256 blocks, 10.0 against 14.5; 4096 x 100 x
@@ -958,7 +977,7 @@ void launch_product(const Product& p, hipStream_t stream) {
   const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
                         (OT == NS_FP32 ? 4 : 2);
   const int64_t few = (int64_t)((p.N + 15) / 16) * ((p.M + 63) / 64);   // blocks of the kernel for few rows
-  if (few <= 256 || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
+  if (few <= (p.M <= 16 ? 512 : 256) || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
     launch_few_of<OT>(p, 1, stream);
   } else if (p.M <= 64) {
     if (p.M <= 16) {
@@ -995,20 +1014,32 @@ void launch_head_stream(const Product& p, int B, hipStream_t stream) {
 }
 
 // The head's logits, B sequences.  Whole calls (d = 4096), the kernel for few rows
-// against the stream: M = 8, 4000 rows 16.8 against 17.1 us, 8000 20.2 against 18.8;
-// M = 64, 4000 rows 16.8 against 20.2, 8000 26.6 against 23.0; 64 sequences of 100
-// rows, M = 8, 21.2 against 19.4.  Eight-row units against taller ones: M = 64,
-// 15500 rows 24.6 against 27.5, 100000 81.1 against 68.8; M = 8, 100000 59.5 against
-// 60.7.  The stream's 32-bit row addresses reach 4 GB.
+// against the stream: M = 8, 8000 rows 15.5 against 17.7 us, 16000 21.4 against 19.9;
+// M = 64, 4000 rows 15.9 against 20.2, 8000 26.3 against 21.8.  Eight-row units
+// against taller ones: M = 64, 15500 rows 24.6 against 27.5, 100000 81.1 against 68.8;
+// M = 8, 100000 59.5 against 60.7.  The stream's 32-bit row addresses reach 4 GB.
 bool few_rows(int B, int n_max, int V, int M, int d) {
-  return (int64_t)B * n_max <= 4096 || (M > 32 && d > kStreamIdsD) || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
+  return (int64_t)B * n_max <= (M <= 16 ? 8192 : 4096) || (M > 32 && d > kStreamIdsD) || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
 }
 
-// Whether the kernel for few rows also quantises (M = 8, 1000 rows 13.6 us against
-// 16.9, 4000 13.8 against 16.8; M = 16, 1000 14.1 against 16.5).  A block's waves
-// quantise the same rows as the next block's, which pays up to a block a CU and for
-// rows of up to 4096 elements (M = 16, 4 x 1000 rows of 8192: 28.0 against 16.0).
-bool fuses_rows(int B, int n_max, int M, int d) { return M <= 16 && (int64_t)B * n_max <= 4096 && d <= 4096; }
+// Whether the kernel for few rows also quantises, which each of its blocks does
+// again: by how often a wave does so (`work`: eight rows of a chunk each) and by the
+// blocks a CU.  One launch less: bf16, d = 4096, M = 8, 4000 rows 11.7 us, 8000 15.1
+// against 15.5 in two launches, 16000 22.9 against 19.9; M = 16, 4000 13.0 against
+// 14.5, 8000 18.3 against 16.7; M = 32, 1000 16.8 against 14.5; d = 1024, M = 8, 16000
+// 14.1 against 14.6.  float32 rows are twice the loads: M = 24, d = 2048, 1000 rows
+// 13.1 against 14.1; M = 32 14.7 against 14.2.
+bool fuses_rows(int B, int n_max, int M, int d, int dtype) {
+  const int work = (M + 7) / 8 * ((chunks_of(d) + 7) / 8), most = dtype == NS_FP32 ? 8192 : 16384;
+  return work <= (dtype == NS_FP32 ? 3 : 4) && (int64_t)B * n_max * work <= most;
+}
+
+template <int ET>
+void launch_fused(const Product& p, int B, const void* h, int d, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)B), block(512);
+  if (p.M <= 16) hipLaunchKernelGGL((k_mx4_head_few<ET, 1>), grid, block, 0, stream, p, h, d);
+  else hipLaunchKernelGGL((k_mx4_head_few<ET, 2>), grid, block, 0, stream, p, h, d);   // no more than 32
+}
 
 void launch_head(const Product& p, int B, int d, hipStream_t stream) {
   if (few_rows(B, p.N, p.V, p.M, d)) {
@@ -1132,11 +1163,10 @@ int nanospec_mx4_logits_topk(const uint8_t* wq, const uint8_t* wscale, const int
   float* z = (float*)(base + l.z);
   const Product p{hq, hs, wq, wscale, row_ids, n_dev, M, n_max, V, pitch_of(d), z, l.ld, 1};
   int rc;
-  if (fuses_rows(B, n_max, M, d)) {
-    const dim3 grid((unsigned)((n_max + 15) / 16), (unsigned)B), block(512);
-    if (dtype == NS_BF16) hipLaunchKernelGGL(k_mx4_head_few<NS_BF16>, grid, block, 0, stream, p, h, d);
-    else if (dtype == NS_FP16) hipLaunchKernelGGL(k_mx4_head_few<NS_FP16>, grid, block, 0, stream, p, h, d);
-    else hipLaunchKernelGGL(k_mx4_head_few<NS_FP32>, grid, block, 0, stream, p, h, d);
+  if (fuses_rows(B, n_max, M, d, dtype)) {
+    if (dtype == NS_BF16) launch_fused<NS_BF16>(p, B, h, d, stream);
+    else if (dtype == NS_FP16) launch_fused<NS_FP16>(p, B, h, d, stream);
+    else launch_fused<NS_FP32>(p, B, h, d, stream);
   } else {
     rc = mx4_rows(h, d, B * M, d, dtype, hq, hs, stream);
     if (rc != NS_OK) return rc;

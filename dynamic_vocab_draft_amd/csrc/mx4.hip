@@ -303,32 +303,35 @@ __device__ __forceinline__ u16x2 two_scales(const char* p) {
 
 // ---------------------------------------------------------------------------
 // The product for few channel rows: bound by latency (4 x 2048 x 256 3.0 us, one
-// trip to memory and the joining of the sums).  A block of eight waves
-// owns 16 channel rows and up to 64 token rows (blockIdx.z of them); each wave
-// takes an eighth of the row's chunks, asks for BATCH of them at once and
-// multiplies; the eight sums are joined in LDS.  Lane (i, g) reads 32 bytes of a
-// chunk, blocks 2 g and 2 g + 1.
+// trip to memory and the joining of the sums).  A block of eight waves owns 16
+// channel rows and up to 64 token rows (blockIdx.z of them); each wave takes an
+// eighth of the row's chunks, asks for BATCH of them at once and multiplies; the
+// eight sums are joined in LDS.  Loads are whole lines, eight lanes a row, and pass
+// through LDS to the lanes that multiply them, without a word to another wave (lanes
+// that loaded what they multiply touched 64 lines a load: 64 x 4096 x 16384 29.1 ->
+// 18.8 us, 8 x 8000 x 4096 7.2 -> 5.4; 64 x 200 x 256 3.2 -> 3.6).  Lane (i, g)
+// multiplies blocks 2 g and 2 g + 1 of row i's chunk.
 // ---------------------------------------------------------------------------
 // A block's 16 channel rows of one sequence, and a wave's share of their chunks.
 struct Channels {
   int j0, n, k0, k1;
-  const uint8_t* w;         // of the lane's row and blocks
-  const uint8_t* ws;
-  __device__ __forceinline__ Channels(const Product& p, int w, int i, int g) {
-    const size_t seq = blockIdx.y;
+  __device__ __forceinline__ Channels(const Product& p, int w) {
     j0 = (int)blockIdx.x * 16;
-    const int j = j0 + i < p.N ? j0 + i : p.N - 1;
-    n = p.n_dev ? p.n_dev[seq] : p.N;
-    int id = p.ids ? p.ids[seq * p.N + j] : j;
+    n = p.n_dev ? p.n_dev[blockIdx.y] : p.N;
     n = n < p.N ? n : p.N;
-    id = id < 0 || id >= p.V ? 0 : id;               // a hole reads row 0; nobody reads its output
     const int chunks = p.pitch / kChunkBytes, per = (chunks + 7) / 8;
     k0 = w * per;
     k1 = k0 + per < chunks ? k0 + per : chunks;
-    this->w = p.w + (size_t)id * p.pitch + g * 32;
-    ws = p.ws + (size_t)id * (p.pitch / 16) + g * 2;
+  }
+  // the block's channel row r; a hole reads row 0, and nobody reads its output
+  __device__ __forceinline__ int id(const Product& p, int r) const {
+    const int j = j0 + r < p.N ? j0 + r : p.N - 1;
+    const int id = p.ids ? p.ids[(size_t)blockIdx.y * p.N + j] : j;
+    return id < 0 || id >= p.V ? 0 : id;
   }
 };
+
+constexpr int kRowInLds = kChunkBytes + 16;          // a row's chunk in LDS: 16 rows meet no bank twice
 
 // The eight waves' sums of token operand u joined by wave u.  Lane (i, g) holds
 // tokens 4 g .. 4 g + 3 of channel i.
@@ -356,36 +359,42 @@ template <int OT, int NMT>
 __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
   constexpr int BATCH = NMT <= 2 ? 4 : 2;            // chunks of a row in flight
   __shared__ f32x4 sh[8][NMT][NS_WAVE];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  // a wave's chunk of 16 channel rows and of NMT times 16 token rows
+  __shared__ __attribute__((aligned(16))) uint8_t codes[8][NMT + 1][16 * kRowInLds];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[8][NMT + 1][16 * kChunkScales];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
   const int m0 = (int)blockIdx.z * NMT * 16, M = p.M - m0, spitch = p.pitch / 16;   // tokens in groups; from here on
   const size_t row0 = (size_t)blockIdx.y * p.M + m0;
-  const Channels c(p, w, i, g);
-  if (c.j0 >= c.n) return;
-  const uint8_t* xr[NMT];
-  const uint8_t* xsr[NMT];
+  const Channels c(p, w);
+  // Eight lanes a row, two loads for 16 rows; of the scales two lanes a row, in
+  // either half of the wave.
+  const int r8 = lane >> 3, r2 = lane >> 1 & 15;
+  const uint8_t *wr[2], *xr[NMT][2], *wsr, *xsr[NMT];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) wr[v] = p.w + (size_t)c.id(p, v * 8 + r8) * p.pitch + (lane & 7) * 16;
+  wsr = p.ws + (size_t)c.id(p, r2) * spitch + (lane & 1) * 4;
 #pragma unroll
   for (int u = 0; u < NMT; ++u) {
-    const size_t m = row0 + (u * 16 + i < M ? u * 16 + i : M - 1);
-    xr[u] = p.x + m * p.pitch + g * 32;
-    xsr[u] = p.xs + m * spitch + g * 2;
+    const auto row = [&](int r) { return row0 + (u * 16 + r < M ? u * 16 + r : M - 1); };
+#pragma unroll
+    for (int v = 0; v < 2; ++v) xr[u][v] = p.x + row(v * 8 + r8) * p.pitch + (lane & 7) * 16;
+    xsr[u] = p.xs + row(r2) * spitch + (lane & 1) * 4;
   }
+  if (c.j0 >= c.n) return;
   f32x4 acc[NMT] = {};
   // `count` chunks at once; those behind the wave's last are its first again, unused
   const auto step = [&](auto count, int k) {
     constexpr int C = decltype(count)::value;
-    i32x4 a[C][2], b[C][NMT][2];
-    uint32_t sa[C], sb[C][NMT];
+    u32x4 x[C][NMT + 1][2];
+    uint32_t s[C][NMT + 1];
 #pragma unroll
     for (int q = 0; q < C; ++q) {
       const int at = q == 0 || k + q < c.k1 ? k + q : c.k0;
-      a[q][0] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes);
-      a[q][1] = *(const i32x4*)(c.w + (size_t)at * kChunkBytes + 16);
-      sa[q] = *(const uint16_t*)(c.ws + at * kChunkScales);
 #pragma unroll
-      for (int u = 0; u < NMT; ++u) {
-        b[q][u][0] = *(const i32x4*)(xr[u] + (size_t)at * kChunkBytes);
-        b[q][u][1] = *(const i32x4*)(xr[u] + (size_t)at * kChunkBytes + 16);
-        sb[q][u] = *(const uint16_t*)(xsr[u] + at * kChunkScales);
+      for (int o = 0; o <= NMT; ++o) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) x[q][o][v] = *(const u32x4*)((o == 0 ? wr[v] : xr[o > 0 ? o - 1 : 0][v]) + (size_t)at * kChunkBytes);
+        s[q][o] = *(const uint32_t*)((o == 0 ? wsr : xsr[o > 0 ? o - 1 : 0]) + at * kChunkScales);
       }
     }
     NS_ISSUE_FENCE();
@@ -393,10 +402,23 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
     for (int q = 0; q < C; ++q)
       if (q == 0 || k + q < c.k1) {                  // uniform over the wave
 #pragma unroll
-        for (int u = 0; u < NMT; ++u) {
-          acc[u] = product128<0>(b[q][u][0], a[q][0], acc[u], sb[q][u], sa[q]);
-          acc[u] = product128<1>(b[q][u][1], a[q][1], acc[u], sb[q][u], sa[q]);
+        for (int o = 0; o <= NMT; ++o) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) *(u32x4*)&codes[w][o][(v * 8 + r8) * kRowInLds + (lane & 7) * 16] = x[q][o][v];
+          *(uint32_t*)&scales[w][o][r2 * kChunkScales + (lane & 1) * 4] = s[q][o];
         }
+        NS_ISSUE_FENCE();                            // a wave's LDS accesses are in order
+        const auto block = [&](int o, int b) { return *(const i32x4*)&codes[w][o][i * kRowInLds + g * 32 + b * 16]; };
+        const auto two = [&](int o) { return (uint32_t)*(const uint16_t*)&scales[w][o][i * kChunkScales + g * 2]; };
+        const i32x4 a0 = block(0, 0), a1 = block(0, 1);
+        const uint32_t sa = two(0);
+#pragma unroll
+        for (int u = 0; u < NMT; ++u) {
+          const uint32_t sb = two(u + 1);
+          acc[u] = product128<0>(block(u + 1, 0), a0, acc[u], sb, sa);
+          acc[u] = product128<1>(block(u + 1, 1), a1, acc[u], sb, sa);
+        }
+        NS_ISSUE_FENCE();
       }
   };
   // two or one where no more are left: their loads are not asked for several times
@@ -416,13 +438,11 @@ __global__ __launch_bounds__(512) void k_mx4_few(Product p) {
 // quantised what they multiply asked for 64 lines a load: 8 hidden rows of 4096,
 // 1000 channel rows, 8.2 -> 6.5 us).  Bound by latency: the ids, then their rows.
 // ---------------------------------------------------------------------------
-constexpr int kHeadRow = kChunkBytes + 16;           // of a row in LDS: 16 rows meet no bank twice
-
 template <int ET, int NMT>
 __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __restrict__ h, int d) {
   constexpr int ROWS = 8;                            // hidden rows at once, two a load
   __shared__ f32x4 sh[8][NMT][NS_WAVE];
-  __shared__ __attribute__((aligned(16))) uint8_t codes[8][NMT * 16 * kHeadRow];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[8][NMT * 16 * kRowInLds];
   __shared__ __attribute__((aligned(16))) uint8_t scales[8][NMT * 16 * kChunkScales];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
   const size_t row0 = (size_t)blockIdx.y * p.M;
@@ -440,13 +460,15 @@ __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __r
       to[t].load(row, k * kChunk + l * (ET == NS_FP32 ? 4 : 8), kChunk / 2, tail, rest);
     }
   };
-  const Channels c(p, w, i, g);
+  const Channels c(p, w);
+  const int id = c.id(p, i);
+  const uint8_t *wr = p.w + (size_t)id * p.pitch + g * 32, *wsr = p.ws + (size_t)id * (p.pitch / 16) + g * 2;
   if (c.k0 < c.k1) load(c.k0, 0, v);
   if (c.j0 >= c.n) return;
   f32x4 acc[NMT] = {};
   for (int k = c.k0; k < c.k1; ++k) {
-    const i32x4 a0 = *(const i32x4*)(c.w + (size_t)k * kChunkBytes), a1 = *(const i32x4*)(c.w + (size_t)k * kChunkBytes + 16);
-    const uint32_t sa = *(const uint16_t*)(c.ws + k * kChunkScales);
+    const i32x4 a0 = *(const i32x4*)(wr + (size_t)k * kChunkBytes), a1 = *(const i32x4*)(wr + (size_t)k * kChunkBytes + 16);
+    const uint32_t sa = *(const uint16_t*)(wsr + k * kChunkScales);
     for (int m = 0; m < p.M; m += ROWS) {
       const bool same = m + ROWS < p.M;
       load(same || k + 1 == c.k1 ? k : k + 1, same ? m + ROWS : 0, next);   // behind the last rows any
@@ -454,7 +476,7 @@ __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __r
 #pragma unroll
       for (int t = 0; t < ROWS / 2; ++t) {
         const int r = m + t * 2 + half;
-        put_chunk<ET>(v[t], l, &codes[w][r * kHeadRow], &scales[w][r * kChunkScales]);
+        put_chunk<ET>(v[t], l, &codes[w][r * kRowInLds], &scales[w][r * kChunkScales]);
       }
 #pragma unroll
       for (int t = 0; t < ROWS / 2; ++t) v[t] = next[t];
@@ -463,7 +485,7 @@ __global__ __launch_bounds__(512) void k_mx4_head_few(Product p, const void* __r
 #pragma unroll
     for (int u = 0; u < NMT; ++u) {
       const int r = u * 16 + i;
-      const i32x4 b0 = *(const i32x4*)&codes[w][r * kHeadRow + g * 32], b1 = *(const i32x4*)&codes[w][r * kHeadRow + g * 32 + 16];
+      const i32x4 b0 = *(const i32x4*)&codes[w][r * kRowInLds + g * 32], b1 = *(const i32x4*)&codes[w][r * kRowInLds + g * 32 + 16];
       const uint32_t sb = *(const uint16_t*)&scales[w][r * kChunkScales + g * 2];
       acc[u] = product128<0>(b0, a0, acc[u], sb, sa);
       acc[u] = product128<1>(b1, a1, acc[u], sb, sa);
@@ -956,17 +978,14 @@ void launch_stream(const Product& p, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-// Up to 64 tokens: the kernel for few rows, whose loads of 16 rows are many lines
-// each, up to 8192 channels for 16 tokens (d = 4096, M = 8: 8000 channels 7.2 us
-// against 9.0 streamed, 12000 9.8 against 9.1) and up to 4096 for more (M = 64: 4096
-// 9.6 against 11.8, 5000 16.7 against 12.2; M = 17: 8000 9.5 against 10.5), then the
-// stream, of eight-row units up to 16384 channels (M = 64, 16000 13.5 against 16.1
-// with taller units; 60 x 30000 x 3584 20.7 against 18.7) and for up to 16 tokens
-// (M = 8, 30000 15.0 against 17.0, 128256 57.4 against 58.6).
-// More than 64 tokens over few channels go to the kernel for few rows, 64 at a
-// time, up to a block a CU (100 x 2000 x 16384, 250 blocks, 29.8 us against 44.4 in
-// tiles of 64 tokens; 4096 x 64 x 4096, 256 blocks, 10.0 against 14.5; 4096 x 100 x
-// 4096, 448 blocks, 17.8 against 14.9).
+// The kernel for few rows up to two blocks a CU, four for 16 tokens (d = 4096, M = 8:
+// 12000 channels 7.2 us against 9.2 streamed; M = 32: 8000 8.4 against 10.6, 12000
+// 11.8 against 10.8; M = 64: 8000 12.5 against 13.0, 12000 17.7 against 13.5), 64
+// tokens at a time where there are more (100 x 4000 x 4096 12.1 against 13.4 in tiles,
+// 1000 x 500 x 16384 35.5 against 42.2, 100 x 8000 x 4096 22.3 against 13.8).  Then, up
+// to 64 tokens, the stream, of eight-row units up to 16384 channels (M = 64, 16000 13.5
+// against 16.1 with taller units; 60 x 30000 x 3584 20.7 against 18.7) and for up to 16
+// tokens (M = 8, 30000 15.0 against 17.0, 128256 57.4 against 58.6).
 // The rest takes tiles of 256, 128 or 64 tokens.  Blocks take one tile each a
 // round, and a round takes about 28, 21 and 17 us at d = 4096 (256 x 16384, one
 // round each: 27.2, 20.9, 18.3); the sum over the rounds decides (1000 x 8000 x
@@ -977,7 +996,7 @@ void launch_product(const Product& p, hipStream_t stream) {
   const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
                         (OT == NS_FP32 ? 4 : 2);
   const int64_t few = (int64_t)((p.N + 15) / 16) * ((p.M + 63) / 64);   // blocks of the kernel for few rows
-  if (few <= (p.M <= 16 ? 512 : 256) || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
+  if (few <= (p.M <= 16 ? 1024 : 512) || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
     launch_few_of<OT>(p, 1, stream);
   } else if (p.M <= 64) {
     if (p.M <= 16) {
@@ -1014,21 +1033,21 @@ void launch_head_stream(const Product& p, int B, hipStream_t stream) {
 }
 
 // The head's logits, B sequences.  Whole calls (d = 4096), the kernel for few rows
-// against the stream: M = 8, 8000 rows 15.5 against 17.7 us, 16000 21.4 against 19.9;
-// M = 64, 4000 rows 15.9 against 20.2, 8000 26.3 against 21.8.  Eight-row units
+// against the stream: M = 8, 16000 rows 18.0 against 19.6 us; M = 32, 8000 17.1 against
+// 19.7, 16000 24.1 against 21.7; M = 64, 8000 21.3 against 21.8.  Eight-row units
 // against taller ones: M = 64, 15500 rows 24.6 against 27.5, 100000 81.1 against 68.8;
 // M = 8, 100000 59.5 against 60.7.  The stream's 32-bit row addresses reach 4 GB.
 bool few_rows(int B, int n_max, int V, int M, int d) {
-  return (int64_t)B * n_max <= (M <= 16 ? 8192 : 4096) || (M > 32 && d > kStreamIdsD) || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
+  return (int64_t)B * n_max <= (M <= 16 ? 16384 : 8192) || (M > 32 && d > kStreamIdsD) || (uint64_t)V * (uint64_t)pitch_of(d) > 0xFFFFFFFFull;
 }
 
 // Whether the kernel for few rows also quantises, which each of its blocks does
 // again: by how often a wave does so (`work`: eight rows of a chunk each) and by the
-// blocks a CU.  One launch less: bf16, d = 4096, M = 8, 4000 rows 11.7 us, 8000 15.1
-// against 15.5 in two launches, 16000 22.9 against 19.9; M = 16, 4000 13.0 against
-// 14.5, 8000 18.3 against 16.7; M = 32, 1000 16.8 against 14.5; d = 1024, M = 8, 16000
-// 14.1 against 14.6.  float32 rows are twice the loads: M = 24, d = 2048, 1000 rows
-// 13.1 against 14.1; M = 32 14.7 against 14.2.
+// blocks a CU.  One launch less: bf16, d = 4096, M = 8, 4000 rows 11.7 us, 8000 14.7
+// and 14.8 in two launches, 16000 22.9 and 18.0; M = 16, 4000 13.0 and 14.5, 8000 18.3
+// and 14.6; M = 32, 1000 16.8 and 14.5; d = 1024, M = 8, 16000 14.1 and 14.6.  float32
+// rows are twice the loads: M = 24, d = 2048, 1000 rows 13.1 and 14.1; M = 32 14.7 and
+// 14.2.
 bool fuses_rows(int B, int n_max, int M, int d, int dtype) {
   const int work = (M + 7) / 8 * ((chunks_of(d) + 7) / 8), most = dtype == NS_FP32 ? 8192 : 16384;
   return work <= (dtype == NS_FP32 ? 3 : 4) && (int64_t)B * n_max * work <= most;

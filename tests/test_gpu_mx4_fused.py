@@ -1,6 +1,6 @@
 """The 4-bit head that quantises its hidden rows in the product's launch, beside
-the sizes where it is taken, and the product over few rows with every number of
-chunks that may be left to a wave."""
+the sizes where it is taken, the product over few rows with every number of
+chunks that may be left to a wave, and streams of eight-row units beside it."""
 import pytest
 import torch
 
@@ -42,3 +42,35 @@ def test_products_of_few_rows(ns, d):
     for M, N in ((3, 100), (20, 70), (40, 50), (64, 33)):
         check_product(ns, M, N, d, "fp32", exact=False)
     check_product(ns, 9, 8192 if d == 1792 else 40, d, "bf16", exact=False)
+
+
+@pytest.mark.parametrize("M", [17, 32, 40, 48, 50, 64])
+def test_streams_of_eight_row_units(ns, M):
+    for n, d, dtype in ((8193, 300, "fp32"), (9001, 256, "bf16"), (16384, 1300, "fp16")):
+        check_product(ns, M, n, d, dtype)
+    check_head(ns, 1, M, 5, 9000, 10000, 300, "bf16")
+    check_head(ns, 3, M, 5, 4500, 5500, 128, "fp16", live=[4500, 7, 0], holes=9)
+
+
+@pytest.mark.parametrize("c", [(5, 16400, 4100), (40, 8200, 8300), (64, 8193, 9000)], ids=lambda c: "x".join(str(v) for v in c))
+def test_streams_of_long_rows(ns, c):
+    check_product(ns, *c, "fp32")
+
+
+@pytest.mark.parametrize("c", [(8, 16400, 2100), (30, 8200, 4500), (40, 8200, 3000)], ids=lambda c: "x".join(str(v) for v in c))
+def test_head_streams_of_long_rows(ns, c):
+    M, n, d = c
+    check_head(ns, 1, M, 5, n, n + 1000, d, "bf16")
+
+
+@pytest.mark.parametrize("c", [(8, 16384, 300), (16, 9000, 700), (64, 8192, 520), (100, 4000, 700), (1000, 300, 520), (520, 1024, 40)],
+                         ids=lambda c: "x".join(str(v) for v in c))
+def test_products_of_few_rows_over_many_blocks(ns, c):
+    check_product(ns, *c, "bf16")
+
+
+@pytest.mark.parametrize("c", [(1, 8, 16000, 4100), (1, 64, 8000, 520), (3, 40, 2500, 4100), (1, 40, 300, 16384)],
+                         ids=lambda c: "x".join(str(v) for v in c))
+def test_heads_over_few_rows(ns, c):
+    B, M, n, d = c
+    check_head(ns, B, M, 5, n, n + 100, d, "bf16")

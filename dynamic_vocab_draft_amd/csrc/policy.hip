@@ -62,21 +62,37 @@ __device__ __forceinline__ void put_nothing(const Args& a, size_t row) {
   a.row_loss[row] = 0.0;
 }
 
-// exp(x) - 1 - x.  Near 0 by its series, whose terms past the tenth are below a
-// step of the first.
-__device__ __forceinline__ float exp_past_line(float x) {
-  if (x > 80.f) return expf(x);                            // what is left out is far below its last digit
-  if (fabsf(x) > 0.5f) return expf(x) - 1.f - x;
+// e^x as 2^n and float32's exponential of the rest, n as far as a double's exponent goes.  From e^400 on it stays: a
+// product with it is past float32's range then, whatever its other factors, and still finite.
+__device__ __forceinline__ double exp_of(double x) {
+  x = x > 400.0 ? 400.0 : (x < -400.0 ? -400.0 : x);       // NaN stays
+  const double y = x * 1.4426950408889634, n = rint(y);
+  return ldexp((double)exp2_fast((float)(y - n)), (int)n);
+}
+
+// e^x - 1 and e^x - 1 - x, each by itself: neither is left of the other's digits where |x| is large.  Near 0 the second
+// by its series, whose terms past the tenth are below a step of the first.
+struct Past {
+  double one, line;
+};
+
+__device__ __forceinline__ Past exp_past(double x) {
+  if (fabs(x) > 0.5) {
+    const double e = exp_of(x) - 1.0;
+    return {e, x > 400.0 ? e : e - x};
+  }
+  const float f = (float)x;
   float r = 1.f / 3628800;
-  r = fmaf(r, x, 1.f / 362880);
-  r = fmaf(r, x, 1.f / 40320);
-  r = fmaf(r, x, 1.f / 5040);
-  r = fmaf(r, x, 1.f / 720);
-  r = fmaf(r, x, 1.f / 120);
-  r = fmaf(r, x, 1.f / 24);
-  r = fmaf(r, x, 1.f / 6);
-  r = fmaf(r, x, 0.5f);
-  return r * x * x;
+  r = fmaf(r, f, 1.f / 362880);
+  r = fmaf(r, f, 1.f / 40320);
+  r = fmaf(r, f, 1.f / 5040);
+  r = fmaf(r, f, 1.f / 720);
+  r = fmaf(r, f, 1.f / 120);
+  r = fmaf(r, f, 1.f / 24);
+  r = fmaf(r, f, 1.f / 6);
+  r = fmaf(r, f, 0.5f);
+  const double line = (double)(r * f * f);
+  return {x + line, line};
 }
 
 // What a row needs beside its logits, asked for before they are read.
@@ -121,11 +137,11 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
       float g = clipped ? 0.f : -gain;
       loss = clipped ? -most : -gain;
       if (a.ref) {
-        const float delta = (float)((double)v.ref - lp);
-        kl = exp_past_line(delta);
+        const Past past = exp_past((double)v.ref - lp);
+        kl = (float)past.line;
         if (a.beta != 0.f) {
           loss += (double)a.beta * kl;
-          g -= a.beta * (kl + delta);
+          g -= a.beta * (float)past.one;
         }
       }
       loss = (double)v.w * (loss - (double)a.c_ent * H);

@@ -779,7 +779,8 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
  * float32 has none) cannot have been drawn and teaches nothing: kl, loss and
  * gradient 0.  A row of logits -INFINITY alone has logprob -INFINITY and entropy
  * 0.  A row with a NaN or +INFINITY has no distribution: all of its outputs, the
- * loss and its gradient are NaN.
+ * loss and its gradient are NaN.  A token that the reference rules out (ref
+ * -INFINITY) has kl INFINITY, whose slope, 1 - exp(delta), is 1.
  * Statistics are float32; logprob and its distances from old and ref are taken in
  * float64 and rounded once, the loss is summed in float64.  Values past float32's
  * range become infinite, probabilities below 2^-126 zero in the gradient.  No

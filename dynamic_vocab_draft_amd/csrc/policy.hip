@@ -10,8 +10,9 @@
 //     g = w (-r A [r A <= clip(r) A] + beta (1 - exp(delta))),
 //     dz_j = g_loss t (g ([j = a] - p_j) + w c_H p_j (logp_j + H)).
 // With y_j = log2(e) z'_j - E, S = sum 2^y_j and W = sum 2^y_j y_j the second
-// line is 2^y_j (A + B y_j) off the token.  logp_a and its distances from old and
-// ref are taken in float64, so that a ratio is as exact as S.
+// line is 2^y_j (A + B y_j) off the token.  logp_a, its distances from old and
+// ref and what follows from them are taken in float64, so that a ratio is as exact
+// as S and products past float32's range are infinite, not NaN.
 #include "common.hpp"
 #include "logits.hpp"
 
@@ -43,10 +44,15 @@ struct Args {
 constexpr double kUnseen = -104.0;       // a log-probability below this is that of a probability 0 in float32
 constexpr double kLn2d = 0.69314718055994530942;
 
-// What a row's gradient needs: 2^y (A + B y), and G more at the token.
+// What a row's gradient needs: 2^y (A + B y), and the token's element by itself, where terms past float32's range may
+// cancel.
 struct Slope {
-  float ref, E, A, B, G;
+  float ref, E, A, B, token;
 };
+
+// Slopes past 2^100 are taken 2^k smaller and 2^y 2^k larger, so that a slope past float32's range makes infinities of
+// the elements that are past it, and zeros of masked logits.
+constexpr int kLargeSlope = 100;
 
 // Whether a row is looked at at all.
 __device__ __forceinline__ bool taken(const Args& a, size_t row, int& tok, float& w) {
@@ -112,7 +118,7 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
   float logp = nan, kl = 0.f, H = nan;
   double loss = 0.0;
   if (bad) {
-    r.A = r.B = r.G = kl = nan;
+    r.A = r.B = r.token = kl = nan;
     loss = nan;
   } else if (none) {
     logp = -INFINITY;
@@ -121,34 +127,44 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
     // log2 of S by its mantissa's, in [1/sqrt 2, sqrt 2], which is near 0 where S is
     // near a power of two.  c (1 + eps) is what c stands for; the sum's large terms
     // have c z close to E.
+    float c = a.c, eps = a.eps, eps_low = a.eps_low, eps_high = a.eps_high;
+    asm volatile("" : "+s"(c), "+s"(eps), "+s"(eps_low), "+s"(eps_high));   // widened here, not for all of a block's rows in registers
     int e;
     float m = frexpf(s.S, &e);
     if (m < 0.70710678f) m *= 2.f, --e;
-    const double l0 = (double)e + (double)log2f(m), l = l0 + (double)a.eps * s.E;
-    const double y = ((double)ztok - s.ref) * ((double)a.c * (1.0 + (double)a.eps)) - s.E;
+    const double l0 = (double)e + (double)log2f(m), l = l0 + (double)eps * s.E;
+    const double y = ((double)ztok - s.ref) * ((double)c * (1.0 + (double)eps)) - s.E;
     const double lp = kLn2d * (y - l);
     logp = (float)lp;
     H = fmaxf((float)(kLn2d * (l0 - (double)(s.W / s.S))), 0.f);
     if (lp > kUnseen) {
-      const float ratio = expf((float)(lp - (double)v.old));
-      const float lo = 1.f - a.eps_low, hi = 1.f + a.eps_high;
-      const float held = ratio < lo ? lo : (ratio > hi ? hi : ratio), gain = ratio * v.advantage, most = held * v.advantage;
+      // float64: a ratio of e^88 is past float32, and no advantage times that is still 0
+      const double ratio = exp_of(lp - (double)v.old), adv = (double)v.advantage;
+      const double lo = 1.0 - (double)eps_low, hi = 1.0 + (double)eps_high;
+      const double held = ratio < lo ? lo : (ratio > hi ? hi : ratio), gain = ratio * adv, most = held * adv;
       const bool clipped = gain > most;                    // not where one of them is NaN
-      float g = clipped ? 0.f : -gain;
+      double g = clipped ? 0.0 : -gain;
       loss = clipped ? -most : -gain;
       if (a.ref) {
         const Past past = exp_past((double)v.ref - lp);
         kl = (float)past.line;
         if (a.beta != 0.f) {
-          loss += (double)a.beta * kl;
-          g -= a.beta * (float)past.one;
+          loss += (double)a.beta * past.line;
+          g -= (double)a.beta * past.one;
         }
       }
       loss = (double)v.w * (loss - (double)a.c_ent * H);
-      const float up = v.g_loss * a.t, over = up * v.w / s.S;
-      r.G = up * v.w * g;
-      r.A = over * (a.c_ent * (H - (float)(kLn2d * l)) - g);
-      r.B = over * a.c_ent * (float)kLn2d;
+      const double up = (double)v.g_loss * a.t * v.w, over = up * (double)(1.f / s.S);
+      const double rest = fmax(-exp_past(lp).one, 0.0);    // 1 - p of the token
+      r.token = (float)(up * (g * rest + (double)a.c_ent * (1.0 - rest) * (lp + H)));
+      const double A = over * ((double)a.c_ent * (H - kLn2d * l) - g), B = over * a.c_ent * kLn2d;
+      int k = 0;
+      (void)frexp(A, &k);                                  // 0 of infinities and NaN
+      k = k > kLargeSlope ? k - kLargeSlope : 0;
+      const double b = ldexp(B, -k);
+      r.E -= (float)k;
+      r.A = (float)(ldexp(A, -k) - b * k);
+      r.B = (float)b;
     }
   }
   if (writes) {
@@ -161,9 +177,9 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
   return r;
 }
 
-// The gradient of one element.
+// The gradient of one element.  E is k where ref is not 0.
 __device__ __forceinline__ float slope_at(const Slope& s, float c, float z) {
-  const float y = s.ref == 0.f ? fmaf(z, c, -s.E) : (z - s.ref) * c;
+  const float y = s.ref == 0.f ? fmaf(z, c, -s.E) : (z - s.ref) * c - s.E;
   return exp2_fast(y) * fmaf(s.B, fmaxf(y, -200.f), s.A);
 }
 
@@ -405,7 +421,7 @@ __global__ __launch_bounds__(T) void k_policy_row(Args a) {
     if (tail < a.V) put_elem<ET>(a.dz, to + tail, slope_at(s, a.c, ztail));
     // the thread that wrote the token's element writes it once more
     const int owner = this_tok < nvec * EPV ? this_tok / EPV % T : this_tok - nvec * EPV;
-    if (tid == owner) put_elem<ET>(a.dz, to + this_tok, slope_at(s, a.c, ztok) + s.G);
+    if (tid == owner) put_elem<ET>(a.dz, to + this_tok, s.token);
     if (!more) return;
   }
 }
@@ -638,11 +654,11 @@ __global__ __launch_bounds__(kSlopeThreads) void k_policy_slope(Args a, float* l
     const u32x4 y = in ? slope_of<ET>(s, a.c, usual, x[u]) : u32x4{0, 0, 0, 0};
     __builtin_nontemporal_store(y, (u32x4_any*)(drow + (size_t)at * 16));
     // the token's element once more
-    if (in && at == tok / EPV) put_elem<ET>(drow, tok, slope_at(s, a.c, a.ztok[row]) + s.G);
+    if (in && at == tok / EPV) put_elem<ET>(drow, tok, s.token);
   }
   if (chunk == 0 && tail < a.V) {
     const float z = one_elem<ET>(zrow, tail);
-    put_elem<ET>(drow, tail, in ? slope_at(s, a.c, z) + (tail == tok ? s.G : 0.f) : 0.f);
+    put_elem<ET>(drow, tail, !in ? 0.f : (tail == tok ? s.token : slope_at(s, a.c, z)));
   }
 }
 

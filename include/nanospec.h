@@ -781,10 +781,11 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
  * 0.  A row with a NaN or +INFINITY has no distribution: all of its outputs, the
  * loss and its gradient are NaN.  A token that the reference rules out (ref
  * -INFINITY) has kl INFINITY, whose slope, 1 - exp(delta), is 1.
- * Statistics are float32; logprob and its distances from old and ref are taken in
- * float64 and rounded once, the loss is summed in float64.  Values past float32's
- * range become infinite, probabilities below 2^-126 zero in the gradient.  No
- * atomics, so results repeat bit for bit.
+ * Statistics are float32; logprob, its distances from old and ref, the ratio and the
+ * slopes are taken in float64 and rounded once, the loss is summed in float64.  Values
+ * past float32's range become infinite (an advantage of 0 times any ratio is 0),
+ * probabilities below 2^-126 zero in the gradient.  No atomics, so results repeat bit
+ * for bit.
  * L = 0 gives loss 0.  L <= NS_MAX_ROWS, inv_temp as above.
  * Errors: NS_EINVAL, NS_EDTYPE, NS_ECAPACITY (ws too small), NS_EHIP. */
 size_t nanospec_policy_loss_workspace_bytes(int32_t L, int32_t V);

@@ -1,12 +1,14 @@
-"""Policy loss at the edges of its terms: reference log-probabilities far from the
-policy's.  Definitions and tolerances are those of tests/test_gpu_policy.py."""
+"""Policy loss at the edges of its terms: log-probabilities far apart and past
+float32's range, certain rows, unlikely tokens, outputs over inputs.
+Definitions and tolerances are those of tests/test_gpu_policy.py."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_policy import DT, Case, check
+from tests.gpu_common import say
+from tests.test_gpu_policy import DT, U, Case, check, near, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +43,65 @@ def test_reference_near_and_above(ns, shape):
     logp = c.logp()
     c.ref = (logp + np.resize([-20, -3, -0.6, -0.5, -0.4, -1e-3, 1e-3, 0.5, 0.6, 3, 20], shape[0])).astype(np.float32)
     check(ns, c)
+
+
+def past_range(case, want):
+    """The values that the output's type cannot hold, as infinities."""
+    w = torch.from_numpy(want).float().to(DT[case.dtype]).double().numpy()
+    return np.where(np.isinf(w), w, want)
+
+
+def check_huge(ns, case, what):
+    """As `check`, with values past the outputs' range."""
+    say("policy_loss", case.L, case.V, case.dtype, what)
+    with np.errstate(all="ignore"):
+        want = case.want()
+    z, dz, out = case.device_rows()[1], case.device_rows()[1], case.outputs()
+    ns.nanospec_policy_loss(z, float(case.t), *case.arguments(), out["loss"], out["logprob"], out["kl"], out["entropy"],
+                            torch.tensor([case.g_loss], device="cuda"), dz, workspace(ns, case.L, case.V))
+    torch.cuda.synchronize()
+    for name in ("loss", "logprob", "kl", "entropy"):
+        if out[name] is not None:
+            v, tol = want[name]
+            with np.errstate(all="ignore"):
+                v = torch.from_numpy(v).float().double().numpy()
+            near(out[name], v, np.where(np.isfinite(tol), tol, 0) + U * np.abs(np.where(np.isfinite(v), v, 0)), name)
+    v, tol = want["dlogits"]
+    # where a row's slopes are past 2^100 the kernel takes them 2^k smaller and 2^y 2^k larger, k <= 150 here: the
+    # exponent k + y then rounds by 2^-24 of up to 150 more
+    near(dz, past_range(case, v), tol + 1.1 * 150 * U * np.abs(np.where(np.isfinite(v), v, 0)), "dlogits")
+
+
+@shapes
+@pytest.mark.parametrize("dtype", DT)
+def test_ratios_past_float32(ns, shape, dtype):
+    for what, ahead, advantage in (("no advantage", 100.0, 0.0), ("no advantage, far", 500.0, 0.0), ("clipped", 100.0, 1.5),
+                                   ("not clipped", 100.0, -1.5), ("not clipped, far", 150.0, -0.5)):
+        c = Case(*shape, dtype, lo=0.2, hi=0.28, ent=0.01)
+        c.z[:, 2::3] = -math.inf                  # masked logits have no gradient whatever the slope
+        c.z[np.arange(c.L), c.tokens] = 8.0
+        logp = c.logp()
+        c.ref = (logp + 0.1).astype(np.float32)
+        c.old = np.where(np.arange(c.L) % 2, logp - ahead, logp - 0.05).astype(np.float32)
+        c.advantage[1::2] = advantage
+        check_huge(ns, c, what)
+
+
+@shapes
+def test_unbounded_clip_and_no_advantage(ns, shape):
+    """Without an upper clip the ratio itself is past float32's range on both sides of the comparison."""
+    c = Case(*shape, hi=math.inf, ent=0.0)
+    c.old = np.where(np.arange(c.L) % 2, c.logp() - 200.0, c.old).astype(np.float32)
+    c.advantage[1::2] = 0
+    check_huge(ns, c, "no clip")
+
+
+@shapes
+def test_reference_far_above(ns, shape):
+    """exp(delta) past float32's range."""
+    c = Case(*shape, beta=0.3, ent=0.0)
+    c.z[:, 2::3] = -math.inf
+    c.z[np.arange(c.L), c.tokens] = 8.0
+    c.ref = (c.logp() + np.where(np.arange(c.L) % 2, 100.0, 0.2)).astype(np.float32)
+    c.old = (c.logp() - 0.1).astype(np.float32)
+    check_huge(ns, c, "reference")

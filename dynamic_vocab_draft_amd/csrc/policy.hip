@@ -157,7 +157,8 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
       const double up = (double)v.g_loss * a.t * v.w, over = up * (double)(1.f / s.S);
       const double rest = fmax(-exp_past(lp).one, 0.0);    // 1 - p of the token
       r.token = (float)(up * (g * rest + (double)a.c_ent * (1.0 - rest) * (lp + H)));
-      const double A = over * ((double)a.c_ent * (H - kLn2d * l) - g), B = over * a.c_ent * kLn2d;
+      // every y of the row and H have c as it was rounded, and so has l0
+      const double A = over * ((double)a.c_ent * (H - kLn2d * l0) - g), B = over * a.c_ent * kLn2d;
       int k = 0;
       (void)frexp(A, &k);                                  // 0 of infinities and NaN
       k = k > kLargeSlope ? k - kLargeSlope : 0;

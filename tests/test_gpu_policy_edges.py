@@ -105,3 +105,53 @@ def test_reference_far_above(ns, shape):
     c.ref = (c.logp() + np.where(np.arange(c.L) % 2, 100.0, 0.2)).astype(np.float32)
     c.old = (c.logp() - 0.1).astype(np.float32)
     check_huge(ns, c, "reference")
+
+
+def badly_rounded_temperature(most):
+    """An inverse temperature up to `most` whose product with log2(e) float32 rounds by more than 0.9 half steps."""
+    for i in range(10000):
+        t = np.float32(most - i * most * 1e-6)
+        c = float(t) * 1.4426950408889634
+        off = abs(c - float(np.float32(c))) / (2.0 ** math.floor(math.log2(c)) * U)
+        if off > 0.9 and c / 2.0 ** math.floor(math.log2(c)) < 1.1:
+            return float(t)
+
+
+@pytest.mark.parametrize("L", [7, 120])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_entropy_slope_of_a_certain_row(ns, L, sign):
+    """A row whose largest logit is all of it has entropy 0 and an entropy slope of 0 there, however far the logits lie
+    from zero.  In units of U = 2^-24: the exponential, and the logarithm of its sum, are off by 4 relative to p = 1, the
+    quotient W / S by 2, and the slope A + B y is a sum of terms under 0.4, rounded at each of four steps: 8 in all; twice that is allowed."""
+    t = badly_rounded_temperature(1.5)
+    V = 700
+    c = Case(L, V, t=t, beta=0.0, ent=1.0)
+    top = sign * 460.0                            # |c z| of some 1000
+    c.z[:] = top - 60.0
+    best = (c.tokens + 1) % V
+    c.z[np.arange(L), best] = top
+    c.z[np.arange(L), c.tokens] = top - 40.0
+    c.advantage[:] = 0
+    c.weight[:] = 1
+    c.g_loss = np.float32(1)
+    c.old = c.logp().astype(np.float32)
+    assert (c.logp() > -104).all()
+    z, dz, out = c.device_rows()[1], c.device_rows()[1], c.outputs()
+    ns.nanospec_policy_loss(z, float(c.t), *c.arguments(), out["loss"], out["logprob"], None, out["entropy"], None, dz, workspace(ns, L, V))
+    want = c.want()["dlogits"][0]
+    assert np.abs(want).max() < 1e-12
+    worst = float(dz.abs().max())
+    say("largest slope, in 2^-24", worst / U)
+    assert worst <= 16 * U * float(c.t)
+
+
+@shapes
+@pytest.mark.parametrize("shift", [-930.0, 500.0, 900.0])
+def test_entropy_of_shifted_logits(ns, shape, shift):
+    c = Case(*shape, beta=0.1, ent=0.5, t=badly_rounded_temperature(0.75))
+    z = torch.round(c.z.double() * 64) / 64
+    c.z = (z + shift).float()
+    assert torch.equal(c.z.double() - shift, z)
+    logp = c.logp()
+    c.old, c.ref = (logp - 0.1).astype(np.float32), (logp + 0.2).astype(np.float32)
+    check(ns, c)

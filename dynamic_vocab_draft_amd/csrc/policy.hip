@@ -41,7 +41,10 @@ struct Args {
   float* ztok;                 // [L] the tokens' logits, likewise
 };
 
-constexpr double kUnseen = -104.0;       // a log-probability below this is that of a probability 0 in float32
+// A log-probability below this is that of a probability 0 in float32 (under 2^-150, half the smallest number): no
+// sampler draws such a token.  One that an older policy drew, now that unlikely, would have a ratio of 0 and a KL term
+// past float32's range, which would be the whole batch's loss.  Above it a token counts as it is, however unlikely.
+constexpr double kUnseen = -104.0;
 constexpr double kLn2d = 0.69314718055994530942;
 
 // What a row's gradient needs: 2^y (A + B y), and the token's element by itself, where terms past float32's range may

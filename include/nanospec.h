@@ -775,12 +775,14 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
  *                 graphs among them).
  * A row of weight 0, or whose token lies outside [0, V) (padding), is not looked
  * at: logprob, kl, entropy, loss and gradient 0, whatever its logits.
- * A token of probability 0 (logit -INFINITY, or a logprob below -104, where
- * float32 has none) cannot have been drawn and teaches nothing: kl, loss and
- * gradient 0.  A row of logits -INFINITY alone has logprob -INFINITY and entropy
- * 0.  A row with a NaN or +INFINITY has no distribution: all of its outputs, the
- * loss and its gradient are NaN.  A token that the reference rules out (ref
- * -INFINITY) has kl INFINITY, whose slope, 1 - exp(delta), is 1.
+ * A token of probability 0 (logit -INFINITY, or a finite logprob below -104, where
+ * float32 has no probability) cannot have been drawn and teaches nothing: kl, loss
+ * and gradient 0, the entropy bonus's among them.  This is narrower than the
+ * formulas, which a finite logprob of any size satisfies.
+ * A row of logits -INFINITY alone has logprob -INFINITY and entropy 0.  A row with a
+ * NaN or +INFINITY has no distribution: all of its outputs, the loss and its gradient
+ * are NaN.  A token that the reference rules out (ref -INFINITY) has kl INFINITY, whose
+ * slope, 1 - exp(delta), is 1.
  * Statistics are float32; logprob, its distances from old and ref, the ratio and the
  * slopes are taken in float64 and rounded once, the loss is summed in float64.  Values
  * past float32's range become infinite (an advantage of 0 times any ratio is 0),

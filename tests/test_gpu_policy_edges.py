@@ -155,3 +155,20 @@ def test_entropy_of_shifted_logits(ns, shape, shift):
     logp = c.logp()
     c.old, c.ref = (logp - 0.1).astype(np.float32), (logp + 0.2).astype(np.float32)
     check(ns, c)
+
+
+@shapes
+def test_unlikely_tokens(ns, shape):
+    """Down to a log-probability of -104 a token teaches as any other, below that nothing."""
+    for below, learns in ((80.0, True), (95.0, True), (103.5, True), (104.5, False), (140.0, False)):
+        c = Case(*shape, beta=0.2, ent=0.01)
+        odd = np.arange(1, c.L, 2)
+        c.z[odd, c.tokens[odd]] = -200.0
+        others = torch.logsumexp(c.z[odd].double(), 1)
+        c.z[odd, c.tokens[odd]] = (others - below).float()
+        logp = c.logp()
+        assert ((logp[odd] > -104) == learns).all()
+        c.old, c.ref = (logp - 0.1).astype(np.float32), (logp + 0.3).astype(np.float32)
+        check(ns, c, what=str(below))
+        got = check(ns, c, grad=False, what=str(below))["kl"].cpu().numpy()[odd]
+        assert (got > 0.04).all() if learns else (got == 0).all()

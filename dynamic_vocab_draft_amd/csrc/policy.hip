@@ -38,7 +38,7 @@ struct Args {
   double* row_loss;            // [L]
   int S;                       // parts of a row, a power of two
   Stat* stat;                  // [L][S], where S > 1
-  float* ztok;                 // [L] the tokens' logits, likewise
+  struct Kept* kept;           // [L], likewise
 };
 
 // A log-probability below this is that of a probability 0 in float32 (under 2^-150, half the smallest number): no
@@ -107,9 +107,19 @@ __device__ __forceinline__ Past exp_past(double x) {
 // What a row needs beside its logits, asked for before they are read.
 struct Given {
   float old, ref, advantage, w, g_loss;
+  Given() = default;
   __device__ __forceinline__ Given(const Args& a, size_t row, float weight)
       : old(a.old[row]), ref(a.ref ? a.ref[row] : 0.f), advantage(a.advantage[row]), w(weight),
         g_loss(a.g_loss ? *a.g_loss : 1.f) {}
+};
+
+// The same of a row in parts, with its token (-1 of a row that is not taken) and that token's logit.  The blocks that end
+// the rows and those that take the gradient run at once: they read what a row was given here, so that outputs may
+// replace inputs.
+struct Kept {
+  Given given;
+  float ztok;
+  int tok;
 };
 
 // A row's outputs and slope from its statistics and its token's logit.
@@ -510,6 +520,7 @@ __global__ __launch_bounds__(kPartWaves* NS_WAVE) void k_policy_parts(Args a) {
   float w;
   if (!taken(a, row, tok, w)) {
     if (a.S == 1 && lane == 0) put_nothing(a, row);
+    if (a.S > 1 && part == 0 && lane == 0) a.kept[row].tok = -1;
     return;
   }
   const char* zrow = (const char*)a.z + row * (size_t)a.ld * elem_bytes(ET);
@@ -551,7 +562,7 @@ __global__ __launch_bounds__(kPartWaves* NS_WAVE) void k_policy_parts(Args a) {
     finish(a, row, st, one_elem<ET>(zrow, tok), Given(a, row, w), lane == 0);
   } else if (lane == 0) {
     a.stat[item] = st;
-    if (part == 0) a.ztok[row] = one_elem<ET>(zrow, tok);
+    if (part == 0) a.kept[row] = Kept{Given(a, row, w), one_elem<ET>(zrow, tok), tok};
   }
 }
 
@@ -591,15 +602,11 @@ __device__ __forceinline__ void end_rows(const Args& a, float* loss) {
   const int tid = threadIdx.x, lane = tid & (NS_WAVE - 1), part = tid & (a.S - 1);
   double total = 0.0;
   for (int row = tid / a.S; row < a.L; row += kTotalThreads / a.S) {
-    int tok;
-    float w;
-    const bool in = taken(a, row, tok, w);
-    const Given given(a, row, w);
-    const float ztok = a.ztok[row];                        // of a row that is not taken: anything
+    const Kept kept = a.kept[row];                         // of a row that is not taken: anything but the token
     const Stat st = join_parts(a, a.stat[(size_t)row * a.S + part], lane);
-    if (in) {
+    if (kept.tok >= 0) {
       double mine = 0.0;
-      finish(a, row, st, ztok, given, part == 0, &mine);
+      finish(a, row, st, kept.ztok, kept.given, part == 0, &mine);
       if (part == 0) total += mine;
     } else if (part == 0) {
       put_nothing(a, row);
@@ -613,7 +620,7 @@ __global__ __launch_bounds__(kTotalThreads) void k_policy_end(Args a, float* los
 // The same beside the gradient: the last block ends the rows, each of the others
 // takes a part of one row and joins that row's parts for itself.  dlogits may be
 // logits: a block reads its part before it writes it, and the token's logit is in
-// the workspace.
+// the workspace, as all else that a row was given.
 constexpr int kSlopeThreads = kTotalThreads;
 
 template <int ET>
@@ -631,12 +638,11 @@ __global__ __launch_bounds__(kSlopeThreads) void k_policy_slope(Args a, float* l
   char* drow = (char*)a.dz + row * (size_t)a.ld_d * elem_bytes(ET);
   const int nvec = a.V / EPV, tail = nvec * EPV + tid;
   const int q0 = chunk * kSlopeThreads * U + tid;
-  int tok;
-  float w;
-  const bool in = taken(a, row, tok, w);                   // uniform
+  const int tok = a.kept[row].tok;                         // uniform
+  const bool in = tok >= 0;
   if (in && tid < NS_WAVE) {
-    const Given given(a, row, w);
-    const Slope s = finish(a, row, join_parts(a, a.stat[row * a.S + (lane & (a.S - 1))], lane), a.ztok[row], given, false);
+    const Kept kept = a.kept[row];
+    const Slope s = finish(a, row, join_parts(a, a.stat[row * a.S + (lane & (a.S - 1))], lane), kept.ztok, kept.given, false);
     if (tid == 0) sh = s;
   }
   u32x4 x[U];
@@ -736,13 +742,16 @@ int launch_policy(Args a, float* loss, hipStream_t stream) {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Only as many rows as are taken in parts.
+size_t kept_bytes(int L) { return align256((size_t)(L < 1 ? 1 : (L < kWholeRows ? L : kWholeRows)) * sizeof(Kept)); }
+
 // Room for the parts of L rows or any fewer: a row has at most the parts of a
 // single one (of float32, which has the smallest batches), two where there is a
 // gradient, and rows in more come to less than 3/2 kWavesWanted of them together.
 size_t policy_ws(int L, int V) {
   const size_t l = (size_t)(L > 0 ? L : 1), one = (size_t)parts_of(1, V, NS_FP32);
   const size_t most = l * (one < 2 ? 2 : one), few = l * 2 > kWavesWanted * 3 / 2 ? l * 2 : kWavesWanted * 3 / 2;
-  return align256(l * 8) + align256((most < few ? most : few) * sizeof(Stat)) + align256(l * 4);
+  return align256(l * 8) + kept_bytes(L) + align256((most < few ? most : few) * sizeof(Stat));
 }
 
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
@@ -784,8 +793,8 @@ int nanospec_policy_loss(const void* logits, int64_t ld, int32_t L, int32_t V, i
          old_logprob, ref_logprob, advantage, weight, eps_low, eps_high, kl_coef, ent_coef, logprob, kl, entropy,
          g_loss, dlogits, ld_d, (double*)base, S, nullptr, nullptr};
   const size_t rows = align256((size_t)(L > 0 ? L : 1) * 8);
-  a.ztok = (float*)(base + rows);
-  a.stat = (Stat*)(base + rows + align256((size_t)(L > 0 ? L : 1) * 4));
+  a.kept = (Kept*)(base + rows);
+  a.stat = (Stat*)(base + rows + kept_bytes(L));
   if (L == 0) {
     hipLaunchKernelGGL(k_policy_total, dim3(1), dim3(kTotalThreads), 0, stream, (const double*)a.row_loss, 0, loss);
     return ns_launch_status();

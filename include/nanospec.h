@@ -769,6 +769,9 @@ int nanospec_token_logprobs_grad(const void* logits, int64_t ld, int32_t L, int3
  *                 alone; either the logits themselves (ld_d = ld), which it then
  *                 replaces, or memory apart from them.  What lies between rows is
  *                 untouched.
+ *   logprob, kl and entropy may each be the memory of old_logprob, ref_logprob,
+ *   advantage or weight, which they then replace row by row, loss that of g_loss;
+ *   otherwise outputs lie apart from inputs, and always from one another.
  *   ws          : >= nanospec_policy_loss_workspace_bytes(L, V) bytes, 256-byte
  *                 aligned, no initialisation needed.  The size never falls as L or
  *                 V grows.  Calls sharing a workspace must be ordered (two captured

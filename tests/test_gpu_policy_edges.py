@@ -172,3 +172,22 @@ def test_unlikely_tokens(ns, shape):
         check(ns, c, what=str(below))
         got = check(ns, c, grad=False, what=str(below))["kl"].cpu().numpy()[odd]
         assert (got > 0.04).all() if learns else (got == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 300), (5, 1000), (3, 40001), (95, 3000), (40, 128256), (120, 2000), (300, 70001)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("grad", [True, False])
+def test_outputs_over_a_row_s_inputs(ns, shape, grad):
+    """logprob, kl and entropy may replace the row's inputs, the loss what it is multiplied by."""
+    for turn in range(3):
+        c = Case(*shape, "bf16", seed=turn, ent=0.02)
+        c.weight[::4] = 0
+        want, z, g = c.outputs(), c.device_rows()[1], torch.tensor([c.g_loss], device="cuda")
+        dz = torch.empty_like(z) if grad else None
+        ns.nanospec_policy_loss(z, 1.0, *c.arguments(), want["loss"], want["logprob"], want["kl"], want["entropy"], g, dz, workspace(ns, *shape))
+        for over in ((1, 2, 3), (3, 4, 1)):       # old, ref and advantage; advantage, weight and old
+            args = c.arguments()
+            lp, kl, H = (args[i] for i in over)
+            loss, dz2 = g.clone(), torch.empty_like(z) if grad else None
+            ns.nanospec_policy_loss(z, 1.0, *args, loss, lp, kl, H, loss, dz2, workspace(ns, *shape))
+            assert torch.equal(loss, want["loss"]) and torch.equal(lp, want["logprob"]) and torch.equal(kl, want["kl"])
+            assert torch.equal(H, want["entropy"]) and (not grad or torch.equal(dz, dz2))

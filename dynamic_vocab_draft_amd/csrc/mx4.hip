@@ -41,8 +41,8 @@ constexpr int kRowThreads = 256;
 // whose blocks are more and end sooner.
 constexpr int kManyUnits = 8, kManyChunks = 1 << 17;
 
-// c / d for c < 2^26 and d <= 64, from 2^32 / d rounded up: the product is over
-// by less than c d / 2^32 < 1 / d.  0 stands for 2^32.
+// c / d for c < 2^26 and d <= 64, from 2^32 / d rounded up: the quotient is over
+// by less than c / 2^32 < 1 / d.  0 stands for 2^32.
 __host__ __device__ __forceinline__ uint32_t reciprocal_of(uint32_t d) { return d == 1 ? 0u : 0xFFFFFFFFu / d + 1u; }
 __device__ __forceinline__ uint32_t divided(uint32_t c, uint32_t rcp) { return rcp == 0 ? c : __umulhi(c, rcp); }
 
@@ -978,14 +978,25 @@ void launch_stream(const Product& p, hipStream_t stream) {
                      dim3(kStreamWaves * NS_WAVE), 0, stream, p);
 }
 
-// The kernel for few rows up to two blocks a CU, four for 16 tokens (d = 4096, M = 8:
-// 12000 channels 7.2 us against 9.2 streamed; M = 32: 8000 8.4 against 10.6, 12000
-// 11.8 against 10.8; M = 64: 8000 12.5 against 13.0, 12000 17.7 against 13.5), 64
-// tokens at a time where there are more (100 x 4000 x 4096 12.1 against 13.4 in tiles,
-// 1000 x 500 x 16384 35.5 against 42.2, 100 x 8000 x 4096 22.3 against 13.8).  Then, up
-// to 64 tokens, the stream, of eight-row units up to 16384 channels (M = 64, 16000 13.5
-// against 16.1 with taller units; 60 x 30000 x 3584 20.7 against 18.7) and for up to 16
-// tokens (M = 8, 30000 15.0 against 17.0, 128256 57.4 against 58.6).
+// The kernel for few rows is taken up to this many of its blocks of 16 channels and (up to) 64 tokens.  Against the
+// stream: up to 16 tokens four a CU (d = 4096, M = 8: 12000 channels 7.0 us against 9.1, 16000 8.7 against 10.4), three
+// where rows are short (d = 256: 12000 3.8 and 3.7, 16000 4.2 against 3.7); up to 48 tokens two (M = 32, 8000 channels:
+// d = 4096 8.0 against 10.1, d = 256 4.1 and 4.2); up to 64 two from d = 1024 to 4096 (8000 channels: d = 256 5.5
+// against 5.0, 1024 6.5 and 6.4, 4096 11.8 and 12.3, 8192 20.7 against 19.0).  Against tiles: one a CU (1000 x 256 x
+// 4096 7.0 against 13.0, x 256 3.6 against 4.7), and two where rows are long and of tokens not many, whose rows each
+// channel block asks for anew (400 x 1000 x 256 5.6 against 5.2, x 1024 6.6 and 6.5, x 2048 8.5 against 8.9, x 4096 12.1
+// against 13.5; 2000 x 250 x 4096 12.9 against 14.1, 3000 x 160 x 4096 13.9 and 13.6, 4096 x 100 x 4096 15.0 against
+// 13.6); not four (1000 x 1000 x 4096 23.5 against 13.6).
+int few_blocks(int M, int d) {
+  if (M <= 16) return d >= 1024 ? 1024 : 768;
+  if (M <= 48) return 512;
+  if (M <= 64) return d >= 1024 && d <= 4096 ? 512 : 256;
+  return d >= 2048 && M <= 2048 ? 512 : 256;
+}
+
+// Up to 64 tokens what the kernel for few rows leaves takes the stream, of eight-row units up to 16384 channels (M =
+// 64, 16000 13.5 against 16.1 with taller units; 60 x 30000 x 3584 20.7 against 18.7) and for up to 16 tokens (M = 8,
+// 30000 15.0 against 17.0, 128256 57.4 against 58.6).
 // The rest takes tiles of 256, 128 or 64 tokens.  Blocks take one tile each a
 // round, and a round takes about 28, 21 and 17 us at d = 4096 (256 x 16384, one
 // round each: 27.2, 20.9, 18.3); the sum over the rounds decides (1000 x 8000 x
@@ -996,7 +1007,7 @@ void launch_product(const Product& p, hipStream_t stream) {
   const uint64_t span = ((uint64_t)(p.M - 1) * (uint64_t)p.sm + (uint64_t)(p.N - 1) * (uint64_t)p.sn + 1) *
                         (OT == NS_FP32 ? 4 : 2);
   const int64_t few = (int64_t)((p.N + 15) / 16) * ((p.M + 63) / 64);   // blocks of the kernel for few rows
-  if (few <= (p.M <= 16 ? 1024 : 512) || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
+  if (few <= few_blocks(p.M, p.pitch * 2) || (p.M <= 64 && span >= 0x7FFFFFFFull)) {   // the stream's output offsets have 31 bits
     launch_few_of<OT>(p, 1, stream);
   } else if (p.M <= 64) {
     if (p.M <= 16) {

@@ -9,9 +9,10 @@
 // infinity, whose products are NaN.  The product
 //     out[m, n] = sum_b 2^(ex[m, b] + ew[n, b]) sum_{i in b} xq[m, i] wq[n, i]
 // is one scaled matrix instruction for every 128 elements.  Products of two
-// codes are quarters of integers, and a float32 sum stays exact while its terms'
-// scales lie within some 2^10 of one another (d = 4096), which those of usual
-// rows do; results then do not depend on how the sum was split.
+// codes are quarters of integers up to 144, so a float32 sum is exact, however it
+// was split, while 144 d 2^s <= 2^24, where the terms' scales lie within 2^s of one
+// another: s = 4 at d = 4096.  Rows of random signs, whose sums grow as sqrt(d), stay
+// exact further, to some 2^10.
 #include <type_traits>
 
 #include "common.hpp"

@@ -657,9 +657,10 @@ int nanospec_mx4_gather_rows(const uint8_t* q, const uint8_t* scale, int32_t V, 
 /* The product of M 4-bit token rows and N 4-bit channel rows:
  *     out[m, n] = sum_i x[m, i] w[n, i]
  * over the values that the codes stand for, summed in float32 and rounded once
- * to out_dtype.  Rows whose blocks differ little in scale (by 2^10 at d = 4096)
- * sum without rounding, so that the result does not depend on how the work was
- * split; in general the order of the sum is a function of M, N and d.
+ * to out_dtype.  Where the powers of two of x's and w's blocks together differ by no
+ * more than 2^s along the two rows, and 144 d 2^s <= 2^24 (s = 4 at d = 4096, 2 at
+ * 16384), every sum is exact and does not depend on how the work was split.
+ * Elsewhere the order of the sum is a function of M, N, d, out_dtype and ld_out.
  * out[m, n] is NaN where either row has a block of scale 255.
  *   xq, xs, wq, ws : rows as above.
  *   out            : [M] rows of N elements of out_dtype, ld_out >= N elements
@@ -676,6 +677,7 @@ int nanospec_mx4_matmul(const uint8_t* xq, const uint8_t* xs, int32_t M, const u
  * names, and the k largest logits of each are written with their ids.  Arguments
  * as of nanospec_quant_logits_topk, with
  *   wq, wscale : W_head's 4-bit rows [V x pitch] and scales [V x pitch / 16].
+ * Where sums round, their order is a function of B, V, n_max, n_dev, M, d and dtype.
  * NaN logits are never selected.
  * Errors: NS_EINVAL, NS_EDTYPE, NS_ECAPACITY (ws too small), NS_EHIP. */
 size_t nanospec_mx4_logits_workspace_bytes(int32_t B, int32_t n_max, int32_t M, int32_t k,

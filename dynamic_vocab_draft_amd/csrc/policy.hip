@@ -55,7 +55,7 @@ struct Slope {
 
 // Slopes past 2^100 are taken 2^k smaller and 2^y 2^k larger, so that a slope past float32's range makes infinities of
 // the elements that are past it, and zeros of masked logits.
-constexpr int kLargeSlope = 100;
+constexpr float kLargeSlope = 0x1p100f;
 
 // Whether a row is looked at at all.
 __device__ __forceinline__ bool taken(const Args& a, size_t row, int& tok, float& w) {
@@ -71,25 +71,26 @@ __device__ __forceinline__ void put_nothing(const Args& a, size_t row) {
   a.row_loss[row] = 0.0;
 }
 
-// e^x as 2^n and float32's exponential of the rest, n as far as a double's exponent goes.  From e^400 on it stays: a
-// product with it is past float32's range then, whatever its other factors, and still finite.
+// e^x of a finite x as 2^n and float32's exponential of the rest, n as far as a double's exponent goes.  From e^400 on
+// it stays: a product with it is past float32's range then, whatever its other factors, and still finite.
 __device__ __forceinline__ double exp_of(double x) {
-  x = x > 400.0 ? 400.0 : (x < -400.0 ? -400.0 : x);       // NaN stays
   const double y = x * 1.4426950408889634, n = rint(y);
-  return ldexp((double)exp2_fast((float)(y - n)), (int)n);
+  const int e = (int)n;
+  const float rest = (float)(y - n);                       // of a y past 2^52: what the product left, of no use
+  return ldexp((double)exp2_fast(fabsf(rest) > 1.f ? 0.f : rest), e < -577 ? -577 : (e > 577 ? 577 : e));
 }
 
+// A value whose distances from others are finite.
+__device__ __forceinline__ double no_infinity(float v) { return fabsf(v) == INFINITY ? copysign(1e300, (double)v) : (double)v; }
+
 // e^x - 1 and e^x - 1 - x, each by itself: neither is left of the other's digits where |x| is large.  Near 0 the second
-// by its series, whose terms past the tenth are below a step of the first.
+// by its series, whose terms past the tenth are below a step of the first.  Without a branch: a row waits for this.
 struct Past {
   double one, line;
 };
 
 __device__ __forceinline__ Past exp_past(double x) {
-  if (fabs(x) > 0.5) {
-    const double e = exp_of(x) - 1.0;
-    return {e, x > 400.0 ? e : e - x};
-  }
+  const double e = exp_of(x) - 1.0;
   const float f = (float)x;
   float r = 1.f / 3628800;
   r = fmaf(r, f, 1.f / 362880);
@@ -101,7 +102,8 @@ __device__ __forceinline__ Past exp_past(double x) {
   r = fmaf(r, f, 1.f / 6);
   r = fmaf(r, f, 0.5f);
   const double line = (double)(r * f * f);
-  return {x + line, line};
+  const bool near = fabsf(f) <= 0.5f;
+  return {near ? x + line : e, near ? line : (x > 400.0 ? e : e - x)};
 }
 
 // What a row needs beside its logits, asked for before they are read.
@@ -140,8 +142,9 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
     // log2 of S by its mantissa's, in [1/sqrt 2, sqrt 2], which is near 0 where S is
     // near a power of two.  c (1 + eps) is what c stands for; the sum's large terms
     // have c z close to E.
-    float c = a.c, eps = a.eps, eps_low = a.eps_low, eps_high = a.eps_high;
-    asm volatile("" : "+s"(c), "+s"(eps), "+s"(eps_low), "+s"(eps_high));   // widened here, not for all of a block's rows in registers
+    float c = a.c, eps = a.eps, eps_low = a.eps_low, eps_high = a.eps_high, beta = a.beta, c_ent = a.c_ent;
+    // widened here, not for all of a block's rows in registers
+    asm volatile("" : "+s"(c), "+s"(eps), "+s"(eps_low), "+s"(eps_high), "+s"(beta), "+s"(c_ent));
     int e;
     float m = frexpf(s.S, &e);
     if (m < 0.70710678f) m *= 2.f, --e;
@@ -152,33 +155,36 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
     H = fmaxf((float)(kLn2d * (l0 - (double)(s.W / s.S))), 0.f);
     if (lp > kUnseen) {
       // float64: a ratio of e^88 is past float32, and no advantage times that is still 0
-      const double ratio = exp_of(lp - (double)v.old), adv = (double)v.advantage;
+      const double ratio = exp_of(lp - no_infinity(v.old)), adv = (double)v.advantage;
       const double lo = 1.0 - (double)eps_low, hi = 1.0 + (double)eps_high;
       const double held = ratio < lo ? lo : (ratio > hi ? hi : ratio), gain = ratio * adv, most = held * adv;
       const bool clipped = gain > most;                    // not where one of them is NaN
       double g = clipped ? 0.0 : -gain;
       loss = clipped ? -most : -gain;
       if (a.ref) {
-        const Past past = exp_past((double)v.ref - lp);
+        const Past past = exp_past(no_infinity(v.ref) - lp);
         kl = (float)past.line;
-        if (a.beta != 0.f) {
-          loss += (double)a.beta * past.line;
-          g -= (double)a.beta * past.one;
+        if (beta != 0.f) {
+          loss += (double)beta * past.line;
+          g -= (double)beta * past.one;
         }
       }
-      loss = (double)v.w * (loss - (double)a.c_ent * H);
+      loss = (double)v.w * (loss - (double)c_ent * H);
       const double up = (double)v.g_loss * a.t * v.w, over = up * (double)(1.f / s.S);
-      const double rest = fmax(-exp_past(lp).one, 0.0);    // 1 - p of the token
-      r.token = (float)(up * (g * rest + (double)a.c_ent * (1.0 - rest) * (lp + H)));
+      const float p = exp2_fast((float)(y - l));           // the token's
+      r.token = (float)(up * (g * fmaxf(1.f - p, 0.f) + (double)(c_ent * p) * (lp + H)));
       // every y of the row and H have c as it was rounded, and so has l0
-      const double A = over * ((double)a.c_ent * (H - kLn2d * l0) - g), B = over * a.c_ent * kLn2d;
-      int k = 0;
-      (void)frexp(A, &k);                                  // 0 of infinities and NaN
-      k = k > kLargeSlope ? k - kLargeSlope : 0;
-      const double b = ldexp(B, -k);
-      r.E -= (float)k;
-      r.A = (float)(ldexp(A, -k) - b * k);
-      r.B = (float)b;
+      const double A = over * ((double)c_ent * (H - kLn2d * l0) - g), B = over * c_ent * kLn2d;
+      r.A = (float)A;
+      r.B = (float)B;
+      if (fabsf(r.A) > kLargeSlope) {
+        int k;
+        (void)frexp(A * (double)(1.f / kLargeSlope), &k);  // 0 of infinities
+        const double b = ldexp(B, -k);
+        r.E -= (float)k;
+        r.A = (float)(ldexp(A, -k) - b * k);
+        r.B = (float)b;
+      }
     }
   }
   if (writes) {

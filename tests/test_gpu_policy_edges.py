@@ -191,3 +191,23 @@ def test_outputs_over_a_row_s_inputs(ns, shape, grad):
             ns.nanospec_policy_loss(z, 1.0, *args, loss, lp, kl, H, loss, dz2, workspace(ns, *shape))
             assert torch.equal(loss, want["loss"]) and torch.equal(lp, want["logprob"]) and torch.equal(kl, want["kl"])
             assert torch.equal(H, want["entropy"]) and (not grad or torch.equal(dz, dz2))
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_infinite_old_log_probabilities(ns, grad):
+    """A token that the old policy ruled out has a ratio past any range: 0 with no advantage, clipped with one, infinite against one."""
+    for L in (8, 100):
+        c = Case(L, 700, ent=0.0)
+        z, got = c.device_rows()[1], []
+        for old, advantage in ((-math.inf, (0.0, 1.0)), (-3e38, (0.0, 1.0)), (-300.0, (0.0, 1.0)), (-math.inf, (-1.0, 0.0))):
+            c.old[:] = old
+            c.advantage[:] = np.resize(advantage, L)
+            out, dz = c.outputs(), torch.empty_like(z) if grad else None
+            ns.nanospec_policy_loss(z, 1.0, *c.arguments(), out["loss"], out["logprob"], out["kl"], out["entropy"], None, dz, workspace(ns, L, 700))
+            got.append((out["loss"], dz))
+        assert torch.isfinite(got[0][0]) and all(torch.equal(g[0], got[0][0]) for g in got[1:3])
+        assert got[3][0].item() == math.inf
+        if grad:
+            assert torch.isfinite(got[0][1]).all() and all(torch.equal(g[1], got[0][1]) for g in got[1:3])
+            d = got[3][1].cpu()
+            assert (d[np.arange(0, L, 2), c.tokens[::2]] == math.inf).all() and torch.isfinite(d[1::2]).all() and not d.isnan().any()

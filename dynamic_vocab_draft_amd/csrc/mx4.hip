@@ -32,8 +32,8 @@ __host__ __device__ constexpr int chunks_of(int d) { return (d + kChunk - 1) / k
 __host__ __device__ constexpr int pitch_of(int d) { return chunks_of(d) * kChunkBytes; }
 
 // ---------------------------------------------------------------------------
-// Quantisation: one pass, bound by its bytes (128256 x 4096 bf16 219 us, 6.0 TB/s
-// read and written).  A lane takes eight elements, four lanes a block, so a row's
+// Quantisation: one pass, bound by its bytes (128256 x 4096 bf16 228 to 245 us,
+// 5.4 to 5.8 TB/s read and written).  A lane takes eight elements, four lanes a block, so a row's
 // 256-element chunk is half a wave's.  Of float32 a lane takes four in each half
 // of the chunk, so that a load of all lanes is one run of the row.
 // ---------------------------------------------------------------------------
@@ -295,7 +295,7 @@ __device__ __forceinline__ f32x4 product128(i32x4 a, i32x4 b, f32x4 c, uint32_t 
 }
 
 // Two scales as an operand, whose upper half is nobody's.  A pair, not an integer,
-// so that no instruction clears that half (4096 x 16384 x 16384 479 -> 471 us).
+// so that no instruction clears that half (1.6 % of 4096 x 16384 x 16384).
 __device__ __forceinline__ u16x2 two_scales(const char* p) {
   u16x2 r;
   r.x = *(const uint16_t*)p;
@@ -705,7 +705,7 @@ __global__ __launch_bounds__(kStreamWaves* NS_WAVE, 2) void k_mx4_stream(Product
 
 // ---------------------------------------------------------------------------
 // The product for many token rows: compute-bound, tiles in LDS.  4096 x 128256 x
-// 4096 takes 1010 to 1050 us (4.1 to 4.25 PFLOP/s), 4096 x 16384 x 16384 450 (4.9).
+// 4096 takes 1000 to 1050 us (4.1 to 4.3 PFLOP/s), 4096 x 16384 x 16384 446 to 486 (4.5 to 4.9).
 // The matrix instructions alone reach 7.0 to 7.4 with such data: the power limit
 // holds the clock near 1.85 GHz, and they are busy for 59 % of its cycles.  In
 // between, a stage's 68 KB come in by direct loads at some 57 bytes a cycle, and

@@ -321,7 +321,7 @@ struct Top {
 // what is longer is read again) between its statistics and its gradient, then
 // the row gridDim.x on, whose vectors are asked for as this one's fall free: the
 // memory works on both while either is computed.  Bound by memory: 4096 x 128256
-// bf16 422 us, 5.0 TB/s read and written; 129 x 50257 float32, a row a block, 19 us,
+// bf16 425 us, 4.9 TB/s read and written; 129 x 50257 float32, a row a block, 19 us,
 // most of it the row's way in and out.
 template <int ET, int T, int U>
 __global__ __launch_bounds__(T) void k_policy_row(Args a) {
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(T) void k_policy_stream(Args a) {
 
 // Parts of rows: a wave streams part `part` of S of one row.  With S = 1 it ends
 // the row, else it leaves the part's statistics.  Bound by latency (8 x 128256
-// float32 4.4 us, and 4.7 for k_policy_end behind it).
+// float32 4.4 us, and 4.6 for k_policy_end behind it).
 constexpr int kPartWaves = 4;
 
 template <int ET>

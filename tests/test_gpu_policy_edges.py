@@ -211,3 +211,32 @@ def test_infinite_old_log_probabilities(ns, grad):
             assert torch.isfinite(got[0][1]).all() and all(torch.equal(g[1], got[0][1]) for g in got[1:3])
             d = got[3][1].cpu()
             assert (d[np.arange(0, L, 2), c.tokens[::2]] == math.inf).all() and torch.isfinite(d[1::2]).all() and not d.isnan().any()
+
+
+@shapes
+@pytest.mark.parametrize("shift", [-715.0, 700.0, 709.0])
+def test_logits_on_both_sides_of_the_exponents_limit(ns, shape, shift):
+    """|c z| on both sides of 1024, where parts of a row are kept in two ways and joined."""
+    c = Case(*shape, beta=0.1, ent=0.01)
+    z = torch.round(c.z.double() * 64) / 64
+    c.z = (z + shift).float()
+    assert torch.equal(c.z.double() - shift, z)
+    logp = c.logp()
+    c.old, c.ref = (logp - 0.1).astype(np.float32), (logp + 0.2).astype(np.float32)
+    check(ns, c)
+    check(ns, c, grad=False)
+
+
+@shapes
+def test_ratios_past_float32_of_far_logits(ns, shape):
+    """The two together: slopes past 2^100 in rows whose exponents are taken from their largest logit."""
+    c = Case(*shape, ent=0.01)
+    z = torch.round(c.z.double() * 64) / 64
+    z[:, 2::3] = -math.inf
+    z[np.arange(c.L), c.tokens] = 8.0
+    c.z = (z + 3e4).float()
+    logp = c.logp()
+    c.ref = (logp + 0.1).astype(np.float32)
+    c.old = np.where(np.arange(c.L) % 2, logp - 110.0, logp - 0.05).astype(np.float32)
+    c.advantage[1::2] = -1.5
+    check_huge(ns, c, "far")

@@ -75,9 +75,9 @@ __device__ __forceinline__ void put_nothing(const Args& a, size_t row) {
 // it stays: a product with it is past float32's range then, whatever its other factors, and still finite.
 __device__ __forceinline__ double exp_of(double x) {
   const double y = x * 1.4426950408889634, n = rint(y);
-  const int e = (int)n;
-  const float rest = (float)(y - n);                       // of a y past 2^52: what the product left, of no use
-  return ldexp((double)exp2_fast(fabsf(rest) > 1.f ? 0.f : rest), e < -577 ? -577 : (e > 577 ? 577 : e));
+  const int e = (int)fmin(fmax(n, -577.0), 577.0);
+  const float rest = (float)(y - n);                       // NaN if x is; of a y past 2^52 what the product left, of no use
+  return ldexp((double)exp2_fast(fabsf(rest) > 1.f ? 0.f : rest), e);
 }
 
 // A value whose distances from others are finite.
@@ -197,7 +197,7 @@ __device__ __forceinline__ Slope finish(const Args& a, size_t row, const Stat& s
   return r;
 }
 
-// The gradient of one element.  E is k where ref is not 0.
+// The gradient of one element.  Where ref is not 0, E is -k of a large slope, else 0.
 __device__ __forceinline__ float slope_at(const Slope& s, float c, float z) {
   const float y = s.ref == 0.f ? fmaf(z, c, -s.E) : (z - s.ref) * c - s.E;
   return exp2_fast(y) * fmaf(s.B, fmaxf(y, -200.f), s.A);
